@@ -23,12 +23,15 @@ UPIPE_ERR_UNSUPPORTED = 2
 UPIPE_ERR_WORKSPACE_TOO_SMALL = 3
 UPIPE_ERR_CUDA = 4
 UPIPE_ERR_TIMEOUT = 5
+UPIPE_ERR_PAGE = 6
 
 UPIPE_PASS_FWD, UPIPE_PASS_BWD, UPIPE_PASS_BOTH, UPIPE_PASS_FUSED = 0, 1, 2, 3
 UPIPE_HOST_KV, UPIPE_HOST_ACT = 1, 2
+UPIPE_ROPE_PLAIN, UPIPE_ROPE_LINEAR, UPIPE_ROPE_NTK, UPIPE_ROPE_BY_PARTS = 0, 1, 2, 3
 
 KERNEL_CLASSES = ["layout", "attn_fwd", "bwd_pre", "attn_bwd", "dq_convert", "other",
-                  "loss_gemm", "loss_merge", "kv_h2d", "dkdv_d2h", "kv_wait"]
+                  "loss_gemm", "loss_merge", "kv_h2d", "dkdv_d2h", "kv_wait", "rope",
+                  "kv_append", "attn_paged", "paged_merge"]
 
 # Every symbol include/upipe.h declares, with (restype, argtypes).
 _vp, _i, _i64, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
@@ -37,6 +40,23 @@ _vp, _i, _i64, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes
 class KernelStat(ctypes.Structure):
     _fields_ = [("total_ms", ctypes.c_double), ("launches", ctypes.c_uint64)]
 
+
+class Heads(ctypes.Structure):
+    """upipe_heads: a strided [B, S, heads, D] bf16 tensor."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_s", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class Pages(ctypes.Structure):
+    """upipe_pages: the k and v caches and their strides."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("stride_page", ctypes.c_int64), ("stride_slot", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+_ph, _pp, _d = ctypes.POINTER(Heads), ctypes.POINTER(Pages), ctypes.c_double
 
 SIGNATURES = {
     "upipe_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i, _i, _i64, _i, _i]),
@@ -68,6 +88,16 @@ SIGNATURES = {
     "upipe_mlp_fwd": (_i, [_vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz, _vp]),
     "upipe_mlp_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz,
                            _vp]),
+    "upipe_rope_frequencies": (_i, [ctypes.POINTER(_d), ctypes.POINTER(_d), _i, _d, _i, _d, _d,
+                                    _d, _d]),
+    "upipe_rope_phases": (_i, [ctypes.POINTER(_d), ctypes.POINTER(_u64), _i]),
+    "upipe_rope_fwd": (_i, [_ph, _ph, _ph, _ph, _vp, _i64, _vp, _d, _i, _i64, _i, _i, _i, _vp]),
+    "upipe_rope_bwd": (_i, [_ph, _ph, _ph, _ph, _vp, _i64, _vp, _d, _i, _i64, _i, _i, _i, _vp]),
+    "upipe_kv_append": (_i, [_ph, _ph, _ph, _ph, _pp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+                             _d, _i, _i64, _i, _i, _vp]),
+    "upipe_attn_paged_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i64, _i64, _i64]),
+    "upipe_attn_paged_fwd": (_i, [_ph, _ph, _vp, _pp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i,
+                                  _i64, _i64, _i64, _vp, _sz, _vp]),
 }
 
 
@@ -271,6 +301,65 @@ def upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspa
     _check(st, "upipe_mlp_bwd")
 
 
+def upipe_rope_frequencies(rot_dim, theta=10000.0, scaling=UPIPE_ROPE_PLAIN, factor=1.0,
+                           trained_len=0.0, turns_fast=32.0, turns_slow=1.0):
+    """Returns (list of rot_dim / 2 frequencies in radians a position, mscale)."""
+    f = (_d * max(1, rot_dim // 2))()
+    m = _d()
+    _check(_lib.upipe_rope_frequencies(f, ctypes.byref(m), rot_dim, theta, scaling, factor,
+                                       trained_len, turns_fast, turns_slow),
+           "upipe_rope_frequencies")
+    return list(f), m.value
+
+
+def upipe_rope_phases(inv_freq):
+    """Frequencies (radians a position) as a list of unsigned 64-bit fractions of a turn."""
+    n = len(inv_freq)
+    out = (_u64 * max(1, n))()
+    _check(_lib.upipe_rope_phases((_d * max(1, n))(*inv_freq), out, n), "upipe_rope_phases")
+    return list(out)[:n]
+
+
+def upipe_rope_fwd(q, k, q_out, k_out, pos, pos0, phase, mscale, B, S, D, rot_dim, interleaved,
+                   stream=None):
+    """q, k, q_out, k_out: Heads or None (absent)."""
+    _check(_lib.upipe_rope_fwd(q, k, q_out, k_out, _ptr(pos), pos0, _ptr(phase), mscale, B, S, D,
+                               rot_dim, int(interleaved), _stream(stream, phase)),
+           "upipe_rope_fwd")
+
+
+def upipe_rope_bwd(dq_out, dk_out, dq, dk, pos, pos0, phase, mscale, B, S, D, rot_dim,
+                   interleaved, stream=None):
+    _check(_lib.upipe_rope_bwd(dq_out, dk_out, dq, dk, _ptr(pos), pos0, _ptr(phase), mscale, B,
+                               S, D, rot_dim, int(interleaved), _stream(stream, phase)),
+           "upipe_rope_bwd")
+
+
+def upipe_kv_append(q, q_out, k, v, cache, page_table, table_stride, max_pages, seq_len, cu_rows,
+                    pos, pos0, phase, mscale, B, S, rot_dim, interleaved, stream=None):
+    """q, q_out, k, v: Heads or None; cache: Pages."""
+    _check(_lib.upipe_kv_append(q, q_out, k, v, cache, _ptr(page_table), table_stride, max_pages,
+                                _ptr(seq_len), _ptr(cu_rows), _ptr(pos), pos0, _ptr(phase),
+                                mscale, B, S, rot_dim, int(interleaved),
+                                _stream(stream, page_table)), "upipe_kv_append")
+
+
+def upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, prefix_len, max_q, max_len):
+    return int(_lib.upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, prefix_len, max_q,
+                                                     max_len))
+
+
+def upipe_attn_paged_fwd(q, o, lse, cache, page_table, table_stride, max_pages, seq_len, cu_rows,
+                         prefix_table, prefix_len, B, S, max_q, max_len, workspace,
+                         workspace_bytes=None, stream=None):
+    """q, o: Heads; cache: Pages."""
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(_lib.upipe_attn_paged_fwd(q, o, _ptr(lse), cache, _ptr(page_table), table_stride,
+                                     max_pages, _ptr(seq_len), _ptr(cu_rows), _ptr(prefix_table),
+                                     prefix_len, B, S, max_q, max_len, _ptr(workspace), wb,
+                                     _stream(stream, page_table)), "upipe_attn_paged_fwd")
+
+
 # ---- convenience: allocate outputs / workspace with torch, then call the ABI -------------
 
 def _dims(q, k):
@@ -468,3 +557,221 @@ def mlp_backward(x, w_gu, w_d, dy, seq_tile=8192, workspace=None, stream=None,
     upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspace, None,
                   stream)
     return dx, dw_gu, dw_d
+
+
+# ---- rotary positions, paged cache ----------------------------------------------------------
+
+def _heads(t, name):
+    """upipe_heads of a bf16 [..., heads, D] tensor: [B, S, heads, D], or packed [S, heads, D]."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+    st = t.stride()
+    if t.dim() not in (3, 4) or (st[-1] != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be [B, S, heads, D] or [S, heads, D] with contiguous D, "
+                         f"not {tuple(t.shape)} with strides {st}")
+    return Heads(t.data_ptr(), st[0] if t.dim() == 4 else 0, st[-3], st[-2], t.shape[-2])
+
+
+def _pages(k_pages, v_pages):
+    import torch
+    if k_pages.dtype != torch.bfloat16 or v_pages.dtype != torch.bfloat16:
+        raise TypeError("the caches must be bfloat16")
+    st = k_pages.stride()
+    if k_pages.dim() != 4 or st[3] != 1 or v_pages.shape != k_pages.shape or \
+            v_pages.stride() != st:
+        raise ValueError("k_pages and v_pages must be [n_pages, page_size, heads, D] of one shape "
+                         "and one set of strides, with contiguous D")
+    n, ps, h, D = k_pages.shape
+    return Pages(k_pages.data_ptr(), v_pages.data_ptr(), n, st[0], st[1], st[2], ps, h, D)
+
+
+def _ints(t, dtype, shape, name):
+    """Checks a dense integer tensor that the kernels index."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, not "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _on(stream, device):
+    """Context in which torch allocates for the stream that the call runs on, so that a buffer
+    freed after the call is not handed to other work before that stream is done with it."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def rope_phases(rot_dim, theta=10000.0, scaling=UPIPE_ROPE_PLAIN, factor=1.0, trained_len=0.0,
+                turns_fast=32.0, turns_slow=1.0, inv_freq=None, device="cuda"):
+    """phases (int64 [rot_dim / 2] on the device), mscale: what the rotary calls take. Made once
+    and kept. inv_freq: own frequencies (radians a position, rot_dim / 2 values) instead of
+    theta's."""
+    import torch
+    if inv_freq is None:
+        inv_freq, mscale = upipe_rope_frequencies(rot_dim, theta, scaling, factor, trained_len,
+                                                  turns_fast, turns_slow)
+    else:
+        inv_freq, mscale = [float(f) for f in inv_freq], 1.0
+        if len(inv_freq) != rot_dim // 2:
+            raise ValueError(f"inv_freq has {len(inv_freq)} values, not {rot_dim // 2}")
+    words = [w - (1 << 64) if w >> 63 else w for w in upipe_rope_phases(inv_freq)]
+    return torch.tensor(words, dtype=torch.int64, device=device), mscale
+
+
+def _phases(phases):
+    import torch
+    if phases.dtype != torch.int64 or phases.dim() != 1 or not phases.is_contiguous():
+        raise ValueError("phases must be a contiguous int64 vector (see rope_phases)")
+    return 2 * phases.numel()
+
+
+def _rope(call, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
+    import torch
+    ref = q if q is not None else k
+    if ref is None or ref.dim() != 4 or (k is not None and (
+            k.dim() != 4 or k.shape[:2] != ref.shape[:2] or k.shape[3] != ref.shape[3])):
+        raise ValueError("q and k must be [B, S, heads, D] of the same B, S and D (one may be None)")
+    B, S, _, D = ref.shape
+    _ints(positions, torch.int64, (B, S), "positions")
+    rot = _phases(phases)
+    views, outs = [], []
+    with _on(stream, ref.device):
+        for t, name in ((q, "q"), (k, "k")):
+            if t is None:
+                views += [None, None]
+                outs.append(None)
+                continue
+            y = t if inplace else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            views += [_heads(t, name), _heads(y, name + " out")]
+            outs.append(y)
+    call(views[0], views[2], views[1], views[3], positions, start, phases, mscale, B, S, D, rot,
+         interleaved, stream if stream is not None else _stream(None, ref))
+    return outs[0], outs[1]
+
+
+def rope_forward(q, k, phases, mscale=1.0, interleaved=False, positions=None, start=0,
+                 inplace=False, stream=None):
+    """q, k (bf16 [B, S, heads, D], any strides with contiguous D; one may be None) with their
+    first 2 * len(phases) features rotated by their positions: positions (int64 [B, S]) or
+    start + s. phases, mscale: rope_phases. inplace writes the inputs. Returns (q, k)."""
+    return _rope(upipe_rope_fwd, q, k, phases, mscale, interleaved, positions, start, inplace,
+                 stream)
+
+
+def rope_backward(dq, dk, phases, mscale=1.0, interleaved=False, positions=None, start=0,
+                  inplace=False, stream=None):
+    """The gradients with respect to rope_forward's inputs, from those of its outputs."""
+    return _rope(upipe_rope_bwd, dq, dk, phases, mscale, interleaved, positions, start, inplace,
+                 stream)
+
+
+def _rows(q, cu_seqlens, seq_len):
+    """B, S and leading shape of a padded [B, S, heads, D] or packed [S, heads, D] batch."""
+    import torch
+    B = seq_len.numel()
+    _ints(seq_len, torch.int32, (B,), "seq_len")
+    _ints(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
+    if cu_seqlens is None:
+        if q.dim() != 4 or q.shape[0] != B:
+            raise ValueError(f"a padded batch is [{B}, S, heads, D], not {tuple(q.shape)}")
+        return B, q.shape[1], q.shape[:2]
+    if q.dim() != 3:
+        raise ValueError(f"a packed batch is [rows, heads, D], not {tuple(q.shape)}")
+    return B, q.shape[0], q.shape[:1]
+
+
+def _table(page_table, B):
+    import torch
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be int32 [{B}, max_pages] with contiguous rows")
+    return page_table.stride(0), page_table.shape[1]
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, phases=None,
+              mscale=1.0, interleaved=False, positions=None, start=0, cu_seqlens=None,
+              stream=None):
+    """Writes the new tokens' k (rotated) and v into the paged cache; returns q rotated (None
+    without q).
+
+    k, v (and q): bf16 [B, S, heads, D], or packed [rows, heads, D] with cu_seqlens (int32
+    [B + 1]); k_pages, v_pages: bf16 [n_pages, page_size, heads, D] (any strides with contiguous
+    D); page_table: int32 [B, max_pages]; seq_len: int32 [B], each sequence's tokens in its own
+    pages with the new ones. Positions: positions (int64, one a row), or start + a token's index
+    in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place)."""
+    import torch
+    B, S, lead = _rows(k, cu_seqlens, seq_len)
+    D = k_pages.shape[-1]
+    for t, name in ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out")):
+        if t is not None and (t.shape[:-2] != lead or t.shape[-1] != D):
+            raise ValueError(f"{name} must be {tuple(lead)} + [heads, {D}], not {tuple(t.shape)}")
+    ts, mp = _table(page_table, B)
+    _ints(positions, torch.int64, tuple(lead), "positions")
+    if q is not None and q_out is None:
+        with _on(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if cu_seqlens is not None:
+                q_out.zero_()  # rows of no sequence are not written
+    qv = _heads(q, "q") if q is not None else None
+    qo = _heads(q_out, "q_out") if q is not None else None
+    upipe_kv_append(qv, qo, _heads(k, "k"), _heads(v, "v"), _pages(k_pages, v_pages), page_table,
+                    ts, mp, seq_len, cu_seqlens, positions, start, phases, mscale, B, S,
+                    _phases(phases) if phases is not None else 0, interleaved,
+                    stream if stream is not None else _stream(None, k))
+    return q_out if q is not None else None
+
+
+def paged_attention(q, k_pages, v_pages, page_table, seq_len, prefix_table=None, prefix_len=0,
+                    cu_seqlens=None, max_q=None, max_len=None, out=None, with_lse=False,
+                    lse=None, workspace=None, stream=None):
+    """o, lse of new tokens over a shared prefix and their sequences' own pages.
+
+    q: bf16 [B, S, Hq, D], or packed [rows, Hq, D] with cu_seqlens (int32 [B + 1]). k_pages,
+    v_pages, page_table, seq_len as for kv_append, called before for the same tokens. The first
+    prefix_len tokens of the pages prefix_table (int32) are seen by every row and read once for
+    all; then row i of a sequence with n new tokens sees its own keys 0 .. seq_len - n + i.
+    max_q, max_len: the largest numbers of new and own tokens, hints for tiles and splits only
+    (default: the most that the tensors allow). lse: float32 [B, Hq, S] (packed: [Hq, rows]),
+    returned when given or with_lse, else None."""
+    import torch
+    B, S, lead = _rows(q, cu_seqlens, seq_len)
+    cache = _pages(k_pages, v_pages)
+    Hq, D = q.shape[-2:]
+    if D != cache.D:
+        raise ValueError(f"q has D={D}, the cache {cache.D}")
+    ts, mp = _table(page_table, B)
+    if prefix_len:
+        if prefix_table is None:
+            raise ValueError("prefix_len without prefix_table")
+        _ints(prefix_table, torch.int32, (prefix_table.numel(),), "prefix_table")
+        if prefix_table.numel() * cache.page_size < prefix_len:
+            raise ValueError(f"prefix_table has {prefix_table.numel()} pages of "
+                             f"{cache.page_size} for {prefix_len} tokens")
+    if out is not None and out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
+    rows = S if cu_seqlens is not None else B * S
+    ls = (Hq, S) if cu_seqlens is not None else (B, Hq, S)
+    if lse is not None:
+        _ints(lse, torch.float32, ls, "lse")
+    mq = S if cu_seqlens is None or max_q is None else max_q
+    ml = max_len if max_len is not None else max(1, mp * cache.page_size)
+    with _on(stream, q.device):
+        make = torch.empty if cu_seqlens is None else torch.zeros  # rows of no sequence: not written
+        if out is None:
+            out = make(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and with_lse:
+            lse = make(ls, dtype=torch.float32, device=q.device)
+        if workspace is None and rows:
+            need = upipe_attn_paged_workspace_bytes(B, rows, Hq, cache.heads, D, prefix_len, mq, ml)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    upipe_attn_paged_fwd(_heads(q, "q"), _heads(out, "out"), lse, cache, page_table, ts, mp,
+                         seq_len, cu_seqlens, prefix_table, prefix_len, B, S, mq, ml,
+                         workspace, None if workspace is not None else 0,
+                         stream if stream is not None else _stream(None, q))
+    return out, lse

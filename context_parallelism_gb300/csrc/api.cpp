@@ -75,6 +75,7 @@ struct DevState {
   uint32_t* err = nullptr;  // 256-byte status word allocation
 };
 constexpr int kMaxDev = 64;
+constexpr uint32_t kErrBadPageBit = 0x40000000u;  // kErrBadPage of the kernels (ptx.cuh)
 std::mutex g_mu;
 DevState g_dev[kMaxDev];
 
@@ -220,6 +221,25 @@ cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int64_t cols, int
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_pages(CUtensorMap* map, const void* base, int D, int page_size, int heads,
+                            int64_t n_pages, int64_t slot_stride, int64_t head_stride,
+                            int64_t page_stride, int box_rows) {
+  tensor_map_encoder();
+  if (!g_encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot_stride * 2),
+                                 static_cast<cuuint64_t>(head_stride * 2),
+                                 static_cast<cuuint64_t>(page_stride * 2)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1049,7 +1069,10 @@ int upipe_sync_status(void* stream) {
   UPIPE_CUDA(cudaMemcpy(&w, g_dev[dev].err, sizeof(w), cudaMemcpyDeviceToHost));
   if (w) {
     UPIPE_CUDA(cudaMemset(g_dev[dev].err, 0, sizeof(w)));
-    return fail(UPIPE_ERR_TIMEOUT, "device status word 0x%x: a bounded wait expired", w);
+    if (w & ~kErrBadPageBit)
+      return fail(UPIPE_ERR_TIMEOUT, "device status word 0x%x: a bounded wait expired", w);
+    return fail(UPIPE_ERR_PAGE,
+                "a page-table entry or a length that a call had to follow names no page");
   }
   return UPIPE_OK;
 }
@@ -1062,6 +1085,7 @@ const char* upipe_status_string(int status) {
     case UPIPE_ERR_WORKSPACE_TOO_SMALL: return "UPIPE_ERR_WORKSPACE_TOO_SMALL";
     case UPIPE_ERR_CUDA: return "UPIPE_ERR_CUDA";
     case UPIPE_ERR_TIMEOUT: return "UPIPE_ERR_TIMEOUT";
+    case UPIPE_ERR_PAGE: return "UPIPE_ERR_PAGE";
     default: return "UPIPE_ERR_UNKNOWN";
   }
 }

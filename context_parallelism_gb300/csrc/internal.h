@@ -7,6 +7,7 @@
 #include <cstdio>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -285,6 +286,74 @@ cudaError_t launch_ce_dlogits(const float* logits, const float* lse, const int64
 cudaError_t launch_ce_merge(const float* part, int64_t part_stride, int n_parts,
                             const float* tlogit, const int64_t* target, float* loss, float* lse,
                             int64_t M, int64_t V, cudaStream_t stream);
+
+// ---- rotary positions and the paged cache (rope.cu) ----------------------------------------
+// Tensors 0 = q, 1 = k, 2 = v (append only); heads[t] = 0: absent. Element (b, i, h, d) of a
+// source lies at src[t] + b * src_b[t] + i * src_s[t] + h * src_h[t] + d, destinations likewise;
+// with `append`, k and v go to slot (page, place) of the caches dst[1], dst[2].
+struct RopeArgs {
+  const __nv_bfloat16* src[3];
+  __nv_bfloat16* dst[3];
+  int64_t src_b[3], src_s[3], src_h[3], dst_b[3], dst_s[3], dst_h[3];
+  int heads[3];
+  int B;
+  int64_t S;                // tokens per batch row (unused with cu)
+  int D, rot, copy_tail;    // copy_tail: features [rot, D) are copied (0: they are in place)
+  const int64_t* pos;       // [tokens] or NULL: pos0 + place (append: pos0 + index in the cache)
+  int64_t pos0;
+  const uint64_t* phase;    // [rot / 2] turns a position, in units of 2^-64
+  float mscale, sin_scale;  // factors of the cosine and (signed: the direction) of the sine
+  // append
+  const int32_t* table;     // [B][table_stride] page of each run of page_size tokens
+  int64_t table_stride, max_pages, n_pages;
+  int page_size;
+  int64_t page_stride, slot_stride, head_stride;  // elements
+  const int32_t* seq_len;   // [B] tokens of each sequence in its pages, the new ones among them
+  const int32_t* cu;        // [B + 1] first row of each sequence, or NULL: S rows each
+  uint32_t* err;
+  // set by launch_rope
+  int64_t tok0;
+  uint32_t units, n_chunks, n_groups;
+};
+cudaError_t launch_rope(RopeArgs a, bool interleaved, bool append, int64_t tokens,
+                        cudaStream_t stream);
+
+// ---- attention over a paged cache (attn_paged.cu) -------------------------------------------
+// Builds a 4-D bf16 tensor map [n_pages][heads][page_size][D] over one cache with the given
+// element strides and a box of box_rows slots x 64 features of one head, 128-byte swizzle.
+cudaError_t make_tmap_pages(CUtensorMap* map, const void* base, int D, int page_size, int heads,
+                            int64_t n_pages, int64_t slot_stride, int64_t head_stride,
+                            int64_t page_stride, int box_rows);
+
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  int64_t q_b, q_s, q_h, o_b, o_s, o_h;  // element strides (packed rows use q_s, o_s alone)
+  float* lse;                // [B][Hq][T] ([Hq][rows] with cu) or NULL
+  int64_t rows;              // rows of q: B * T, or the packed rows
+  int64_t T;                 // rows per sequence without cu
+  const int32_t* cu;         // [B + 1] or NULL
+  const int32_t* table;      // [B][table_stride]
+  int64_t table_stride, max_pages, n_pages;
+  const int32_t* seq_len;    // [B]
+  const int32_t* ptable;     // [ceil(prefix / page_size)]
+  int64_t prefix;
+  int B, Hq, Hkv, G, D, page_size, box_rows;
+  float scale_log2;
+  // partial results, one per (part, row, head): the numerator [D] fp32 and (max in log2 units,
+  // sum of the rounded weights, sum of the weights, 0). Parts [0, splits_p) cover the prefix,
+  // the others the sequence's own pages. With one part the kernels write o and lse themselves.
+  float* part_o;
+  float4* part_ml;
+  int splits_p, splits_o;    // key splits of the prefix (0: none) and of the own pages
+  int tiles_p, tiles_o;      // row tiles of the prefix items, and of each sequence's items
+  uint32_t* err;
+};
+// Plan of one call (host arithmetic): fills splits and tiles from the sizes and hints.
+void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len);
+cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
+                              const CUtensorMap& v_map, int64_t max_q, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 // ---- services of api.cpp to the other entry points -----------------------------------------
 // Per-device state (streams, status word) for `dev`, created on first use; a upipe status.

@@ -14,6 +14,7 @@ namespace upipe {
 enum : uint32_t {
   kErrNone = 0,
   kErrWaitTimeout = 1u,  // a bounded mbarrier wait expired; low bits of the word hold where
+  kErrBadPage = 0x40000000u,  // a page-table entry that a call had to follow names no page
 };
 
 // Default limit for every mbarrier wait in the attention kernels. No legitimate wait inside

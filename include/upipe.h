@@ -64,7 +64,9 @@ typedef enum {
   UPIPE_ERR_UNSUPPORTED = 2,          /* valid request outside what the kernels implement */
   UPIPE_ERR_WORKSPACE_TOO_SMALL = 3,  /* workspace_bytes < upipe_workspace_bytes(...) */
   UPIPE_ERR_CUDA = 4,                 /* a CUDA runtime/driver call failed */
-  UPIPE_ERR_TIMEOUT = 5               /* a kernel's bounded wait expired (see sync_status) */
+  UPIPE_ERR_TIMEOUT = 5,              /* a kernel's bounded wait expired (see sync_status) */
+  UPIPE_ERR_PAGE = 6                  /* a page-table entry or a length that a kernel had to
+                                         follow names no page of the cache (see sync_status) */
 } upipe_status;
 
 /* Which pass a workspace is sized for. UPIPE_PASS_FUSED: the loss's one-call forward and
@@ -185,7 +187,8 @@ int upipe_head_to_seq_major(const void* src, void* dst, int B, int64_t S, int H,
 /*
  * Synchronises `stream`, then reads and clears the current device's status word.
  * Returns UPIPE_OK, UPIPE_ERR_TIMEOUT (a kernel's bounded wait expired since the last
- * check) or UPIPE_ERR_CUDA (the synchronisation itself failed).
+ * check), UPIPE_ERR_PAGE (a kernel of the paged-cache calls met a page that does not exist
+ * since the last check) or UPIPE_ERR_CUDA (the synchronisation itself failed).
  */
 int upipe_sync_status(void* stream);
 
@@ -287,6 +290,133 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
                   float* dw_gu, float* dw_d, int64_t S, int Dm, int F, int64_t seq_tile,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Rotary positions --------------------------------------------------------------------
+ *
+ * The positions of q and k, before attention (training and prefill). For pair i < rot/2 of a
+ * head of token t at position p:
+ *   c = mscale cos(p f_i), s = mscale sin(p f_i);  y1 = x1 c - x2 s,  y2 = x2 c + x1 s,
+ * (x1, x2) = (x_i, x_{i + rot/2}) (interleaved = 0) or (x_{2i}, x_{2i+1}) (interleaved = 1);
+ * features rot..D-1 are copied. Backward: the gradient with respect to x of <dy, y>, the same
+ * map with -s. bf16 in and out, fp32 arithmetic, one rounding. The angle is exact for every
+ * 64-bit position, whatever its size: frequencies are kept as phases, 64-bit fixed-point
+ * fractions of a turn a position, and p * phase modulo 2^64 is the angle's fraction of a turn.
+ */
+
+/* A strided [B, S, heads, D] tensor of bf16: element (b, s, h, d) at
+ * data[b * stride_b + s * stride_s + h * stride_h + d]. data is 16-byte aligned; strides of
+ * extents above 1 are multiples of 8 elements, not negative, and at least D in tensors that are
+ * written. heads = 0 (or a NULL pointer to this struct): the tensor is absent. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_s, stride_h;
+  int32_t heads;
+} upipe_heads;
+
+/* How a context longer than the trained one is reached. LINEAR: f / factor. NTK: theta times
+ * factor^(rot / (rot - 2)). BY_PARTS: with r_i = trained_len f_i / (2 pi) the turns of pair i
+ * over the trained length and g = clip((r - turns_slow) / (turns_fast - turns_slow), 0, 1):
+ * f (g + (1 - g) / factor), and mscale = 0.1 ln(factor) + 1 (1 otherwise). */
+enum { UPIPE_ROPE_PLAIN = 0, UPIPE_ROPE_LINEAR = 1, UPIPE_ROPE_NTK = 2, UPIPE_ROPE_BY_PARTS = 3 };
+
+/* Host arithmetic, no device: f_i = theta^(-2i / rot_dim), scaled, in radians a position
+ * (inv_freq: rot_dim / 2 doubles, host memory), and the factor of cos and sin. */
+int upipe_rope_frequencies(double* inv_freq, double* mscale, int rot_dim, double theta,
+                           int scaling, double factor, double trained_len, double turns_fast,
+                           double turns_slow);
+/* Host arithmetic: phase[i] = frac(inv_freq[i] / (2 pi)) 2^64 (host memory). Copy the result to
+ * the device once; the calls below take that copy. */
+int upipe_rope_phases(const double* inv_freq, uint64_t* phase, int n);
+
+/*
+ * q and k (either may be absent) are rotated into q_out and k_out. An output is its input (same
+ * data and strides: in place) or does not overlap it. pos: device [B][S] positions, or NULL for
+ * pos0 + s. phase: device, rot_dim / 2 words. Supported: D a multiple of 8 up to 1024, rot_dim
+ * a multiple of 16 up to D. B = 0 or S = 0 does nothing. The backward takes the gradients of
+ * the outputs and writes those of the inputs. Neither allocates anything or touches the status
+ * word, so both may be captured into a graph from their first call on.
+ */
+int upipe_rope_fwd(const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+                   const upipe_heads* k_out, const int64_t* pos, int64_t pos0,
+                   const uint64_t* phase, double mscale, int B, int64_t S, int D, int rot_dim,
+                   int interleaved, void* stream);
+int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const upipe_heads* dq,
+                   const upipe_heads* dk, const int64_t* pos, int64_t pos0, const uint64_t* phase,
+                   double mscale, int B, int64_t S, int D, int rot_dim, int interleaved,
+                   void* stream);
+
+/* ---- Paged key/value cache and attention over it ------------------------------------------
+ *
+ * Serving after a prefill (upipe_attn_fwd with lse = NULL): new keys and values go into a paged
+ * cache, and the new tokens attend over a prefix that the whole batch shares and over their own
+ * pages. Inference only (no backward). The pages this library's schedules follow describe
+ * training; these calls have no counterpart there.
+ *
+ * Rows. B sequences with S new tokens each (cu_rows = NULL; q, k, v, o are [B, S, heads, D]), or
+ * a packed batch of S rows in all (cu_rows: device int32 [B + 1], not decreasing; sequence b
+ * owns rows cu_rows[b] .. cu_rows[b+1]-1; stride_b is not used). Packed rows that no sequence
+ * owns are neither read nor written. A sequence may have no row.
+ * Own tokens. seq_len[b] (device int32) counts sequence b's tokens in its own pages, this
+ * call's n_b new ones among them: new token i has index j = seq_len[b] - n_b + i, and lies in
+ * slot j % page_size of page page_table[b * table_stride + j / page_size] (device int32,
+ * max_pages entries a sequence). A row with j < 0 has no place in the cache: the append skips
+ * it, and attention sees no own key there; so a padded batch row is one of length 0.
+ * Pages. A page-table entry is followed only where a key is read or written. One that names no
+ * page (or a length beyond max_pages * page_size) never leads outside the cache: the append
+ * drops the token, attention reads zeros, and the next upipe_sync_status returns
+ * UPIPE_ERR_PAGE.
+ * Both calls use the device's status word: make the first one on a device (of any call that
+ * uses it) before a stream capture. They are asynchronous, deterministic and may be captured.
+ */
+
+/* k and v caches with one set of element strides: element (page, slot, head, d) at
+ * page * stride_page + slot * stride_slot + head * stride_head + d. 16-byte aligned; strides
+ * multiples of 8, at least D. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages, stride_page, stride_slot, stride_head;
+  int32_t page_size, heads, D;
+} upipe_pages;
+
+/*
+ * Writes the new tokens' k (rotated) and v into the cache and q (rotated; may be absent) into
+ * q_out. Positions: pos (device int64, one a row), or NULL for pos0 + j (pos0: the length of
+ * the shared prefix). phase = NULL: nothing is rotated. Any page_size >= 1; D and rot_dim as
+ * for upipe_rope_fwd. q_out is q itself or does not overlap it. Two rows must not name the same
+ * slot. q rows are rotated whether or not their token has a place in the cache.
+ */
+int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_heads* k,
+                    const upipe_heads* v, const upipe_pages* cache, const int32_t* page_table,
+                    int64_t table_stride, int64_t max_pages, const int32_t* seq_len,
+                    const int32_t* cu_rows, const int64_t* pos, int64_t pos0,
+                    const uint64_t* phase, double mscale, int B, int64_t S, int rot_dim,
+                    int interleaved, void* stream);
+
+/*
+ * o = softmax(q k^T / sqrt(D)) v over the keys that each row sees: the first prefix_len tokens of
+ * the pages prefix_table (device int32, ceil(prefix_len / page_size) entries; unused and may be
+ * NULL when prefix_len = 0), the same for every row and read once for all of them, then its
+ * sequence's own keys 0 .. j. lse (device float32, [B][Hq][S], or [Hq][S] for a packed batch;
+ * or NULL) = ln sum exp(scores). A row that sees no key gets o = 0 and lse = -inf. What slots
+ * outside prefix_len and seq_len hold does not matter, NaN included.
+ *   max_q (packed batches: new tokens of the longest sequence) and max_len (largest seq_len)
+ *   only choose tiles and key splits; any value >= 1 gives right results.
+ *   workspace: device, 256-byte aligned, >= upipe_attn_paged_workspace_bytes(...) for the same
+ *   sizes (rows = B * S, or S for a packed batch); contents on entry ignored, on exit undefined.
+ *   Calls (and captured graphs) that may run at the same time need workspaces of their own.
+ * Supported: D 64 or 128, Hq a multiple of Hkv, page_size a multiple of 16, up to 2^24 rows,
+ * prefix_len up to 2^30. B = 0 or S = 0 does nothing. One key order per shape: results repeat
+ * bitwise for the same sizes and hints.
+ */
+size_t upipe_attn_paged_workspace_bytes(int B, int64_t rows, int Hq, int Hkv, int D,
+                                        int64_t prefix_len, int64_t max_q, int64_t max_len);
+int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
+                         const upipe_pages* cache, const int32_t* page_table,
+                         int64_t table_stride, int64_t max_pages, const int32_t* seq_len,
+                         const int32_t* cu_rows, const int32_t* prefix_table, int64_t prefix_len,
+                         int B, int64_t S, int64_t max_q, int64_t max_len, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* ---- Diagnostics ---------------------------------------------------------------------- */
 
 /* Kernel classes for launch counting and profiling. */
@@ -304,7 +434,11 @@ enum {
   UPIPE_K_DKDV_D2H = 9,   /* not a kernel: one trunk's dK/dV copied device -> host */
   UPIPE_K_KV_WAIT = 10,   /* not a kernel: how long the compute stream stalled waiting for a
                              staged key/value trunk (the copy time not hidden behind compute) */
-  UPIPE_K_COUNT = 11
+  UPIPE_K_ROPE = 11,      /* rotary positions */
+  UPIPE_K_KV_APPEND = 12, /* append to the paged cache */
+  UPIPE_K_ATTN_PAGED = 13, /* attention over the paged cache: one launch per kind of item */
+  UPIPE_K_PAGED_MERGE = 14, /* joins the parts of its rows */
+  UPIPE_K_COUNT = 15
 };
 
 typedef struct {

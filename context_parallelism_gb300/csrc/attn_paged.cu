@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   int tile, n_tiles;
   {
     int64_t x = blockIdx.x;
-    const int64_t n_p = static_cast<int64_t>(a.splits_p) * a.tiles_p * a.Hkv;
+    const int64_t n_p =
+        a.splits_x ? 0 : static_cast<int64_t>(a.splits_p) * a.tiles_p * a.Hkv;
     int split, splits;
     if (x < n_p) {
       it.kvh = static_cast<int>(x % a.Hkv);
@@ -567,7 +568,7 @@ cudaError_t launch_one(const PagedArgs& a, const CUtensorMap& km, const CUtensor
                                    L::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t n = static_cast<int64_t>(a.Hkv) *
-                    (static_cast<int64_t>(a.splits_p) * a.tiles_p +
+                    ((a.splits_x ? 0 : static_cast<int64_t>(a.splits_p) * a.tiles_p) +
                      static_cast<int64_t>(a.splits_o) * a.tiles_o * a.B);
   if (n > 0x7fffffff) return cudaErrorInvalidValue;
   launch_begin(13, stream);
@@ -579,26 +580,56 @@ cudaError_t launch_one(const PagedArgs& a, const CUtensorMap& km, const CUtensor
 
 }  // namespace
 
+namespace {
+// Rows beyond which the prefix goes to the tensor-core kernel with 128-row tiles.
+bool prefix_on_tc(const PagedArgs& a) { return a.prefix >= 128 && a.rows * a.G > 16; }
+bool small_tiles(const PagedArgs& a, int64_t max_q) {
+  return max_q * a.G <= 16 && (a.prefix == 0 || a.splits_x || a.rows * a.G <= 16);
+}
+}  // namespace
+
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   const int64_t rows_o = max_q * a->G, rows_p = a->rows * a->G;
-  const int MT = rows_o <= 16 && (a->prefix == 0 || rows_p <= 16) ? 16 : 64;
+  constexpr int kSms = 152;
+  a->splits_x = 0;
+  if (prefix_on_tc(*a)) {
+    // One CTA per SM: waves of items, each as long as its share of key tiles and about four
+    // tiles' time of start and end. The fewest splits of the shortest time.
+    const bool pair = rows_p > 128;
+    a->tiles_p = static_cast<int>((rows_p + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    const int64_t items = static_cast<int64_t>(a->tiles_p) * a->Hkv;
+    const int64_t nt = (a->prefix + 127) / 128;
+    int64_t best = INT64_MAX;
+    for (int64_t s = 1; s <= nt && s <= 160; ++s) {
+      const int64_t waves = (items * s + kSms - 1) / kSms;
+      const int64_t cost = waves * ((nt + s - 1) / s + 4);
+      if (cost < best) {
+        best = cost;
+        a->splits_x = static_cast<int>(s);
+      }
+      if (waves > 16) break;
+    }
+    a->splits_p = a->splits_x * (pair ? 1 : 2);
+  }
+  const int MT = small_tiles(*a, max_q) ? 16 : 64;
   a->tiles_o = static_cast<int>((rows_o + MT - 1) / MT);
-  a->tiles_p = static_cast<int>((rows_p + MT - 1) / MT);
-  const int64_t slots = 608;  // two blocks on each of 152 SMs, twice over
+  const int64_t slots = 4 * kSms;  // two blocks on each SM, twice over
   auto splits = [&](int64_t items, int64_t keys) -> int {
     const int64_t nt = (keys + 255) / 256;
     int64_t s = (slots + items - 1) / items;
     if (s > nt) s = nt;
     return static_cast<int>(s < 1 ? 1 : s);
   };
-  a->splits_p = a->prefix ? splits(static_cast<int64_t>(a->tiles_p) * a->Hkv, a->prefix) : 0;
+  if (!a->splits_x) {
+    a->tiles_p = static_cast<int>((rows_p + MT - 1) / MT);
+    a->splits_p = a->prefix ? splits(static_cast<int64_t>(a->tiles_p) * a->Hkv, a->prefix) : 0;
+  }
   a->splits_o = splits(static_cast<int64_t>(a->tiles_o) * a->Hkv * a->B, max_len);
 }
 
 cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
                               const CUtensorMap& v_map, int64_t max_q, cudaStream_t stream) {
-  const int64_t rows_o = max_q * a.G, rows_p = a.rows * a.G;
-  const bool small = rows_o <= 16 && (a.prefix == 0 || rows_p <= 16);
+  const bool small = small_tiles(a, max_q);
   if (a.D == 128)
     return small ? launch_one<128, 16>(a, k_map, v_map, stream)
                  : launch_one<128, 64>(a, k_map, v_map, stream);

@@ -345,7 +345,9 @@ struct PagedArgs {
   // the others the sequence's own pages. With one part the kernels write o and lse themselves.
   float* part_o;
   float4* part_ml;
-  int splits_p, splits_o;    // key splits of the prefix (0: none) and of the own pages
+  int splits_p, splits_o;    // parts of the prefix (0: none), key splits of the own pages
+  int splits_x;              // key splits of launch_attn_prefix; 0: attn_paged_kernel takes the
+                             // prefix too, in splits_p splits
   int tiles_p, tiles_o;      // row tiles of the prefix items, and of each sequence's items
   uint32_t* err;
 };
@@ -353,6 +355,8 @@ struct PagedArgs {
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len);
 cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
                               const CUtensorMap& v_map, int64_t max_q, cudaStream_t stream);
+cudaError_t launch_attn_prefix(const PagedArgs& a, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 // ---- services of api.cpp to the other entry points -----------------------------------------

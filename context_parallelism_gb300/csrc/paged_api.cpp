@@ -215,7 +215,8 @@ int attn_plan(int B, int64_t rows, int Hq, int Hkv, int D, int64_t prefix_len, i
   if (max_q > rows) max_q = rows;
   plan_paged(a, max_q, max_len);
   const int64_t items = static_cast<int64_t>(Hkv) *
-                        (static_cast<int64_t>(a->splits_p) * a->tiles_p +
+                        (static_cast<int64_t>(a->splits_x ? a->splits_x : a->splits_p) *
+                             a->tiles_p +
                          static_cast<int64_t>(a->splits_o) * a->tiles_o * B);
   if (items > 0x7fffffff)
     return pfail(UPIPE_ERR_UNSUPPORTED, "too many row tiles: give max_q");
@@ -473,6 +474,7 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   PAGED_CUDA(make_tmap_pages(&vm, cache->v, D, cache->page_size, cache->heads, cache->n_pages,
                              cache->stride_slot, cache->stride_head, cache->stride_page,
                              a.box_rows));
+  if (a.splits_x) PAGED_CUDA(launch_attn_prefix(a, km, vm, stream));
   PAGED_CUDA(launch_attn_paged(a, km, vm, max_q < rows ? max_q : rows, stream));
   if (a.splits_p + a.splits_o > 1) PAGED_CUDA(launch_paged_merge(a, stream));
   return UPIPE_OK;

@@ -31,7 +31,7 @@ UPIPE_ROPE_PLAIN, UPIPE_ROPE_LINEAR, UPIPE_ROPE_NTK, UPIPE_ROPE_BY_PARTS = 0, 1,
 
 KERNEL_CLASSES = ["layout", "attn_fwd", "bwd_pre", "attn_bwd", "dq_convert", "other",
                   "loss_gemm", "loss_merge", "kv_h2d", "dkdv_d2h", "kv_wait", "rope",
-                  "kv_append", "attn_paged", "paged_merge"]
+                  "kv_append", "attn_paged", "paged_merge", "attn_prefix"]
 
 # Every symbol include/upipe.h declares, with (restype, argtypes).
 _vp, _i, _i64, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
@@ -138,11 +138,32 @@ def _ptr(x):
 def _stream(stream, *tensors):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
     for t in tensors:
         if hasattr(t, "is_cuda") and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return _current_stream(t)
     return None
+
+
+_torch = None
+_raw_stream = None
+
+
+def _lazy_torch():
+    """torch, imported once: the calls for single tokens are bound by the host's time."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _torch = torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _torch
+
+
+def _current_stream(t):
+    """Handle of the current stream on a CUDA tensor's device."""
+    torch = _torch or _lazy_torch()
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _check(status, where):
@@ -561,50 +582,47 @@ def mlp_backward(x, w_gu, w_d, dy, seq_tile=8192, workspace=None, stream=None,
 
 # ---- rotary positions, paged cache ----------------------------------------------------------
 
-def _heads(t, name):
-    """upipe_heads of a bf16 [..., heads, D] tensor: [B, S, heads, D], or packed [S, heads, D]."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+def _heads(t, name, dims):
+    """upipe_heads of a bf16 [B, S, heads, D] (dims 4) or packed [S, heads, D] (dims 3) tensor."""
+    torch = _torch or _lazy_torch()
     st = t.stride()
-    if t.dim() not in (3, 4) or (st[-1] != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be [B, S, heads, D] or [S, heads, D] with contiguous D, "
-                         f"not {tuple(t.shape)} with strides {st}")
-    return Heads(t.data_ptr(), st[0] if t.dim() == 4 else 0, st[-3], st[-2], t.shape[-2])
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+    if len(st) != dims or st[-1] != 1:
+        raise ValueError(f"{name} must have {dims} dimensions with contiguous features, not "
+                         f"{tuple(t.shape)} with strides {st}")
+    return Heads(t.data_ptr(), st[0] if dims == 4 else 0, st[-3], st[-2], t.shape[-2])
 
 
 def _pages(k_pages, v_pages):
-    import torch
-    if k_pages.dtype != torch.bfloat16 or v_pages.dtype != torch.bfloat16:
+    torch = _torch or _lazy_torch()
+    if k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16:
         raise TypeError("the caches must be bfloat16")
-    st = k_pages.stride()
-    if k_pages.dim() != 4 or st[3] != 1 or v_pages.shape != k_pages.shape or \
-            v_pages.stride() != st:
+    st, shape = k_pages.stride(), k_pages.shape
+    if len(st) != 4 or st[3] != 1 or v_pages.shape != shape or v_pages.stride() != st:
         raise ValueError("k_pages and v_pages must be [n_pages, page_size, heads, D] of one shape "
-                         "and one set of strides, with contiguous D")
-    n, ps, h, D = k_pages.shape
-    return Pages(k_pages.data_ptr(), v_pages.data_ptr(), n, st[0], st[1], st[2], ps, h, D)
+                         "and one set of strides, with contiguous features")
+    return Pages(k_pages.data_ptr(), v_pages.data_ptr(), shape[0], st[0], st[1], st[2], shape[1],
+                 shape[2], shape[3])
 
 
-def _ints(t, dtype, shape, name):
-    """Checks a dense integer tensor that the kernels index."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, not "
-                         f"{t.dtype} {tuple(t.shape)}")
+def _dense(t, dtype, shape, name):
+    """Checks a dense tensor that the kernels index; a missing one passes."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
 
 
-def _on(stream, device):
-    """Context in which torch allocates for the stream that the call runs on, so that a buffer
-    freed after the call is not handed to other work before that stream is done with it."""
-    import contextlib
-    import torch
+def _empty(stream, like, shape, dtype, zero=False):
+    """An uninitialised (or zeroed) tensor beside `like`, allocated for the stream that the call
+    runs on, so that its memory is not handed to other work before that stream is done with it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
+    torch = _torch or _lazy_torch()
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return _empty(None, like, shape, dtype, zero)
 
 
 def rope_phases(rot_dim, theta=10000.0, scaling=UPIPE_ROPE_PLAIN, factor=1.0, trained_len=0.0,
@@ -625,34 +643,38 @@ def rope_phases(rot_dim, theta=10000.0, scaling=UPIPE_ROPE_PLAIN, factor=1.0, tr
 
 
 def _phases(phases):
-    import torch
-    if phases.dtype != torch.int64 or phases.dim() != 1 or not phases.is_contiguous():
+    torch = _torch or _lazy_torch()
+    if phases.dtype is not torch.int64 or phases.dim() != 1 or not phases.is_contiguous():
         raise ValueError("phases must be a contiguous int64 vector (see rope_phases)")
-    return 2 * phases.numel()
+    return 2 * phases.shape[0]
 
 
 def _rope(call, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
-    import torch
+    torch = _torch or _lazy_torch()
     ref = q if q is not None else k
-    if ref is None or ref.dim() != 4 or (k is not None and (
-            k.dim() != 4 or k.shape[:2] != ref.shape[:2] or k.shape[3] != ref.shape[3])):
-        raise ValueError("q and k must be [B, S, heads, D] of the same B, S and D (one may be None)")
+    if ref is None or ref.dim() != 4:
+        raise ValueError("q and k must be [B, S, heads, D] (one may be None)")
     B, S, _, D = ref.shape
-    _ints(positions, torch.int64, (B, S), "positions")
+    if k is not None and k is not ref and (k.dim() != 4 or k.shape[:2] != ref.shape[:2] or
+                                           k.shape[3] != D):
+        raise ValueError("q and k must agree in B, S and D")
+    if positions is not None:
+        _dense(positions, torch.int64, ref.shape[:2], "positions")
     rot = _phases(phases)
-    views, outs = [], []
-    with _on(stream, ref.device):
-        for t, name in ((q, "q"), (k, "k")):
-            if t is None:
-                views += [None, None]
-                outs.append(None)
-                continue
-            y = t if inplace else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-            views += [_heads(t, name), _heads(y, name + " out")]
-            outs.append(y)
-    call(views[0], views[2], views[1], views[3], positions, start, phases, mscale, B, S, D, rot,
-         interleaved, stream if stream is not None else _stream(None, ref))
-    return outs[0], outs[1]
+    q_in = q_out = k_in = k_out = None
+    if q is not None:
+        q_in = _heads(q, "q", 4)
+        if not inplace:
+            q = _empty(stream, q, q.shape, q.dtype)
+        q_out = q_in if inplace else _heads(q, "q", 4)
+    if k is not None:
+        k_in = _heads(k, "k", 4)
+        if not inplace:
+            k = _empty(stream, k, k.shape, k.dtype)
+        k_out = k_in if inplace else _heads(k, "k", 4)
+    call(q_in, k_in, q_out, k_out, positions, start, phases, mscale, B, S, D, rot, interleaved,
+         stream if stream is not None else _stream(None, ref))
+    return q, k
 
 
 def rope_forward(q, k, phases, mscale=1.0, interleaved=False, positions=None, start=0,
@@ -671,25 +693,25 @@ def rope_backward(dq, dk, phases, mscale=1.0, interleaved=False, positions=None,
                  stream)
 
 
-def _rows(q, cu_seqlens, seq_len):
-    """B, S and leading shape of a padded [B, S, heads, D] or packed [S, heads, D] batch."""
-    import torch
+def _batch(q, cu_seqlens, seq_len):
+    """B, S and dimensions of a padded [B, S, heads, D] or packed [S, heads, D] batch."""
+    torch = _torch or _lazy_torch()
     B = seq_len.numel()
-    _ints(seq_len, torch.int32, (B,), "seq_len")
-    _ints(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
+    _dense(seq_len, torch.int32, (B,), "seq_len")
     if cu_seqlens is None:
         if q.dim() != 4 or q.shape[0] != B:
             raise ValueError(f"a padded batch is [{B}, S, heads, D], not {tuple(q.shape)}")
-        return B, q.shape[1], q.shape[:2]
+        return B, q.shape[1], 4
+    _dense(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
     if q.dim() != 3:
         raise ValueError(f"a packed batch is [rows, heads, D], not {tuple(q.shape)}")
-    return B, q.shape[0], q.shape[:1]
+    return B, q.shape[0], 3
 
 
 def _table(page_table, B):
-    import torch
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    torch = _torch or _lazy_torch()
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or \
+            page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError(f"page_table must be int32 [{B}, max_pages] with contiguous rows")
     return page_table.stride(0), page_table.shape[1]
 
@@ -705,24 +727,26 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, p
     D); page_table: int32 [B, max_pages]; seq_len: int32 [B], each sequence's tokens in its own
     pages with the new ones. Positions: positions (int64, one a row), or start + a token's index
     in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place)."""
-    import torch
-    B, S, lead = _rows(k, cu_seqlens, seq_len)
-    D = k_pages.shape[-1]
-    for t, name in ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out")):
-        if t is not None and (t.shape[:-2] != lead or t.shape[-1] != D):
-            raise ValueError(f"{name} must be {tuple(lead)} + [heads, {D}], not {tuple(t.shape)}")
+    torch = _torch or _lazy_torch()
+    B, S, dims = _batch(k, cu_seqlens, seq_len)
+    lead, D = k.shape[:-2], k_pages.shape[-1]
+    if k.shape[-1] != D or v.shape != k.shape:
+        raise ValueError(f"k and v must have one shape with {D} features, not {tuple(k.shape)} "
+                         f"and {tuple(v.shape)}")
     ts, mp = _table(page_table, B)
-    _ints(positions, torch.int64, tuple(lead), "positions")
-    if q is not None and q_out is None:
-        with _on(stream, q.device):
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if cu_seqlens is not None:
-                q_out.zero_()  # rows of no sequence are not written
-    qv = _heads(q, "q") if q is not None else None
-    qo = _heads(q_out, "q_out") if q is not None else None
-    upipe_kv_append(qv, qo, _heads(k, "k"), _heads(v, "v"), _pages(k_pages, v_pages), page_table,
-                    ts, mp, seq_len, cu_seqlens, positions, start, phases, mscale, B, S,
-                    _phases(phases) if phases is not None else 0, interleaved,
+    if positions is not None:
+        _dense(positions, torch.int64, lead, "positions")
+    qv = qo = None
+    if q is not None:
+        if q_out is None:  # rows of no sequence are not written
+            q_out = _empty(stream, q, q.shape, q.dtype, zero=cu_seqlens is not None)
+        if q.shape[:-2] != lead or q.shape[-1] != D or q_out.shape != q.shape:
+            raise ValueError(f"q and q_out must be {tuple(lead)} + [heads, {D}], not "
+                             f"{tuple(q.shape)} and {tuple(q_out.shape)}")
+        qv, qo = _heads(q, "q", dims), _heads(q_out, "q_out", dims)
+    upipe_kv_append(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims), _pages(k_pages, v_pages),
+                    page_table, ts, mp, seq_len, cu_seqlens, positions, start, phases, mscale, B,
+                    S, _phases(phases) if phases is not None else 0, interleaved,
                     stream if stream is not None else _stream(None, k))
     return q_out if q is not None else None
 
@@ -736,11 +760,11 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, prefix_table=None,
     v_pages, page_table, seq_len as for kv_append, called before for the same tokens. The first
     prefix_len tokens of the pages prefix_table (int32) are seen by every row and read once for
     all; then row i of a sequence with n new tokens sees its own keys 0 .. seq_len - n + i.
-    max_q, max_len: the largest numbers of new and own tokens, hints for tiles and splits only
+    max_q, max_len: the largest numbers of new and own tokens, hints for tiles and blocks only
     (default: the most that the tensors allow). lse: float32 [B, Hq, S] (packed: [Hq, rows]),
     returned when given or with_lse, else None."""
-    import torch
-    B, S, lead = _rows(q, cu_seqlens, seq_len)
+    torch = _torch or _lazy_torch()
+    B, S, dims = _batch(q, cu_seqlens, seq_len)
     cache = _pages(k_pages, v_pages)
     Hq, D = q.shape[-2:]
     if D != cache.D:
@@ -749,29 +773,33 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, prefix_table=None,
     if prefix_len:
         if prefix_table is None:
             raise ValueError("prefix_len without prefix_table")
-        _ints(prefix_table, torch.int32, (prefix_table.numel(),), "prefix_table")
+        _dense(prefix_table, torch.int32, (prefix_table.numel(),), "prefix_table")
         if prefix_table.numel() * cache.page_size < prefix_len:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages of "
                              f"{cache.page_size} for {prefix_len} tokens")
-    if out is not None and out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
-    rows = S if cu_seqlens is not None else B * S
-    ls = (Hq, S) if cu_seqlens is not None else (B, Hq, S)
-    if lse is not None:
-        _ints(lse, torch.float32, ls, "lse")
-    mq = S if cu_seqlens is None or max_q is None else max_q
+    packed = cu_seqlens is not None
+    if packed:
+        rows, mq = S, S if max_q is None else max_q
+    else:
+        rows, mq = B * S, S
     ml = max_len if max_len is not None else max(1, mp * cache.page_size)
-    with _on(stream, q.device):
-        make = torch.empty if cu_seqlens is None else torch.zeros  # rows of no sequence: not written
-        if out is None:
-            out = make(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None and with_lse:
-            lse = make(ls, dtype=torch.float32, device=q.device)
-        if workspace is None and rows:
-            need = upipe_attn_paged_workspace_bytes(B, rows, Hq, cache.heads, D, prefix_len, mq, ml)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    upipe_attn_paged_fwd(_heads(q, "q"), _heads(out, "out"), lse, cache, page_table, ts, mp,
-                         seq_len, cu_seqlens, prefix_table, prefix_len, B, S, mq, ml,
-                         workspace, None if workspace is not None else 0,
-                         stream if stream is not None else _stream(None, q))
+    # rows of no sequence are not written: zeros in what is made here
+    if out is None:
+        out = _empty(stream, q, q.shape, q.dtype, zero=packed)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
+    if lse is not None:
+        _dense(lse, torch.float32, (Hq, S) if packed else (B, Hq, S), "lse")
+    elif with_lse:
+        lse = _empty(stream, q, (Hq, S) if packed else (B, Hq, S), torch.float32, zero=packed)
+    wb = None
+    if workspace is None:
+        wb = 0
+        if rows:
+            wb = max(256, upipe_attn_paged_workspace_bytes(B, rows, Hq, cache.heads, D, prefix_len,
+                                                           mq, ml))
+            workspace = _empty(stream, q, (wb,), torch.uint8)
+    upipe_attn_paged_fwd(_heads(q, "q", dims), _heads(out, "out", dims), lse, cache, page_table,
+                         ts, mp, seq_len, cu_seqlens, prefix_table, prefix_len, B, S, mq, ml,
+                         workspace, wb, stream if stream is not None else _stream(None, q))
     return out, lse

@@ -1,12 +1,12 @@
 // Attention of a batch's new tokens over a paged key/value cache: the prefix that the whole batch
-// shares, computed once for all its rows, and each sequence's own pages.
+// shares (where attn_prefix.cu does not take it) and each sequence's own pages.
 //
 // Row (sequence b, new token i of n, q-head h) sees the prefix's keys 0..P-1 and its own keys
-// 0..len_b - n + i. Per kv-head, an item is a tile of rows (the G q-heads of consecutive tokens;
-// of all sequences for the prefix, of one for its own pages) against one range of keys:
+// 0..len_b - n + i. Per kv-head, a segment is a tile of rows (the G q-heads of consecutive
+// tokens; of all sequences for the prefix, of one for its own pages) with all its keys:
 //   s = scale <q, k>,  m = max s,  p = exp2(s - m) (log2 units),  O~ = sum p v,  l = sum p,
-// one pass with the running maximum and sum. An item's (m, l, O~) is one part of its rows; the
-// parts of a row are joined by
+// one pass with the running maximum and sum. A segment may be cut along its keys; each piece's
+// (m, l, O~) is one part of its rows, and the parts of a row are joined by
 //   M = max m_p,  o = sum 2^(m_p - M) O~_p / sum 2^(m_p - M) l_p,  lse = ln 2 (M + log2 l).
 // P is rounded to bf16 for the P V product. Two sums are kept: that of the rounded weights
 // divides O~ (numerator and denominator agree), that of the fp32 weights gives lse.
@@ -15,9 +15,16 @@
 // 4 x rows FLOP). The matrix instruction is mma.sync m16n8k16: a decode step has G to 16 rows a
 // kv-head, which a 128-row tcgen05 tile would fill to an eighth at most.
 //
-// Block: one producer warp (TMA boxes of page rows into a ring of 64-key stages) and four
-// consumer warps. Row tiles of 16 split each stage's keys over the four warps (16 each), which
-// join their statistics at the end; row tiles of 64 give each warp 16 rows and all keys.
+// Shares. The key tiles of all segments, in order, are cut into equal shares, one per worker:
+// lengths are read on the device, so ragged batches and captured graphs whose lengths move stay
+// balanced. A worker's share is a run of pieces of neighbouring segments; the piece of segment g
+// at worker c is kept in slot g + c (each step along the run moves g or c by one, so slots are
+// distinct, and a segment's pieces are neighbours). Segments are numbered sequence, row tile,
+// kv-head: neighbouring workers read neighbouring heads of the same pages.
+//
+// Two kernels, by the rows that a sequence has for a kv-head:
+//   up to 16 (a decode step): a worker is a single warp with a ring of TMA-fed stages of its own;
+//   17 and more: a worker is a block of one producer warp and four consumer warps of 16 rows.
 #include <cfloat>
 
 #include "internal.h"
@@ -26,17 +33,7 @@
 namespace upipe {
 namespace {
 
-constexpr int kKeys = 64;     // keys per stage
-constexpr int kThreads = 160;  // 4 consumer warps + 1 producer warp
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y,
-                                            int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
+constexpr int kSms = 152;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -50,6 +47,15 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// Transpose of an 8 x 8 matrix of 16-bit elements, two per lane in row-major lane order.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -59,123 +65,629 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int MT>
+// What is to be known of a piece to compute it.
+struct Piece {
+  int64_t tok0;      // first row of q of the segment's group
+  int64_t slot;
+  int32_t row0;      // first row (token, head-of-group order) of the tile
+  int32_t n_rows;    // rows of the group
+  int32_t kvh, own;  // own: the keys are the sequence's own (causal limit)
+  int32_t n_kt;      // tiles; -1: no more pieces
+  int32_t keys;      // keys of the piece
+  int32_t before;    // keys of the piece that token 0 sees, less one (own pieces; clamped)
+  int32_t parts;     // pieces of the segment
+  int32_t first;     // this one is its first
+};
+
+static_assert(sizeof(Piece) % 8 == 0, "pieces keep the alignment of their words");
+
+// a / b for 0 <= a, 0 < b; 32-bit where it can be (the 64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
+
+// One group of segments (the prefix: b = -1, or a sequence): its rows and keys.
+struct Group {
+  int tok0, n_tok;   // rows of q
+  int keys;
+  uint32_t segs;     // row tiles x kv-heads
+  uint32_t cost;     // tiles per segment, at least one (a segment without keys still writes)
+  __device__ __forceinline__ uint64_t tiles() const { return static_cast<uint64_t>(segs) * cost; }
+};
+
+template <int KS, int MT>
+__device__ __forceinline__ Group load_group(const PagedArgs& a, int b, bool report) {
+  Group g;
+  const int rows = static_cast<int>(a.rows);
+  if (b < 0) {
+    g.tok0 = 0;
+    g.n_tok = a.splits_x || !a.prefix ? 0 : a.cu ? min(rows, max(a.cu[a.B], 0)) : rows;
+    g.keys = static_cast<int>(a.prefix);
+  } else {
+    const int len = a.seq_len[b];
+    if (a.cu) {
+      const int c0 = a.cu[b], c1 = a.cu[b + 1];
+      g.tok0 = min(max(c0, 0), rows);
+      g.n_tok = max(min(c1, rows) - g.tok0, 0);
+    } else {
+      g.tok0 = b * static_cast<int>(a.T);
+      g.n_tok = static_cast<int>(a.T);
+    }
+    if (report && len > a.cap) atomicOr(a.err, kErrBadPage);
+    g.keys = min(max(len, 0), a.cap);
+  }
+  g.segs = (static_cast<uint32_t>(g.n_tok * a.G) + (MT - 1)) / MT * a.Hkv;
+  g.cost = max((static_cast<uint32_t>(g.keys) + (KS - 1)) / KS, 1u);
+  return g;
+}
+
+// A place in a worker's share; every lane of the warp holds the same.
+template <int KS, int MT>
+struct Walk {
+  Group g;
+  uint32_t left, share;      // tiles that are still to come, and of a whole share
+  uint32_t group_seg, seg, kt;  // segments before the group; segment of the group, tile of it
+  int b, worker, kvh, row0;
+  int k_lo, k_hi;            // the piece's keys
+
+  // Cuts all tiles into the workers' shares (of at least `least` tiles) and finds this worker's
+  // start. Sequences are taken 32 at a time, one per lane.
+  __device__ __forceinline__ void init(const PagedArgs& a, int lane, int worker_, int n_workers,
+                                       uint32_t least) {
+    worker = worker_;
+    left = group_seg = seg = kt = 0;
+    kvh = row0 = 0;
+    b = -1;
+    Group mine;  // sequence `lane`, kept for the second pass
+    mine.segs = mine.cost = 0;
+    if (lane < a.B) mine = load_group<KS, MT>(a, lane, worker == 0);
+    g = load_group<KS, MT>(a, -1, false);
+    uint64_t total = mine.tiles();
+    for (int b0 = lane + 32; b0 < a.B; b0 += 32)
+      total += load_group<KS, MT>(a, b0, worker == 0).tiles();
+#pragma unroll
+    for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+    total += g.tiles();
+    const uint64_t sh = total + n_workers - 1;
+    share = max(static_cast<uint32_t>((sh >> 32) ? sh / n_workers : static_cast<uint32_t>(sh) / n_workers),
+                least);
+    uint64_t x = static_cast<uint64_t>(worker) * share;
+    if (x >= total) return;
+    left = static_cast<uint32_t>(min(static_cast<uint64_t>(share), total - x));
+    if (x >= g.tiles()) {
+      x -= g.tiles();
+      group_seg = g.segs;
+      for (int b0 = 0;; b0 += 32) {
+        if (b0 > 0) {
+          mine.segs = mine.cost = 0;
+          if (b0 + lane < a.B) mine = load_group<KS, MT>(a, b0 + lane, false);
+        }
+        uint64_t ws = mine.tiles();  // inclusive sums over the lanes
+        uint32_t ns = mine.segs;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const uint64_t u = __shfl_up_sync(0xffffffffu, ws, s);
+          const uint32_t v = __shfl_up_sync(0xffffffffu, ns, s);
+          if (lane >= s) {
+            ws += u;
+            ns += v;
+          }
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, ws > x);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          b = b0 + l;
+          x -= __shfl_sync(0xffffffffu, ws - mine.tiles(), l);
+          group_seg += __shfl_sync(0xffffffffu, ns - mine.segs, l);
+          g.tok0 = __shfl_sync(0xffffffffu, mine.tok0, l);
+          g.n_tok = __shfl_sync(0xffffffffu, mine.n_tok, l);
+          g.keys = __shfl_sync(0xffffffffu, mine.keys, l);
+          g.segs = __shfl_sync(0xffffffffu, mine.segs, l);
+          g.cost = __shfl_sync(0xffffffffu, mine.cost, l);
+          break;
+        }
+        x -= __shfl_sync(0xffffffffu, ws, 31);
+        group_seg += __shfl_sync(0xffffffffu, ns, 31);
+        if (b0 + 32 >= a.B) {  // not reached: the shares add up to the tiles
+          left = 0;
+          return;
+        }
+      }
+    }
+    seg = static_cast<uint32_t>((x >> 32) ? x / g.cost : static_cast<uint32_t>(x) / g.cost);
+    kt = static_cast<uint32_t>(x - static_cast<uint64_t>(seg) * g.cost);
+    const uint32_t rt = seg / a.Hkv;
+    kvh = static_cast<int>(seg - rt * a.Hkv);
+    row0 = static_cast<int>(rt) * MT;
+  }
+
+  // The next piece; false at the end of the share.
+  __device__ __forceinline__ bool next(const PagedArgs& a, Piece* p) {
+    if (left == 0) return false;
+    while (seg >= g.segs) {
+      group_seg += g.segs;
+      seg = 0;
+      row0 = kvh = 0;
+      if (++b >= a.B) return false;
+      g = load_group<KS, MT>(a, b, false);
+    }
+    const uint32_t n = min(g.cost - kt, left);
+    k_lo = min(static_cast<int>(kt * KS), g.keys);
+    k_hi = static_cast<int>(min((kt + n) * KS, static_cast<uint32_t>(g.keys)));
+    p->tok0 = g.tok0;
+    p->slot = static_cast<int64_t>(group_seg) + seg + worker;
+    p->row0 = row0;
+    p->n_rows = g.n_tok * a.G;
+    p->kvh = kvh;
+    p->own = b >= 0;
+    p->keys = k_hi - k_lo;
+    p->n_kt = (p->keys + KS - 1) / KS;
+    p->before = g.keys - g.n_tok - k_lo;
+    p->first = kt == 0;
+    // workers from the segment's first tile to its last (known where the segment starts)
+    const uint32_t rest = g.cost - kt - n;
+    p->parts = kt == 0 ? 1 + static_cast<int>(rest ? (rest + share - 1) / share : 0u) : 2;
+    left -= n;
+    kt += n;
+    if (kt == g.cost) {
+      kt = 0;
+      ++seg;
+      if (++kvh == a.Hkv) {
+        kvh = 0;
+        row0 += MT;
+      }
+    }
+    return true;
+  }
+};
+
+// Token and q-head of a tile's row, and its place in q, o and lse.
+struct Row {
+  int i, h;       // token of the group, q-head
+  int64_t t;      // row of q
+  int64_t b, s;   // batch row and place (packed rows: 0 and t)
+};
+
+__device__ __forceinline__ Row find_row(const PagedArgs& a, const Piece& p, int r) {
+  Row w;
+  const int row = p.row0 + r;
+  // one token's rows, as in a plain decode step, need no division
+  w.i = row < a.G ? 0 : static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.G));
+  w.h = p.kvh * a.G + row - w.i * a.G;
+  w.t = p.tok0 + w.i;
+  if (a.cu) {
+    w.b = 0;
+    w.s = w.t;
+  } else if (p.own) {  // the group is a batch row of T tokens
+    w.s = w.i;
+    w.b = a.T == 1 ? w.t : div_fl(p.tok0, a.T);
+  } else {
+    w.b = a.T == 1 ? w.t : div_fl(w.t, a.T);
+    w.s = w.t - w.b * a.T;
+  }
+  return w;
+}
+
+// Where a row's results go: its own outputs if the piece is all that its row has, else its slot.
+struct RowOut {
+  __nv_bfloat16* o;
+  float* lse;
+  float* part;
+  float4* ml;
+};
+
+// say: this lane tells the join where the row's pieces are.
+__device__ __forceinline__ RowOut row_out(const PagedArgs& a, const Piece& p, int r, int MT, int D,
+                                          bool say) {
+  RowOut w = {nullptr, nullptr, nullptr, nullptr};
+  const Row f = find_row(a, p, r);
+  const bool sole = p.parts == 1 && a.prefix == 0;
+  if (sole) {
+    w.o = a.o + f.b * a.o_b + f.s * a.o_s + f.h * a.o_h;
+    if (a.lse) w.lse = a.lse + (a.cu ? f.h * a.rows + f.t : (f.b * a.Hq + f.h) * a.T + f.s);
+  } else if (p.slot < a.n_slots) {  // beyond only for cu_rows that decrease
+    w.part = a.slot_o + (p.slot * MT + r) * D;
+    w.ml = a.slot_ml + (p.slot * MT + r);
+  }
+  if (p.first && say)
+    a.desc[(p.own ? a.rows * a.Hq : 0) + f.t * a.Hq + f.h] =
+        make_int2(static_cast<int>(p.slot * MT + r), sole ? 0 : p.parts);
+  return w;
+}
+
+__device__ __forceinline__ const __nv_bfloat16* q_row(const PagedArgs& a, const Piece& p, int r) {
+  if (p.row0 + r >= p.n_rows) return nullptr;
+  const Row f = find_row(a, p, r);
+  return a.q + f.b * a.q_b + f.s * a.q_s + f.h * a.q_h;
+}
+
+// Keys of the piece that a row sees.
+__device__ __forceinline__ int row_limit(const PagedArgs& a, const Piece& p, int r) {
+  const int row = p.row0 + r;
+  if (row >= p.n_rows) return 0;
+  if (!p.own) return p.keys;
+  const int i = row < a.G ? 0 : static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.G));
+  return min(p.keys, p.before + i + 1);
+}
+
+// ---- up to 16 rows: one warp a worker --------------------------------------------------------
+//
+// S^T = K Q^T and O^T += V^T P^T: keys and features fill the instruction's 16 rows, the few query
+// rows its 8 columns (NR column tiles). The warp keeps its piece's rows in registers and issues
+// the TMA copies into its ring itself, each stage's next one as soon as it has read it, running
+// on into the pieces that follow: no producer, no barrier but a stage's own, nothing to meet at.
+constexpr int kWarps = 8;
+
+template <int D, int NR>
+struct DLayout {
+  static constexpr int kKeys = 2048 / D;            // 8 KiB of K and V a stage
+  static constexpr int kStage = 2 * kKeys * D * 2;
+  static constexpr int kStages = 3;
+  static constexpr int kPieces = 4;                 // published ahead: one a stage and one more
+  static constexpr int kBar = kWarps * kStages * kStage;
+  static constexpr int kPiece = kBar + kWarps * kStages * 8;
+  static constexpr int kBytes = kPiece + kWarps * kPieces * static_cast<int>(sizeof(Piece)) + 1024;
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
+  using L = DLayout<D, NR>;
+  constexpr int MT = 8 * NR, KS = L::kKeys, NS = L::kStages;
+  constexpr int kHalf = KS * 128;      // bytes of a stage's 64 features of K or V
+  constexpr int kVoff = KS * D * 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar) + warp * NS;
+  Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPiece) + warp * L::kPieces;
+  const uint32_t ring = smem_u32(smem) + warp * NS * L::kStage;
+
+  launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  {
+    // the tables, on their way to L2 while the lengths are read
+    const uint32_t line = blockIdx.x * blockDim.x + threadIdx.x;
+    const uint32_t per = static_cast<uint32_t>(min((a.max_pages + 31) / 32, int64_t(1) << 20));
+    const uint32_t b = line / per;
+    if (b < static_cast<uint32_t>(a.B))
+      prefetch_l2(a.table + b * a.table_stride + (line - b * per) * 32);
+  }
+  __syncwarp();
+
+  // ---- the copies: a place in the share that runs ahead of the computation ----
+  Walk<KS, MT> wk;
+  // neighbouring shares on neighbouring SMs; few shares on one warp each
+  wk.init(a, lane, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x),
+          static_cast<int>(gridDim.x) * kWarps, static_cast<uint32_t>(a.least));
+  // A tile is KS / bx boxes of bx page rows, two lanes' halves of the features each. Pages are
+  // looked up 32 boxes at a time, one a lane, so that a tile's copy waits for no load.
+  const int bx = a.box_rows;  // 16 or 32: divides page_size and the tile's keys
+  const int shift = bx == 16 ? 4 : 5;
+  const int box = lane / (D / 64), half = lane % (D / 64);
+  const bool mine = box * bx < KS;
+  const uint32_t off = half * kHalf + box * bx * 128;
+  uint32_t n_cp = 0, n_pc = 0;  // tiles copied and pieces published so far
+  int left = 0;                 // tiles of the piece that are still to be copied
+  int key0 = 0, kvh = 0;
+  int win = 0, win_page = -1, win_slot = 0;  // first key of the 32 boxes looked up; this lane's
+  const int32_t* pages = nullptr;
+  bool more = true;
+  // A box past the keys, or of a page that does not exist, lies outside the tensor map (page -1)
+  // and reads as zeros; nothing outside the caches is touched.
+  auto look_up = [&]() {
+    win = key0;
+    const int key = key0 + lane * bx;
+    win_page = -1;
+    win_slot = 0;
+    if (key < wk.k_hi) {
+      const uint32_t pg = static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size);
+      win_page = pages[pg];
+      win_slot = key - static_cast<int>(pg) * a.page_size;
+      if (win_page < 0 || win_page >= a.n_pages) {
+        win_page = -1;
+        atomicOr(a.err, kErrBadPage);
+      }
+    }
+  };
+  // Publishes the next piece (one without keys too).
+  auto publish = [&]() {
+    Piece p;
+    more = wk.next(a, &p);
+    if (!more) p.n_kt = -1;
+    if (lane == 0) pieces[n_pc % L::kPieces] = p;
+    __syncwarp();
+    ++n_pc;
+    left = more ? p.n_kt : 0;
+    if (left == 0) return;
+    key0 = wk.k_lo;
+    kvh = p.kvh;
+    pages = p.own ? a.table + wk.b * a.table_stride : a.ptable;
+    look_up();
+  };
+  // Copies the next tile, if there is one, into the stage that the tile kStages before it has left,
+  // publishing pieces on the way as long as there is room for them.
+  auto copy_next = [&](uint32_t n_done) {
+    while (left == 0) {
+      if (!more || n_pc - n_done >= static_cast<uint32_t>(L::kPieces)) return;
+      publish();
+    }
+    if (((key0 - win) >> shift) + KS / bx > 32) look_up();
+    const int s = static_cast<int>(n_cp % NS);
+    const int src = (((key0 - win) >> shift) + box) & 31;
+    const int page = __shfl_sync(0xffffffffu, win_page, src);
+    const int slot = __shfl_sync(0xffffffffu, win_slot, src);
+    if (lane == 0) mbar_arrive_expect_tx(full + s, L::kStage);
+    __syncwarp();
+    if (mine) {
+      const uint32_t dst = ring + s * L::kStage + off;
+      tma_load_4d(dst, &tm_k, half * 64, slot, kvh, page, full + s);
+      tma_load_4d(dst + kVoff, &tm_v, half * 64, slot, kvh, page, full + s);
+    }
+    ++n_cp;
+    --left;
+    key0 += KS;
+  };
+
+  uint32_t n_it = 0, n_done = 0;  // tiles and pieces computed
+  publish();
+  bool ok = true;
+  while (ok) {
+    const Piece p = pieces[n_done % L::kPieces];
+    if (p.n_kt < 0) break;
+    // B fragments of Q^T: row lane/4 of each tile, features (lane%4)*2 and +8 of each 16
+    uint32_t qf[NR][D / 16][2];
+    int lim[NR][2];  // key limits of this thread's two statistics rows of each tile
+#pragma unroll
+    for (int c = 0; c < NR; ++c) {
+      const __nv_bfloat16* qp = q_row(a, p, c * 8 + (lane >> 2));
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[c][k][e] = qp ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + e * 8 + (lane & 3) * 2) : 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[c][e] = row_limit(a, p, c * 8 + (lane & 3) * 2 + e);
+    }
+    float o[NR][D / 16][4];
+    float m[NR][2], lb[NR][2], lf[NR][2];
+#pragma unroll
+    for (int c = 0; c < NR; ++c) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[c][e] = -INFINITY;
+        lb[c][e] = lf[c][e] = 0.f;
+      }
+    }
+    // the first copies, behind the loads of q
+    if (n_done == 0)
+      for (int i = 0; i < NS; ++i) copy_next(0);
+    for (int j = 0; j < p.n_kt; ++j, ++n_it) {
+      const int s = static_cast<int>(n_it % NS);
+      ok = __all_sync(0xffffffffu, mbar_wait(full + s, (n_it / NS) & 1));
+      if (!ok) break;
+      const uint32_t sk = ring + s * L::kStage, sv = sk + kVoff;
+      const int k0 = j * KS;
+      // Values past the piece's last key (slots of its last page that no token fills) may be
+      // anything, infinities and NaN among them, and 0 * inf is not 0: they are cleared.
+      if (k0 + KS > p.keys) {
+        for (int x = lane; x < KS * (D / 8); x += 32) {
+          const int r = x / (D / 8), ch = x % (D / 8);
+          if (r >= p.keys - k0)
+            st_shared_v4(sv + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before TMA may fill the stage again
+        __syncwarp();
+      }
+      float sc[NR][KS / 16][4], sd[NR][KS / 16][4];  // two chains of sums: half the latency
+#pragma unroll
+      for (int c = 0; c < NR; ++c)
+#pragma unroll
+        for (int t = 0; t < KS / 16; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[c][t][e] = sd[c][t][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const int ch = (k & 3) * 2 + (lane >> 4);
+#pragma unroll
+        for (int t = 0; t < KS / 16; ++t) {
+          const int r = t * 16 + (lane & 15);
+          uint32_t ka[4];
+          ldsm4(ka, sk + (k >> 2) * kHalf + r * 128 + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+          for (int c = 0; c < NR; ++c)
+            mma16816(k & 1 ? sd[c][t] : sc[c][t], ka, qf[c][k][0], qf[c][k][1]);
+        }
+      }
+      // scores: [e] = key (lane/4) + 8 (e/2), row (lane%4)*2 + e%2 of the tile
+#pragma unroll
+      for (int c = 0; c < NR; ++c) {
+        float mx[2] = {m[c][0], m[c][1]};
+#pragma unroll
+        for (int t = 0; t < KS / 16; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool seen = k0 + t * 16 + (lane >> 2) + (e >> 1) * 8 < lim[c][e & 1];
+            sc[c][t][e] = seen ? (sc[c][t][e] + sd[c][t][e]) * a.scale_log2 : -INFINITY;
+            mx[e & 1] = fmaxf(mx[e & 1], sc[c][t][e]);
+          }
+        float al[2], base[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1)
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
+          base[e] = mx[e] == -INFINITY ? 0.f : mx[e];
+          al[e] = ex2_approx(m[c][e] - base[e]);
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[c][0] || mx[1] > m[c][1])) {
+#pragma unroll
+          for (int n2 = 0; n2 < D / 16; ++n2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[c][n2][e] *= al[e & 1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            lb[c][e] *= al[e];
+            lf[c][e] *= al[e];
+            m[c][e] = mx[e];
+          }
+        }
+        // weights, rounded to bf16 once for the product; two rows of one key are packed and
+        // transposed into the product's B layout (two keys of one row)
+#pragma unroll
+        for (int t = 0; t < KS / 16; ++t) {
+          uint32_t pb[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p0 = ex2_approx(sc[c][t][2 * e] - base[0]);
+            const float p1 = ex2_approx(sc[c][t][2 * e + 1] - base[1]);
+            lf[c][0] += p0;
+            lf[c][1] += p1;
+            const uint32_t w = pack_bf16(p0, p1);
+            add_bf16x2(lb[c][0], lb[c][1], w);
+            pb[e] = movmatrix(w);
+          }
+          sc[c][t][0] = __uint_as_float(pb[0]);
+          sc[c][t][1] = __uint_as_float(pb[1]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < KS / 16; ++t)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          const int r = t * 16 + ((lane >> 4) << 3) + (lane & 7);
+          const int ch = (d & 3) * 2 + ((lane >> 3) & 1);
+          uint32_t va[4];
+          ldsm4_t(va, sv + (d >> 2) * kHalf + r * 128 + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+          for (int c = 0; c < NR; ++c)
+            mma16816(o[c][d], va, __float_as_uint(sc[c][t][0]), __float_as_uint(sc[c][t][1]));
+        }
+      __syncwarp();
+      copy_next(n_done);
+    }
+    if (!ok) break;
+    // statistics over the lanes that share a row
+#pragma unroll
+    for (int c = 0; c < NR; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          lb[c][e] += __shfl_xor_sync(0xffffffffu, lb[c][e], x);
+          lf[c][e] += __shfl_xor_sync(0xffffffffu, lf[c][e], x);
+        }
+    // row (lane%4)*2 + e of a tile: this lane has features lane/4 + 8 i of it
+#pragma unroll
+    for (int c = 0; c < NR; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = c * 8 + (lane & 3) * 2 + e;
+        if (p.row0 + r >= p.n_rows) continue;
+        const int d0 = lane >> 2;
+        const RowOut w = row_out(a, p, r, MT, D, d0 == 0);
+        if (w.o) {
+          const float inv = lb[c][e] == 0.f ? 0.f : 1.f / lb[c][e];
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              w.o[n * 16 + f * 8 + d0] = __float2bfloat16_rn(o[c][n][2 * f + e] * inv);
+          if (w.lse && d0 == 0) *w.lse = (m[c][e] + log2f(lf[c][e])) * 0.69314718055994530942f;
+        } else if (w.part) {
+          if (lf[c][e] != 0.f) {  // NaN goes through
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) w.part[n * 16 + f * 8 + d0] = o[c][n][2 * f + e];
+          }
+          if (d0 == 0) *w.ml = make_float4(m[c][e], lb[c][e], lf[c][e], 0.f);
+        }
+      }
+    ++n_done;
+    // the room for pieces may have held the copies up; at least the next piece is published here
+    while (n_cp - n_it < static_cast<uint32_t>(NS) && (left > 0 || (more && n_pc - n_done < static_cast<uint32_t>(L::kPieces)))) {
+      const uint32_t before = n_cp;
+      copy_next(n_done);
+      if (n_cp == before) break;
+    }
+  }
+  if (!ok) {  // a copy did not arrive within the limit
+    if (lane == 0) atomicOr(a.err, kErrWaitTimeout | 0x10000u);
+    for (uint32_t j = n_it; j < n_cp; ++j) mbar_wait(full + j % NS, (j / NS) & 1, 100000000ull);
+  }
+  // the prefix kernel that this one may have started beside is done before this one is, so that
+  // what follows this one follows both
+  grid_dependency_wait();
+}
+
+// ---- more rows: one block a worker --------------------------------------------------------------
+//
+// Row tiles of 64: one producer warp, which walks the share, publishes each piece and streams its
+// keys and values through a ring of 64-key stages, running ahead into the next pieces, and four
+// consumer warps, each with 16 rows and every stage: S = Q K^T, O += P V.
+constexpr int kThreads = 160;
+constexpr int kPieces = 4;     // pieces published ahead
+
+template <int D>
 struct PLayout {
+  static constexpr int kKeys = 64;
   static constexpr int kStage = 2 * kKeys * D * 2;  // K then V
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kMl = kStages * kStage;      // 16-row tiles: 4 warps x 16 rows float4
-  static constexpr int kBar = kMl + 4 * 16 * 16;
-  static constexpr int kAbort = kBar + (2 * kStages + 2) * 8;
+  static constexpr int kStages = 98304 / kStage;
+  static constexpr int kBar = kStages * kStage;
+  static constexpr int kPiece = kBar + (2 * kStages + 2 * kPieces + 2) * 8;
+  static constexpr int kAbort = kPiece + kPieces * static_cast<int>(sizeof(Piece));
   static constexpr int kBytes = kAbort + 16 + 1024;
 };
 
-// Rows [row0, row0 + n_rows) of an item in (token, head-of-group) order, and its key range.
-struct Item {
-  int kvh;
-  int part;
-  int b;             // own sequence (-1: the prefix)
-  int64_t tok0;      // first token (row of q) of the segment
-  int64_t n_tok;     // tokens of the segment
-  int64_t k_lo, k_hi;
-  int64_t own_before;  // own keys that the first token sees less one (causal limit), own items
-  const int32_t* pages;
-  int64_t n_table;
-};
-
-__device__ __forceinline__ int64_t row_limit(const Item& it, int64_t i) {
-  return it.b < 0 ? it.k_hi : min(it.k_hi, it.own_before + i + 1);
-}
-
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
-    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
-  using L = PLayout<D, MT>;
-  constexpr int KW = MT == 16 ? 16 : 64;  // keys of a stage that one warp works on
+  using L = PLayout<D>;
+  constexpr int MT = 64;
+  constexpr int KS = L::kKeys, NS = L::kStages;
+  constexpr int kHalf = KS * 128;      // bytes of a stage's 64 features of K or V
+  constexpr int kVoff = KS * D * 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* empty = full + L::kStages;
-  uint64_t* meet = empty + L::kStages;  // the four consumer warps among themselves
-  uint64_t* joined = meet + 1;          // 16-row tiles: the stages' memory is free again
+  uint64_t* empty = full + NS;
+  uint64_t* piece_full = empty + NS;
+  uint64_t* piece_empty = piece_full + kPieces;
+  uint64_t* meet = piece_empty + kPieces;  // the four consumer warps among themselves
+  Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPiece);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
+  launch_dependents();
+  if (threadIdx.x == 128) {
+    for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 4);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(piece_full + i, 1);
+      mbar_init(piece_empty + i, 4);
+    }
     mbar_init(meet, 4);
-    mbar_init(joined, 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
-
-  // ---- which item ------------------------------------------------------------------------
-  Item it;
-  int tile, n_tiles;
-  {
-    int64_t x = blockIdx.x;
-    const int64_t n_p =
-        a.splits_x ? 0 : static_cast<int64_t>(a.splits_p) * a.tiles_p * a.Hkv;
-    int split, splits;
-    if (x < n_p) {
-      it.kvh = static_cast<int>(x % a.Hkv);
-      x /= a.Hkv;
-      tile = static_cast<int>(x % a.tiles_p);
-      split = static_cast<int>(x / a.tiles_p);
-      n_tiles = a.tiles_p;
-      splits = a.splits_p;
-      it.part = split;
-      it.b = -1;
-      it.tok0 = 0;
-      it.n_tok = a.rows;
-      if (a.cu) it.n_tok = min(a.rows, max(static_cast<int64_t>(a.cu[a.B]), int64_t(0)));
-      it.k_lo = 0;
-      it.k_hi = a.prefix;
-      it.own_before = 0;
-      it.pages = a.ptable;
-      it.n_table = (a.prefix + a.page_size - 1) / a.page_size;
-    } else {
-      x -= n_p;
-      it.kvh = static_cast<int>(x % a.Hkv);
-      x /= a.Hkv;
-      tile = static_cast<int>(x % a.tiles_o);
-      x /= a.tiles_o;
-      split = static_cast<int>(x % a.splits_o);
-      it.b = static_cast<int>(x / a.splits_o);
-      n_tiles = a.tiles_o;
-      splits = a.splits_o;
-      it.part = a.splits_p + split;
-      if (a.cu) {
-        const int64_t c0 = a.cu[it.b], c1 = a.cu[it.b + 1];
-        it.tok0 = min(max(c0, int64_t(0)), a.rows);
-        it.n_tok = max(min(c1, a.rows) - it.tok0, int64_t(0));
-      } else {
-        it.tok0 = it.b * a.T;
-        it.n_tok = a.T;
-      }
-      const int64_t cap = a.max_pages * a.page_size;
-      int64_t len = a.seq_len[it.b];
-      if (len > cap && threadIdx.x == 0) atomicOr(a.err, kErrBadPage);
-      len = min(max(len, int64_t(0)), cap);
-      it.k_lo = 0;
-      it.k_hi = len;
-      it.own_before = len - it.n_tok;
-      it.pages = a.table + it.b * a.table_stride;
-      it.n_table = a.max_pages;
-    }
-    // this split's share of the 64-key tiles, at least four of them
-    const int64_t nt = (it.k_hi + kKeys - 1) / kKeys;
-    const int64_t share = max((nt + splits - 1) / splits, int64_t(4));
-    it.k_lo = min(it.k_hi, split * share * kKeys);
-    it.k_hi = min(it.k_hi, (split + 1) * share * kKeys);
-  }
-  const int n_kt = static_cast<int>((it.k_hi - it.k_lo + kKeys - 1) / kKeys);
-  const int64_t n_rows = it.n_tok * a.G;
 
   auto wait = [&](uint64_t* br, uint32_t parity) -> bool {
     if (mbar_try_wait(br, parity)) return true;
@@ -195,55 +707,75 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 4) {
     // ---------------- producer: lane x loads box x of each stage ----------------
-    const int bx = a.box_rows;  // divides page_size and 64
-    const int boxes = kKeys / bx * (D / 64);
-    uint32_t n_it = 0;
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const int bx = a.box_rows;  // divides page_size and the stage's keys
+    const int r = lane / (D / 64) * bx, half = lane % (D / 64);
+    const bool mine = r < KS;
+    const uint32_t off = half * kHalf + r * 128;
+    Walk<KS, MT> wk;
+    wk.init(a, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x),
+            static_cast<uint32_t>(a.least));
+    uint32_t n_it = 0, n_pc = 0;
     bool ok = true;
-    uint32_t n_rt = 0;
-    for (int64_t rt = tile; ok && rt * MT < n_rows; rt += n_tiles, ++n_rt) {
-      if (MT == 16 && n_rt > 0)
-        ok = __all_sync(0xffffffffu, wait(joined, (n_rt - 1) & 1));
-      for (int j = 0; ok && j < n_kt; ++j, ++n_it) {
-        const int s = static_cast<int>(n_it % L::kStages);
-        const uint32_t ph = n_it / L::kStages;
-        if (ph > 0) ok = __all_sync(0xffffffffu, wait(empty + s, (ph - 1) & 1));
+    while (ok) {
+      Piece p;
+      const bool more = wk.next(a, &p);
+      if (!more) p.n_kt = -1;
+      const int ps = n_pc % kPieces;
+      if (n_pc >= kPieces) ok = __all_sync(0xffffffffu, wait(piece_empty + ps, (n_pc / kPieces - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) {
+        pieces[ps] = p;
+        mbar_arrive(piece_full + ps);
+      }
+      ++n_pc;
+      if (!more) break;
+      const int32_t* pages = p.own ? a.table + wk.b * a.table_stride : a.ptable;
+      for (int j = 0; j < p.n_kt; ++j, ++n_it) {
+        const int s = static_cast<int>(n_it % NS);
+        // A box past the keys, or of a page that does not exist, lies outside the tensor map
+        // and reads as zeros; nothing outside the caches is touched.
+        const int key = wk.k_lo + j * KS + r;
+        int page = -1, slot = 0;
+        if (mine && key < wk.k_hi) {
+          const uint32_t pg = static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size);
+          page = pages[pg];
+          slot = key - static_cast<int>(pg) * a.page_size;
+          if (page < 0 || page >= a.n_pages) {
+            page = -1;
+            atomicOr(a.err, kErrBadPage);
+          }
+        }
+        if (n_it >= NS) ok = __all_sync(0xffffffffu, wait(empty + s, (n_it / NS - 1) & 1));
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(full + s, L::kStage);
         __syncwarp();
-        const uint32_t base = smem_u32(smem) + s * L::kStage;
-        const int64_t k0 = it.k_lo + static_cast<int64_t>(j) * kKeys;
-        for (int x = lane; x < boxes; x += 32) {
-          const int r = x / (D / 64) * bx, half = x % (D / 64);
-          const int64_t key = k0 + r;
-          // A box past the keys, or of a page that does not exist, lies outside the tensor map
-          // and reads as zeros; nothing outside the caches is touched.
-          int page = -1, slot = 0;
-          if (key < it.k_hi) {
-            const int64_t pg = key / a.page_size;
-            page = pg < it.n_table ? it.pages[pg] : -1;
-            slot = static_cast<int>(key - pg * a.page_size);
-            if (page < 0 || page >= a.n_pages) {
-              page = -1;
-              atomicOr(a.err, kErrBadPage);
-            }
-          }
-          const uint32_t dst = base + half * (kKeys * 128) + r * 128;
-          tma_load_4d(dst, &tm_k, half * 64, slot, it.kvh, page, full + s);
-          tma_load_4d(dst + kKeys * D * 2, &tm_v, half * 64, slot, it.kvh, page, full + s);
+        if (mine) {
+          const uint32_t dst = smem_u32(smem) + s * L::kStage + off;
+          tma_load_4d(dst, &tm_k, half * 64, slot, p.kvh, page, full + s);
+          tma_load_4d(dst + kVoff, &tm_v, half * 64, slot, p.kvh, page, full + s);
         }
       }
     }
     if (!ok) {  // copies in flight land before the block's shared memory goes
-      for (uint32_t j = (n_it >= L::kStages ? n_it - L::kStages : 0); j < n_it; ++j)
-        mbar_wait(full + j % L::kStages, (j / L::kStages) & 1, 100000000ull);
+      for (uint32_t j = (n_it >= NS ? n_it - NS : 0); j < n_it; ++j)
+        mbar_wait(full + j % NS, (j / NS) & 1, 100000000ull);
     }
   } else {
     // ---------------- consumers ----------------
-    const int kw0 = MT == 16 ? warp * 16 : 0;
-    const int r_lo = lane >> 2;
+    {
+      // the tables, on their way to L2 while the producer reads the lengths
+      const uint32_t line = blockIdx.x * 128 + threadIdx.x;
+      const uint32_t per = static_cast<uint32_t>(min((a.max_pages + 31) / 32, int64_t(1) << 20));
+      const uint32_t b = line / per;
+      if (b < static_cast<uint32_t>(a.B))
+        prefetch_l2(a.table + b * a.table_stride + (line - b * per) * 32);
+    }
     const uint32_t sm0 = smem_u32(smem);
-    const bool sole = a.splits_p + a.splits_o == 1;
-    uint32_t n_it = 0, n_meet = 0;
+    uint32_t n_it = 0, n_meet = 0, n_pc = 0;
     bool ok = true;
     // Every consumer warp has come here, and sees what the others wrote; false on expiry.
     auto meet_all = [&]() -> bool {
@@ -251,34 +783,40 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(meet);
       return __all_sync(0xffffffffu, wait(meet, n_meet++ & 1));
     };
-    for (int64_t rt = tile; ok && rt * MT < n_rows; rt += n_tiles) {
-      // this thread's two rows: token, head and key limit
-      int64_t tok[2];
-      int head[2];
-      int64_t lim[2];
+    // Values past the piece's last key (slots of its last page that no token fills) may be
+    // anything, infinities and NaN among them, and 0 * inf is not 0: rows [r0, r0 + n) of the
+    // stage's V are cleared from row `valid` on.
+    auto clear_v = [&](uint32_t sv, int r0, int n, int valid) {
+      for (int x = lane; x < n * (D / 8); x += 32) {
+        const int r = r0 + x / (D / 8), ch = x % (D / 8);
+        if (r >= valid)
+          st_shared_v4(sv + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();  // before TMA may fill the stage again
+    };
+    while (ok) {
+      const int ps = n_pc % kPieces;
+      ok = __all_sync(0xffffffffu, wait(piece_full + ps, (n_pc / kPieces) & 1));
+      if (!ok) break;
+      const Piece p = pieces[ps];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(piece_empty + ps);
+      ++n_pc;
+      if (p.n_kt < 0) break;
+
+      const int r_lo = lane >> 2;
+      uint32_t qf[D / 16][4];
+      int lim[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t r = rt * MT + (MT == 16 ? 0 : warp * 16) + r_lo + 8 * e;
-        const int64_t i = r / a.G;
-        head[e] = it.kvh * a.G + static_cast<int>(r - i * a.G);
-        tok[e] = r < n_rows ? it.tok0 + i : -1;
-        lim[e] = r < n_rows ? row_limit(it, i) : it.k_lo;
-      }
-      uint32_t qf[D / 16][4];
-      {
-        const __nv_bfloat16* qp[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t t = tok[e];
-          const int64_t bb = a.cu ? 0 : t / a.T, ii = a.cu ? t : t - bb * a.T;
-          qp[e] = t < 0 ? nullptr : a.q + bb * a.q_b + ii * a.q_s + head[e] * a.q_h + (lane & 3) * 2;
-        }
+        const int r = warp * 16 + r_lo + 8 * e;
+        const __nv_bfloat16* qp = q_row(a, p, r);
+        lim[e] = row_limit(a, p, r);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            qf[k][e] = qp[e & 1] ? *reinterpret_cast<const uint32_t*>(qp[e & 1] + k * 16 + (e >> 1) * 8)
-                                 : 0u;
+          for (int f = 0; f < 2; ++f)
+            qf[k][e + 2 * f] = qp ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + f * 8 + (lane & 3) * 2) : 0u;
       }
       float o[D / 8][4];
 #pragma unroll
@@ -286,50 +824,39 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
       float m[2] = {-INFINITY, -INFINITY}, lb[2] = {0.f, 0.f}, lf[2] = {0.f, 0.f};
-
-      for (int j = 0; j < n_kt; ++j, ++n_it) {
-        const int s = static_cast<int>(n_it % L::kStages);
-        ok = __all_sync(0xffffffffu, wait(full + s, (n_it / L::kStages) & 1));
+      for (int j = 0; j < p.n_kt; ++j, ++n_it) {
+        const int s = static_cast<int>(n_it % NS);
+        ok = __all_sync(0xffffffffu, wait(full + s, (n_it / NS) & 1));
         if (!ok) break;
-        const uint32_t sk = sm0 + s * L::kStage, sv = sk + kKeys * D * 2;
-        const int64_t k0 = it.k_lo + static_cast<int64_t>(j) * kKeys;
-        // Values past the range's last key (slots of its last page that no token fills) may be
-        // anything, infinities and NaN among them, and 0 * inf is not 0: they are cleared.
-        if (k0 + kKeys > it.k_hi) {
-          const int valid = static_cast<int>(it.k_hi - k0);
-          for (int x = lane; x < 16 * (D / 8); x += 32) {
-            const int r = warp * 16 + x / (D / 8), ch = x % (D / 8);
-            if (r >= valid)
-              st_shared_v4(sv + (ch >> 3) * (kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                           0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();  // before TMA may fill the stage again
-          if (MT == 16) __syncwarp();
-          else ok = meet_all();
+        const uint32_t sk = sm0 + s * L::kStage, sv = sk + kVoff;
+        const int k0 = j * KS;
+        if (k0 + KS > p.keys) {
+          clear_v(sv, warp * 16, 16, p.keys - k0);
+          ok = meet_all();
           if (!ok) break;
         }
-        float sc[KW / 8][4];
+        float sc[KS / 8][4];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
+        for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int ch = (k & 3) * 2 + ((lane >> 3) & 1);
 #pragma unroll
-          for (int kg = 0; kg < KW / 16; ++kg) {
-            const int r = kw0 + kg * 16 + ((lane >> 4) << 3) + (lane & 7);
+          for (int kg = 0; kg < KS / 16; ++kg) {
+            const int r = kg * 16 + ((lane >> 4) << 3) + (lane & 7);
             uint32_t kb[4];
-            ldsm4(kb, sk + (k >> 2) * (kKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4));
+            ldsm4(kb, sk + (k >> 2) * (kHalf) + r * 128 + ((ch ^ (r & 7)) << 4));
             mma16816(sc[2 * kg], qf[k], kb[0], kb[1]);
             mma16816(sc[2 * kg + 1], qf[k], kb[2], kb[3]);
           }
         }
         // scale, mask, running maximum
-        const int64_t kb0 = k0 + kw0 + (lane & 3) * 2;
+        const int kb0 = k0 + (lane & 3) * 2;
         float mx[2] = {m[0], m[1]};
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
+        for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool seen = kb0 + n * 8 + (e & 1) < lim[e >> 1];
@@ -357,9 +884,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         // weights, rounded to bf16 once for the product
-        uint32_t pf[KW / 16][4];
+        uint32_t pf[KS / 16][4];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n) {
+        for (int n = 0; n < KS / 8; ++n) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float p0 = ex2_approx(sc[n][2 * e] - base[e]);
@@ -373,13 +900,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
 #pragma unroll
-        for (int kg = 0; kg < KW / 16; ++kg)
+        for (int kg = 0; kg < KS / 16; ++kg)
 #pragma unroll
           for (int dp = 0; dp < D / 16; ++dp) {
-            const int r = kw0 + kg * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
+            const int r = kg * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
             const int ch = (dp & 3) * 2 + (lane >> 4);
             uint32_t vb[4];
-            ldsm4_t(vb, sv + (dp >> 2) * (kKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4));
+            ldsm4_t(vb, sv + (dp >> 2) * (kHalf) + r * 128 + ((ch ^ (r & 7)) << 4));
             mma16816(o[2 * dp], pf[kg], vb[0], vb[1]);
             mma16816(o[2 * dp + 1], pf[kg], vb[2], vb[3]);
           }
@@ -393,143 +920,92 @@ __global__ void __launch_bounds__(kThreads, 2)
         lb[e] += __shfl_xor_sync(0xffffffffu, lb[e], 2);
         lf[e] += __shfl_xor_sync(0xffffffffu, lf[e], 1);
         lf[e] += __shfl_xor_sync(0xffffffffu, lf[e], 2);
-      }
-      if (MT == 16) {
-        // join the four warps' key shares: statistics first, then the numerators
-        float4* ml = reinterpret_cast<float4*>(smem + L::kMl);
-        if ((lane & 3) == 0)
+        const int r = warp * 16 + r_lo + 8 * e;
+        if (p.row0 + r >= p.n_rows) continue;
+        const RowOut w = row_out(a, p, r, MT, D, (lane & 3) == 0);
+        if (w.o) {
+          const float inv = lb[e] == 0.f ? 0.f : 1.f / lb[e];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            ml[warp * 16 + r_lo + 8 * e] = make_float4(m[e], lb[e], lf[e], 0.f);
-        ok = meet_all();
-        if (!ok) break;
-        float w[2];
-        float4 all[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r_lo + 8 * e;
-          float M = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) M = fmaxf(M, ml[u * 16 + r].x);
-          const float bs = M == -INFINITY ? 0.f : M;
-          all[e] = make_float4(M, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float4 v = ml[u * 16 + r];
-            const float f = ex2_approx(v.x - bs);
-            all[e].y += f * v.y;
-            all[e].z += f * v.z;
-          }
-          w[e] = ex2_approx(m[e] - bs);
-        }
-        // Numerators go through the stages' memory: every copy of this row tile has landed and
-        // been read. Row r of warp u at ((u * 16 + r) * (D + 4)) floats.
-        float* ob = reinterpret_cast<float*>(smem);
-        constexpr int kPitch = D + 4;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float2*>(ob + (warp * 16 + r_lo + 8 * e) * kPitch + n * 8 +
-                                       (lane & 3) * 2) =
-                make_float2(o[n][2 * e] * w[e], o[n][2 * e + 1] * w[e]);
-        ok = meet_all();
-        if (!ok) break;
-        // warp u finishes rows 4u .. 4u+3, a lane D/32 features each
-        for (int q = 0; q < 4; ++q) {
-          const int r = warp * 4 + q;
-          const int64_t row = rt * 16 + r;
-          if (row >= n_rows) break;
-          float v[D / 32];
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            const int d = lane * (D / 32) + x;
-            v[x] = (ob[r * kPitch + d] + ob[(16 + r) * kPitch + d]) +
-                   (ob[(32 + r) * kPitch + d] + ob[(48 + r) * kPitch + d]);
-          }
-          const int src = (r & 7) * 4;
-          float4 st;
-          st.x = __shfl_sync(0xffffffffu, r < 8 ? all[0].x : all[1].x, src);
-          st.y = __shfl_sync(0xffffffffu, r < 8 ? all[0].y : all[1].y, src);
-          st.z = __shfl_sync(0xffffffffu, r < 8 ? all[0].z : all[1].z, src);
-          const int64_t i = row / a.G;
-          const int h = it.kvh * a.G + static_cast<int>(row - i * a.G);
-          const int64_t t = it.tok0 + i;
-          if (sole) {
-            const int64_t bb = a.cu ? 0 : t / a.T, ii = a.cu ? t : t - bb * a.T;
-            const float inv = st.y == 0.f ? 0.f : 1.f / st.y;
-            __nv_bfloat16* op = a.o + bb * a.o_b + ii * a.o_s + h * a.o_h + lane * (D / 32);
-#pragma unroll
-            for (int x = 0; x < D / 32; x += 2)
-              *reinterpret_cast<uint32_t*>(op + x) = pack_bf16(v[x] * inv, v[x + 1] * inv);
-            if (a.lse && lane == 0) {
-              const int64_t at = a.cu ? h * a.rows + t : (bb * a.Hq + h) * a.T + ii;
-              a.lse[at] = (st.x + log2f(st.z)) * 0.69314718055994530942f;
-            }
-          } else {
-            const int64_t at = (static_cast<int64_t>(it.part) * a.rows + t) * a.Hq + h;
-            if (st.z != 0.f) {  // NaN goes through
-              float* op = a.part_o + at * D + lane * (D / 32);
-#pragma unroll
-              for (int x = 0; x < D / 32; x += 2)
-                *reinterpret_cast<float2*>(op + x) = make_float2(v[x], v[x + 1]);
-            }
-            if (lane == 0) a.part_ml[at] = st;
-          }
-        }
-        // the next row tile's copies (async proxy) may overwrite ob (generic proxy)
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(joined);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (tok[e] < 0) continue;
-          const int64_t t = tok[e];
-          if (sole) {
-            const int64_t bb = a.cu ? 0 : t / a.T, ii = a.cu ? t : t - bb * a.T;
-            const float inv = lb[e] == 0.f ? 0.f : 1.f / lb[e];
-            __nv_bfloat16* op = a.o + bb * a.o_b + ii * a.o_s + head[e] * a.o_h + (lane & 3) * 2;
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<uint32_t*>(w.o + n * 8 + (lane & 3) * 2) =
+                pack_bf16(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+          if (w.lse && (lane & 3) == 0) *w.lse = (m[e] + log2f(lf[e])) * 0.69314718055994530942f;
+        } else if (w.part) {
+          if (lf[e] != 0.f) {  // NaN goes through
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<uint32_t*>(op + n * 8) =
-                  pack_bf16(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-            if (a.lse && (lane & 3) == 0) {
-              const int64_t at = a.cu ? head[e] * a.rows + t : (bb * a.Hq + head[e]) * a.T + ii;
-              a.lse[at] = (m[e] + log2f(lf[e])) * 0.69314718055994530942f;
-            }
-          } else {
-            const int64_t at = (static_cast<int64_t>(it.part) * a.rows + t) * a.Hq + head[e];
-            if (lf[e] != 0.f) {
-              float* op = a.part_o + at * D + (lane & 3) * 2;
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2*>(op + n * 8) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
-            }
-            if ((lane & 3) == 0) a.part_ml[at] = make_float4(m[e], lb[e], lf[e], 0.f);
+              *reinterpret_cast<float2*>(w.part + n * 8 + (lane & 3) * 2) =
+                  make_float2(o[n][2 * e], o[n][2 * e + 1]);
           }
+          if ((lane & 3) == 0) *w.ml = make_float4(m[e], lb[e], lf[e], 0.f);
         }
       }
     }
   }
+  // the prefix kernel that this one may have started beside is done before this one is, so that
+  // what follows this one follows both
+  grid_dependency_wait();
 }
 
-// Joins the parts of a row: one warp per (row, head), parts in order.
-template <int D>
+// Joins the parts of a row: kWarps warps per (row, head), warp u taking the parts u, u + kWarps,
+// ... of each 32; up to eight numerators are in flight per warp. The order of the sums is fixed.
+// A row's parts are the prefix kernel's, then the pieces that desc names for the prefix and for
+// its own keys. Bound: latency (a few dependent loads) for few rows, L2 for many.
+template <int D, int kWarps>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t x = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
-  const int64_t t = x / a.Hq;
+  constexpr int kRows = 8 / kWarps;  // rows per block
+  constexpr int kQ = 32 / kWarps < 8 ? 32 / kWarps : 8;  // parts in flight per warp
+  __shared__ float red[kWarps > 1 ? 8 : 1][D + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = warp % kWarps;
+  const int64_t x = blockIdx.x * int64_t(kRows) + warp / kWarps;
+  const int64_t t = div_fl(x, a.Hq);
   const int h = static_cast<int>(x - t * a.Hq);
-  if (t >= a.rows) return;
-  if (a.cu && (t >= a.cu[a.B] || t < a.cu[0])) return;  // rows of no sequence stay as they are
-  const int parts = a.splits_p + a.splits_o;
+  bool live = t < a.rows;
+  if (live && a.cu) live = t < a.cu[a.B] && t >= a.cu[0];  // rows of no sequence stay as they are
+  grid_dependency_wait();
   const int64_t step = a.rows * a.Hq;
   const int64_t at = t * a.Hq + h;
+  int n_x = 0, n_p = 0, n_o = 0;
+  int64_t first_p = 0, first_o = 0;
+  if (live) {
+    const int2 own = a.desc[step + at];
+    first_o = own.x;
+    n_o = own.y;
+    if (a.splits_x) {
+      n_x = a.splits_p;
+    } else if (a.prefix) {
+      const int2 pre = a.desc[at];
+      first_p = pre.x;
+      n_p = pre.y;
+    }
+    live = n_o != 0;  // finished by the kernel before
+    // stay inside the slots whatever desc holds (cu_rows that decrease)
+    const int64_t top = a.n_slots * a.mt;
+    if (first_o < 0 || n_o < 0 || first_o + (n_o - int64_t(1)) * a.mt >= top) n_o = 0;
+    if (first_p < 0 || n_p < 0 || first_p + (n_p - int64_t(1)) * a.mt >= top) n_p = 0;
+  }
+  if (kWarps == 1 && !live) return;
+  const int parts = live ? n_x + n_p + n_o : 0;
+  // row of statistics and numerators of part p
+  auto where = [&](int p, const float4** ml, const float** o) {
+    if (p < n_x) {
+      *ml = a.part_ml + p * step + at;
+      *o = a.part_o + (p * step + at) * D;
+    } else {
+      const int64_t s = p < n_x + n_p ? first_p + static_cast<int64_t>(p - n_x) * a.mt
+                                      : first_o + static_cast<int64_t>(p - n_x - n_p) * a.mt;
+      *ml = a.slot_ml + s;
+      *o = a.slot_o + s * D;
+    }
+  };
   float M = -INFINITY;
   for (int p = lane; p < parts; p += 32) {
-    const float4 v = a.part_ml[p * step + at];
+    const float4* ml;
+    const float* o;
+    where(p, &ml, &o);
+    const float4 v = *ml;
     if (v.z != 0.f) M = fmaxf(M, v.x);
   }
 #pragma unroll
@@ -538,60 +1014,124 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   float lb = 0.f, lf = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const float4 v = a.part_ml[p * step + at];
-    if (v.z == 0.f) continue;
-    const float w = ex2_approx(v.x - M);
-    lb += w * v.y;
-    lf += w * v.z;
-    const float* op = a.part_o + (p * step + at) * D + lane * E;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    // lane p: the weight of part p0 + p; a part without keys (sum exactly 0) has written no
+    // numerator and is passed over, one with NaN is not
+    float w = -1.f;
+    if (p0 + lane < parts) {
+      const float4* ml;
+      const float* o;
+      where(p0 + lane, &ml, &o);
+      const float4 v = *ml;
+      if (v.z != 0.f) {
+        w = ex2_approx(v.x - M);
+        if (lane % kWarps == u) {
+          lb += w * v.y;
+          lf += w * v.z;
+        }
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * op[e];
+    for (int q0 = 0; q0 < 32; q0 += kQ * kWarps) {
+      float r[kQ][E], wq[kQ];
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int p = q0 + q * kWarps + u;
+        wq[q] = __shfl_sync(0xffffffffu, w, p);
+        if (wq[q] >= 0.f || wq[q] != wq[q]) {
+          const float4* ml;
+          const float* o;
+          where(p0 + p, &ml, &o);
+          if (E == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(o + lane * E);
+            r[q][0] = f.x; r[q][1] = f.y; r[q][E - 2] = f.z; r[q][E - 1] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(o + lane * E);
+            r[q][0] = f.x; r[q][1] = f.y;
+          }
+        } else {
+          wq[q] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) r[q][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wq[q] * r[q][e];
+      if (p0 + q0 + kQ * kWarps >= parts) break;
+    }
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) {
+    lb += __shfl_xor_sync(0xffffffffu, lb, s);
+    lf += __shfl_xor_sync(0xffffffffu, lf, s);
+  }
+  if (kWarps > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[warp % 8][lane * E + e] = acc[e];
+    if (lane == 0) {
+      red[warp % 8][D] = lb;
+      red[warp % 8][D + 1] = lf;
+    }
+    __syncthreads();
+    if (u != 0 || !live) return;
+    lb = lf = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += red[(warp + v) % 8][lane * E + e];
+      lb += red[(warp + v) % 8][D];
+      lf += red[(warp + v) % 8][D + 1];
+    }
   }
   const float inv = lb == 0.f ? 0.f : 1.f / lb;  // no key in sight: zeros
   const int64_t bb = a.cu ? 0 : t / a.T, ii = a.cu ? t : t - bb * a.T;
   __nv_bfloat16* op = a.o + bb * a.o_b + ii * a.o_s + h * a.o_h + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (E == 4)
+    *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                               pack_bf16(acc[E - 2] * inv, acc[E - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(op) = pack_bf16(acc[0] * inv, acc[1] * inv);
   if (a.lse && lane == 0) {
     const int64_t li = a.cu ? h * a.rows + t : (bb * a.Hq + h) * a.T + ii;
     a.lse[li] = (M + log2f(lf)) * 0.69314718055994530942f;
   }
 }
 
-template <int D, int MT>
-cudaError_t launch_one(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
-                       cudaStream_t stream) {
-  using L = PLayout<D, MT>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&attn_paged_kernel<D, MT>),
-                                   L::kBytes);
+template <int D, int NR>
+cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
+                          cudaStream_t stream) {
+  using L = DLayout<D, NR>;
+  const cudaError_t e = ensure_smem_attr(
+      reinterpret_cast<const void*>(&paged_decode_kernel<D, NR>), L::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t n = static_cast<int64_t>(a.Hkv) *
-                    ((a.splits_x ? 0 : static_cast<int64_t>(a.splits_p) * a.tiles_p) +
-                     static_cast<int64_t>(a.splits_o) * a.tiles_o * a.B);
-  if (n > 0x7fffffff) return cudaErrorInvalidValue;
-  launch_begin(13, stream);
-  attn_paged_kernel<D, MT><<<static_cast<unsigned>(n), kThreads, L::kBytes, stream>>>(km, vm, a);
-  e = cudaGetLastError();
-  launch_end(13, stream);
-  return e;
+  // beside the prefix kernel, if there is one
+  return launch_after(paged_decode_kernel<D, NR>, dim3(a.grid), dim3(kWarps * 32), L::kBytes,
+                      stream, a.splits_x != 0, km, vm, a);
 }
 
-}  // namespace
+template <int D>
+cudaError_t launch_rows(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
+                        cudaStream_t stream) {
+  using L = PLayout<D>;
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(&paged_rows_kernel<D>), L::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(paged_rows_kernel<D>, dim3(a.grid), dim3(kThreads), L::kBytes, stream,
+                      a.splits_x != 0, km, vm, a);
+}
 
-namespace {
 // Rows beyond which the prefix goes to the tensor-core kernel with 128-row tiles.
 bool prefix_on_tc(const PagedArgs& a) { return a.prefix >= 128 && a.rows * a.G > 16; }
-bool small_tiles(const PagedArgs& a, int64_t max_q) {
-  return max_q * a.G <= 16 && (a.prefix == 0 || a.splits_x || a.rows * a.G <= 16);
-}
+
 }  // namespace
 
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   const int64_t rows_o = max_q * a->G, rows_p = a->rows * a->G;
-  constexpr int kSms = 152;
-  a->splits_x = 0;
+  a->splits_x = a->splits_p = a->tiles_p = 0;
   if (prefix_on_tc(*a)) {
     // One CTA per SM: waves of items, each as long as its share of key tiles and about four
     // tiles' time of start and end. The fewest splits of the shortest time.
@@ -611,39 +1151,53 @@ void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
     }
     a->splits_p = a->splits_x * (pair ? 1 : 2);
   }
-  const int MT = small_tiles(*a, max_q) ? 16 : 64;
-  a->tiles_o = static_cast<int>((rows_o + MT - 1) / MT);
-  const int64_t slots = 4 * kSms;  // two blocks on each SM, twice over
-  auto splits = [&](int64_t items, int64_t keys) -> int {
-    const int64_t nt = (keys + 255) / 256;
-    int64_t s = (slots + items - 1) / items;
-    if (s > nt) s = nt;
-    return static_cast<int>(s < 1 ? 1 : s);
-  };
-  if (!a->splits_x) {
-    a->tiles_p = static_cast<int>((rows_p + MT - 1) / MT);
-    a->splits_p = a->prefix ? splits(static_cast<int64_t>(a->tiles_p) * a->Hkv, a->prefix) : 0;
-  }
-  a->splits_o = splits(static_cast<int64_t>(a->tiles_o) * a->Hkv * a->B, max_len);
+  const int64_t most = a->prefix && !a->splits_x ? rows_p : rows_o;
+  a->mt = most <= 8 ? 8 : most <= 16 ? 16 : 64;
+  // segments: every sequence's rows fill whole tiles and one that is not full
+  const int64_t segs = (rows_p / a->mt + a->B) * a->Hkv;
+  const int64_t segs_p = a->prefix && !a->splits_x ? (rows_p + a->mt - 1) / a->mt * a->Hkv : 0;
+  // Workers: eight warps on each SM, or two blocks; fewer where there are fewer shares. A share is
+  // at least 64 keys of a decode step: shorter ones cost more in the join than they save.
+  const bool warps = a->mt != 64;
+  const int ks = a->ks = warps ? 2048 / a->D : 64;
+  a->least = warps ? 64 / ks : 1;
+  const int64_t tiles = segs * ((max_len + ks - 1) / ks) + segs_p * ((a->prefix + ks - 1) / ks);
+  const int64_t want = (tiles + a->least - 1) / a->least, most_blocks = warps ? kSms : 2 * kSms;
+  a->grid = static_cast<unsigned>(want < most_blocks ? want : most_blocks);
+  a->n_slots = segs + segs_p + static_cast<int64_t>(a->grid) * (warps ? kWarps : 1);
 }
 
 cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
-                              const CUtensorMap& v_map, int64_t max_q, cudaStream_t stream) {
-  const bool small = small_tiles(a, max_q);
+                              const CUtensorMap& v_map, cudaStream_t stream) {
+  launch_begin(13, stream);
+  cudaError_t e;
   if (a.D == 128)
-    return small ? launch_one<128, 16>(a, k_map, v_map, stream)
-                 : launch_one<128, 64>(a, k_map, v_map, stream);
-  return small ? launch_one<64, 16>(a, k_map, v_map, stream)
-               : launch_one<64, 64>(a, k_map, v_map, stream);
+    e = a.mt == 8    ? launch_decode<128, 1>(a, k_map, v_map, stream)
+        : a.mt == 16 ? launch_decode<128, 2>(a, k_map, v_map, stream)
+                     : launch_rows<128>(a, k_map, v_map, stream);
+  else
+    e = a.mt == 8    ? launch_decode<64, 1>(a, k_map, v_map, stream)
+        : a.mt == 16 ? launch_decode<64, 2>(a, k_map, v_map, stream)
+                     : launch_rows<64>(a, k_map, v_map, stream);
+  launch_end(13, stream);
+  return e;
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (a.rows * a.Hq + 7) / 8;
+  // Eight warps a row where rows alone would leave most of the GPU's warps idle.
+  const int64_t rows = a.rows * a.Hq;
+  const bool wide = rows < 1024;
+  const int64_t blocks = wide ? rows : (rows + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 n(static_cast<unsigned>(blocks)), th(256);
   launch_begin(14, stream);
-  if (a.D == 128) paged_merge_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  else paged_merge_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (a.D == 128)
+    e = wide ? launch_after(paged_merge_kernel<128, 8>, n, th, 0, stream, true, a)
+             : launch_after(paged_merge_kernel<128, 1>, n, th, 0, stream, true, a);
+  else
+    e = wide ? launch_after(paged_merge_kernel<64, 8>, n, th, 0, stream, true, a)
+             : launch_after(paged_merge_kernel<64, 1>, n, th, 0, stream, true, a);
   launch_end(14, stream);
   return e;
 }

@@ -42,15 +42,6 @@ struct XLayout {
   static constexpr int kBytes = kAbort + 4 + 1024;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y,
-                                            int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 template <int D, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -73,6 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
 
   // kv-heads of one key range are neighbours (they read neighbouring bytes of the same pages),
   // then row blocks (the same bytes, from L2), then key ranges.
@@ -418,10 +410,10 @@ cudaError_t launch_one(const PagedArgs& a, const CUtensorMap& km, const CUtensor
   if (e != cudaSuccess) return e;
   const int64_t n = static_cast<int64_t>(a.Hkv) * a.tiles_p * a.splits_x;
   if (n > 0x7fffffff) return cudaErrorInvalidValue;
-  launch_begin(13, stream);
+  launch_begin(15, stream);
   attn_prefix_kernel<D, kPair><<<static_cast<unsigned>(n), kThreads, L::kBytes, stream>>>(km, vm, a);
   e = cudaGetLastError();
-  launch_end(13, stream);
+  launch_end(15, stream);
   return e;
 }
 

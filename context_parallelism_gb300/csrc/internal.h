@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include <cstdio>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -66,6 +67,24 @@ int make_attn_plan(int B, int64_t S, int Hq, int Hkv, int D, int causal, int hea
 // (kernel, device): the attribute is per device, so a process that drives several GPUs sets it
 // on each. Thread-safe.
 cudaError_t ensure_smem_attr(const void* kernel, int bytes);
+
+// Launches a kernel; with `early` it may start while the kernel before it in the stream still
+// runs (programmatic dependent launch: the kernel waits for that one itself).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream, bool early, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // Restores the caller's current device when the scope ends (the entry points select the
 // device their tensors live on, and must not leave it changed).
@@ -335,26 +354,38 @@ struct PagedArgs {
   const int32_t* cu;         // [B + 1] or NULL
   const int32_t* table;      // [B][table_stride]
   int64_t table_stride, max_pages, n_pages;
+  int cap;                   // keys that a row of the table holds, at most 2^31 - 64
   const int32_t* seq_len;    // [B]
   const int32_t* ptable;     // [ceil(prefix / page_size)]
   int64_t prefix;
-  int B, Hq, Hkv, G, D, page_size, box_rows;
+  int B, Hq, Hkv, G, D, page_size;
+  int box_rows;              // rows of the tensor maps' boxes: divides page_size and the stage
   float scale_log2;
-  // partial results, one per (part, row, head): the numerator [D] fp32 and (max in log2 units,
-  // sum of the rounded weights, sum of the weights, 0). Parts [0, splits_p) cover the prefix,
-  // the others the sequence's own pages. With one part the kernels write o and lse themselves.
+  // Prefix parts of launch_attn_prefix, one per (part, row, head): the numerator [D] fp32 and
+  // (max in log2 units, sum of the rounded weights, sum of the weights, 0).
   float* part_o;
   float4* part_ml;
-  int splits_p, splits_o;    // parts of the prefix (0: none), key splits of the own pages
   int splits_x;              // key splits of launch_attn_prefix; 0: attn_paged_kernel takes the
-                             // prefix too, in splits_p splits
-  int tiles_p, tiles_o;      // row tiles of the prefix items, and of each sequence's items
+                             // prefix too
+  int splits_p;              // parts that these give each row
+  int tiles_p;               // its row tiles
+  // Pieces of attn_paged_kernel: slot s holds mt rows of numerators and statistics; desc[0] and
+  // desc[1], [rows][Hq] each, name a row's first slot row and number of pieces (0: the row is
+  // finished), for the prefix and for its own keys.
+  float* slot_o;
+  float4* slot_ml;
+  int2* desc;
+  int64_t n_slots;
+  int mt;                    // rows per tile: 8, 16 or 64
+  int ks;                    // keys per tile
+  int least;                 // tiles of the smallest share
+  unsigned grid;
   uint32_t* err;
 };
-// Plan of one call (host arithmetic): fills splits and tiles from the sizes and hints.
+// Plan of one call (host arithmetic): tiles, splits and slots from the sizes and the hints.
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len);
 cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
-                              const CUtensorMap& v_map, int64_t max_q, cudaStream_t stream);
+                              const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_attn_prefix(const PagedArgs& a, const CUtensorMap& k_map,
                                const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);

@@ -189,9 +189,14 @@ int gcd(int x, int y) {
   return x;
 }
 
+// Byte offsets of an attention call's workspace, each 256-byte aligned.
+struct PagedPlan {
+  size_t px_o, px_ml, slot_o, slot_ml, desc, total;
+};
+
 // Shape checks and plan of an attention call (no device access).
 int attn_plan(int B, int64_t rows, int Hq, int Hkv, int D, int64_t prefix_len, int64_t max_q,
-              int64_t max_len, PagedArgs* a, size_t* ml_at, size_t* bytes) {
+              int64_t max_len, PagedArgs* a, PagedPlan* p) {
   if (B < 1 || rows < 1 || Hq < 1 || Hkv < 1 || D < 1 || prefix_len < 0 || max_q < 1 ||
       max_len < 1)
     return pfail(UPIPE_ERR_INVALID_ARG,
@@ -212,23 +217,25 @@ int attn_plan(int B, int64_t rows, int Hq, int Hkv, int D, int64_t prefix_len, i
   a->G = Hq / Hkv;
   a->D = D;
   a->prefix = prefix_len;
-  if (max_q > rows) max_q = rows;
-  plan_paged(a, max_q, max_len);
-  const int64_t items = static_cast<int64_t>(Hkv) *
-                        (static_cast<int64_t>(a->splits_x ? a->splits_x : a->splits_p) *
-                             a->tiles_p +
-                         static_cast<int64_t>(a->splits_o) * a->tiles_o * B);
-  if (items > 0x7fffffff)
-    return pfail(UPIPE_ERR_UNSUPPORTED, "too many row tiles: give max_q");
-  const size_t parts = static_cast<size_t>(a->splits_p) + a->splits_o;
-  if (parts == 1) {
-    *ml_at = 0;
-    *bytes = 256;
-  } else {
-    const size_t n = parts * static_cast<size_t>(rows) * Hq;
-    *ml_at = al256(n * D * 4);
-    *bytes = *ml_at + al256(n * 16);
-  }
+  plan_paged(a, max_q < rows ? max_q : rows, max_len);
+  if (a->n_slots * a->mt > 0x7fffffff ||
+      static_cast<int64_t>(a->Hkv) * a->tiles_p * a->splits_x > 0x7fffffff)
+    return pfail(UPIPE_ERR_UNSUPPORTED, "B=%d rows=%lld Hq=%d: too many row tiles", B,
+                 (long long)rows, Hq);
+  const size_t px = static_cast<size_t>(a->splits_p) * rows * Hq;
+  const size_t sl = static_cast<size_t>(a->n_slots) * a->mt;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += al256(bytes);
+    return at;
+  };
+  p->px_o = take(px * D * 4);
+  p->px_ml = take(px * 16);
+  p->slot_o = take(sl * D * 4);
+  p->slot_ml = take(sl * 16);
+  p->desc = take(2 * static_cast<size_t>(rows) * Hq * 8);
+  p->total = off;
   return UPIPE_OK;
 }
 
@@ -389,10 +396,8 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
 size_t upipe_attn_paged_workspace_bytes(int B, int64_t rows, int Hq, int Hkv, int D,
                                         int64_t prefix_len, int64_t max_q, int64_t max_len) {
   PagedArgs a{};
-  size_t ml = 0, bytes = 0;
-  return attn_plan(B, rows, Hq, Hkv, D, prefix_len, max_q, max_len, &a, &ml, &bytes) == UPIPE_OK
-             ? bytes
-             : 0;
+  PagedPlan p{};
+  return attn_plan(B, rows, Hq, Hkv, D, prefix_len, max_q, max_len, &a, &p) == UPIPE_OK ? p.total : 0;
 }
 
 int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
@@ -421,9 +426,9 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   PagedArgs a{};
   const int64_t rows = cu_rows ? S : static_cast<int64_t>(B) * S;
   if (!cu_rows) max_q = S;
-  size_t ml_at = 0, need = 0;
-  st = attn_plan(B, rows, q->heads, cache->heads, cache->D, prefix_len, max_q, max_len, &a, &ml_at,
-                 &need);
+  PagedPlan plan{};
+  st = attn_plan(B, rows, q->heads, cache->heads, cache->D, prefix_len, max_q, max_len, &a,
+                 &plan);
   if (st != UPIPE_OK) return st;
   const int D = cache->D;
   const int64_t vb = cu_rows ? 1 : B;
@@ -436,8 +441,9 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   if (st == UPIPE_OK && prefix_len) st = p.add(prefix_table, "prefix_table", 4);
   if (st == UPIPE_OK) st = p.add(workspace, "workspace", 256);
   if (st != UPIPE_OK) return st;
-  if (workspace_bytes < need)
-    return pfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (workspace_bytes < plan.total)
+    return pfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes,
+                 plan.total);
   st = p.resolve();
   if (st != UPIPE_OK) return st;
   a.q = static_cast<const __nv_bfloat16*>(q->data);
@@ -455,28 +461,43 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   a.table_stride = table_stride;
   a.max_pages = max_pages;
   a.n_pages = cache->n_pages;
+  const int64_t cap_most = 0x7fffffff - 63;
+  a.cap = static_cast<int>(max_pages > cap_most / cache->page_size
+                               ? cap_most
+                               : max_pages * cache->page_size);
   a.seq_len = seq_len;
   a.ptable = prefix_table;
   a.page_size = cache->page_size;
-  a.box_rows = gcd(cache->page_size, 64);
   a.scale_log2 = 1.0f / std::sqrt(static_cast<float>(D)) * 1.4426950408889634f;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + ml_at);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(ws + plan.px_o);
+  a.part_ml = reinterpret_cast<float4*>(ws + plan.px_ml);
+  a.slot_o = reinterpret_cast<float*>(ws + plan.slot_o);
+  a.slot_ml = reinterpret_cast<float4*>(ws + plan.slot_ml);
+  a.desc = reinterpret_cast<int2*>(ws + plan.desc);
   const DeviceGuard dguard;
   PAGED_CUDA(cudaSetDevice(p.dev));
   st = device_status_word(p.dev, &a.err);
   if (st != UPIPE_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  auto maps = [&](CUtensorMap* km, CUtensorMap* vm, int box_rows) -> cudaError_t {
+    cudaError_t e = make_tmap_pages(km, cache->k, D, cache->page_size, cache->heads,
+                                    cache->n_pages, cache->stride_slot, cache->stride_head,
+                                    cache->stride_page, box_rows);
+    if (e != cudaSuccess) return e;
+    return make_tmap_pages(vm, cache->v, D, cache->page_size, cache->heads, cache->n_pages,
+                           cache->stride_slot, cache->stride_head, cache->stride_page, box_rows);
+  };
   CUtensorMap km, vm;
-  PAGED_CUDA(make_tmap_pages(&km, cache->k, D, cache->page_size, cache->heads, cache->n_pages,
-                             cache->stride_slot, cache->stride_head, cache->stride_page,
-                             a.box_rows));
-  PAGED_CUDA(make_tmap_pages(&vm, cache->v, D, cache->page_size, cache->heads, cache->n_pages,
-                             cache->stride_slot, cache->stride_head, cache->stride_page,
-                             a.box_rows));
-  if (a.splits_x) PAGED_CUDA(launch_attn_prefix(a, km, vm, stream));
-  PAGED_CUDA(launch_attn_paged(a, km, vm, max_q < rows ? max_q : rows, stream));
-  if (a.splits_p + a.splits_o > 1) PAGED_CUDA(launch_paged_merge(a, stream));
+  if (a.splits_x) {
+    a.box_rows = gcd(cache->page_size, 128);
+    PAGED_CUDA(maps(&km, &vm, a.box_rows));
+    PAGED_CUDA(launch_attn_prefix(a, km, vm, stream));
+  }
+  a.box_rows = gcd(cache->page_size, a.ks);
+  PAGED_CUDA(maps(&km, &vm, a.box_rows));
+  PAGED_CUDA(launch_attn_paged(a, km, vm, stream));
+  PAGED_CUDA(launch_paged_merge(a, stream));
   return UPIPE_OK;
 }
 

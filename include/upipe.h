@@ -399,8 +399,9 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
  * sequence's own keys 0 .. j. lse (device float32, [B][Hq][S], or [Hq][S] for a packed batch;
  * or NULL) = ln sum exp(scores). A row that sees no key gets o = 0 and lse = -inf. What slots
  * outside prefix_len and seq_len hold does not matter, NaN included.
- *   max_q (packed batches: new tokens of the longest sequence) and max_len (largest seq_len)
- *   only choose tiles and key splits; any value >= 1 gives right results.
+ *   max_q (new tokens of the longest sequence; S is taken in a padded batch) and max_len (the
+ *   largest seq_len) only choose the tile and the number of blocks; any value >= 1 gives right
+ *   results.
  *   workspace: device, 256-byte aligned, >= upipe_attn_paged_workspace_bytes(...) for the same
  *   sizes (rows = B * S, or S for a packed batch); contents on entry ignored, on exit undefined.
  *   Calls (and captured graphs) that may run at the same time need workspaces of their own.
@@ -436,9 +437,10 @@ enum {
                              staged key/value trunk (the copy time not hidden behind compute) */
   UPIPE_K_ROPE = 11,      /* rotary positions */
   UPIPE_K_KV_APPEND = 12, /* append to the paged cache */
-  UPIPE_K_ATTN_PAGED = 13, /* attention over the paged cache: one launch per kind of item */
+  UPIPE_K_ATTN_PAGED = 13, /* attention over the paged cache: own pages (and short prefixes) */
   UPIPE_K_PAGED_MERGE = 14, /* joins the parts of its rows */
-  UPIPE_K_COUNT = 15
+  UPIPE_K_ATTN_PREFIX = 15, /* the shared prefix on 128-row tensor-core tiles */
+  UPIPE_K_COUNT = 16
 };
 
 typedef struct {

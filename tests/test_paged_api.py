@@ -120,16 +120,21 @@ def test_workspace_zero_for_invalid(args):
     assert up.upipe_attn_paged_workspace_bytes(*args) == 0
 
 
-def test_workspace_grows_with_rows_only_by_parts():
-    """Whole parts of rows x Hq x (D + 4) floats, at most one part a split; 256 bytes for a call
-    whose every row is one part."""
+def test_workspace_is_bounded_by_the_rows_and_the_blocks():
+    """Pieces: a tile of rows each for every sequence's and kv-head's rows and every block, at
+    most 304; prefix parts: rows x Hq each, at most 160 splits of two. D + 4 floats a row, and
+    16 bytes a row and head for the descriptors. Nothing grows with the lengths beyond that."""
     for B, rows, Hq, Hkv, D, P, mq, ml in [(1, 1, 32, 8, 128, 0, 1, 131072),
                                            (64, 64, 32, 8, 128, 32768, 1, 1500),
-                                           (96, 240, 64, 8, 128, 131000, 5, 700)]:
+                                           (96, 240, 64, 8, 128, 131000, 5, 700),
+                                           (1, 1, 4, 4, 64, 0, 1, 1)]:
         ws = up.upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, P, mq, ml)
-        part = rows * Hq * (D + 4) * 4
-        assert ws >= 2 * part and ws < 700 * part
-    assert up.upipe_attn_paged_workspace_bytes(1, 1, 4, 4, 64, 0, 1, 200) == 256
+        mt = 64
+        segs = (rows * Hq // Hkv // mt + B + 1) * Hkv * (2 if P else 1)
+        most = ((segs + 304) * mt + (320 * rows * Hq if P else 0)) * (D + 4) * 4
+        assert 0 < ws <= most + 16 * rows * Hq + 5 * 256
+        assert up.upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, P, mq, 1 << 30) <= \
+            most + 16 * rows * Hq + 5 * 256
 
 
 def _t(*shape, dtype=torch.bfloat16):

@@ -42,7 +42,7 @@ struct XLayout {
   static constexpr int kBytes = kAbort + 4 + 1024;
 };
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
@@ -232,19 +232,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- Q, softmax ----------------
     {
-      constexpr int kChunks = D / 8;
-      for (int i = threadIdx.x; i < L::kQTiles * 128 * kChunks; i += 256) {
-        const int r = i / kChunks, c = i % kChunks;
-        const int64_t row = row0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < n_rows) {
-          const int64_t t = row / a.G;
-          const int h = kvh * a.G + static_cast<int>(row - t * a.G);
-          const int64_t bb = a.cu ? 0 : t / a.T, ii = a.cu ? t : t - bb * a.T;
-          v = *reinterpret_cast<const uint4*>(a.q + bb * a.q_b + ii * a.q_s + h * a.q_h + c * 8);
+      // a thread loads one 16-byte chunk of every kStep-th row, eight rows in flight
+      constexpr int kChunks = D / 8, kStep = 256 / kChunks, kRows = L::kQTiles * 128;
+      const int c = threadIdx.x % kChunks;
+      const uint32_t G = a.G, T = static_cast<uint32_t>(a.T);
+#pragma unroll 1
+      for (int r0 = threadIdx.x / kChunks; r0 < kRows; r0 += 8 * kStep) {
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int64_t row = row0 + r0 + u * kStep;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (r0 + u * kStep < kRows && row < n_rows) {
+            const uint32_t t = static_cast<uint32_t>(row) / G;
+            const int h = kvh * a.G + static_cast<int>(static_cast<uint32_t>(row) - t * G);
+            const uint32_t bb = a.cu ? 0 : T == 1 ? t : t / T, ii = a.cu ? t : t - bb * T;
+            v[u] = *reinterpret_cast<const uint4*>(a.q + bb * a.q_b + ii * a.q_s + h * a.q_h + c * 8);
+          }
         }
-        st_shared_v4(smem_u32(smem) + L::kQ + (r >> 7) * kTile + swz_offset(r & 127, c * 8), v.x,
-                     v.y, v.z, v.w);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = r0 + u * kStep;
+          if (r < kRows)
+            st_shared_v4(smem_u32(smem) + L::kQ + (r >> 7) * kTile + swz_offset(r & 127, c * 8),
+                         v[u].x, v[u].y, v[u].z, v[u].w);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -314,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
         const uint64_t nm2 = f2_pack(-mb, -mb);
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        uint64_t f0 = 0, f1 = 0;  // pairs of fp32 sums
+        uint64_t f0 = 0, f1 = 0;  // pairs of sums of the fp32 weights, for lse alone
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float x0, x1;
           f2_unpack(ffma2(f2_pack_u(ra[2 * i], ra[2 * i + 1]), sl2, nm2), x0, x1);
           const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          f0 = fadd2(f0, f2_pack(e0, e1));
+          if (kLse) f0 = fadd2(f0, f2_pack(e0, e1));
           ra[i] = pack_bf16(e0, e1);
           add_bf16x2(s0, s1, ra[i]);
         }
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x0, x1;
           f2_unpack(ffma2(f2_pack_u(rb[2 * i], rb[2 * i + 1]), sl2, nm2), x0, x1);
           const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          f1 = fadd2(f1, f2_pack(e0, e1));
+          if (kLse) f1 = fadd2(f1, f2_pack(e0, e1));
           rb[i] = pack_bf16(e0, e1);
           add_bf16x2(s2, s3, rb[i]);
         }
@@ -354,9 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         lb += (s0 + s1) + (s2 + s3);
-        float g0, g1;
-        f2_unpack(fadd2(f0, f1), g0, g1);
-        lf += g0 + g1;
+        if (kLse) {
+          float g0, g1;
+          f2_unpack(fadd2(f0, f1), g0, g1);
+          lf += g0 + g1;
+        }
         tmem_wait_st();
       }
       tc_fence_before();
@@ -369,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (good && work) {
       const int part = kPair ? split : 2 * split + w;
-      const int64_t t = row / a.G;
+      if (!kLse) lf = lb;
+      const int64_t t = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.G);
       const int h = kvh * a.G + static_cast<int>(row - t * a.G);
       const int64_t at = (static_cast<int64_t>(part) * a.rows + t) * a.Hq + h;
       const bool row_ok = row < n_rows;
@@ -381,10 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32_sync(tO + lane_off + c * 32, r);
           if (row_ok) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(op + c * 32 + i) =
-                  make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                              __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+            for (int i = 0; i < 32; i += 8) st_global_v8(op + c * 32 + i, &r[i]);
           }
         }
       }
@@ -401,32 +413,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kLse>
 cudaError_t launch_one(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                        cudaStream_t stream) {
   using L = XLayout<D, kPair>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&attn_prefix_kernel<D, kPair>),
-                                   L::kBytes);
+  cudaError_t e = ensure_smem_attr(
+      reinterpret_cast<const void*>(&attn_prefix_kernel<D, kPair, kLse>), L::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t n = static_cast<int64_t>(a.Hkv) * a.tiles_p * a.splits_x;
   if (n > 0x7fffffff) return cudaErrorInvalidValue;
   launch_begin(15, stream);
-  attn_prefix_kernel<D, kPair><<<static_cast<unsigned>(n), kThreads, L::kBytes, stream>>>(km, vm, a);
+  attn_prefix_kernel<D, kPair, kLse><<<static_cast<unsigned>(n), kThreads, L::kBytes, stream>>>(km, vm, a);
   e = cudaGetLastError();
   launch_end(15, stream);
   return e;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
+                     cudaStream_t stream) {
+  if (a.rows * a.G > 128)
+    return a.lse ? launch_one<D, true, true>(a, km, vm, stream)
+                 : launch_one<D, true, false>(a, km, vm, stream);
+  return a.lse ? launch_one<D, false, true>(a, km, vm, stream)
+               : launch_one<D, false, false>(a, km, vm, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefix(const PagedArgs& a, const CUtensorMap& k_map,
                                const CUtensorMap& v_map, cudaStream_t stream) {
-  const bool pair = a.rows * a.G > 128;
-  if (a.D == 128)
-    return pair ? launch_one<128, true>(a, k_map, v_map, stream)
-                : launch_one<128, false>(a, k_map, v_map, stream);
-  return pair ? launch_one<64, true>(a, k_map, v_map, stream)
-              : launch_one<64, false>(a, k_map, v_map, stream);
+  return a.D == 128 ? launch_d<128>(a, k_map, v_map, stream) : launch_d<64>(a, k_map, v_map, stream);
 }
 
 }  // namespace upipe

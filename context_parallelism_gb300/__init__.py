@@ -616,9 +616,13 @@ def _dense(t, dtype, shape, name):
 def _empty(stream, like, shape, dtype, zero=False):
     """An uninitialised (or zeroed) tensor beside `like`, allocated for the stream that the call
     runs on, so that its memory is not handed to other work before that stream is done with it."""
-    if stream is None:
-        return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
     torch = _torch or _lazy_torch()
+    if stream is None:
+        if zero:
+            return torch.zeros(shape, dtype=dtype, device=like.device)
+        if shape is like.shape:
+            return torch.empty_like(like)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -663,15 +667,15 @@ def _rope(call, q, k, phases, mscale, interleaved, positions, start, inplace, st
     rot = _phases(phases)
     q_in = q_out = k_in = k_out = None
     if q is not None:
-        q_in = _heads(q, "q", 4)
+        q_in = q_out = _heads(q, "q", 4)
         if not inplace:
-            q = _empty(stream, q, q.shape, q.dtype)
-        q_out = q_in if inplace else _heads(q, "q", 4)
+            q = torch.empty_like(q) if stream is None else _empty(stream, q, q.shape, q.dtype)
+            q_out = _heads(q, "q", 4)
     if k is not None:
-        k_in = _heads(k, "k", 4)
+        k_in = k_out = _heads(k, "k", 4)
         if not inplace:
-            k = _empty(stream, k, k.shape, k.dtype)
-        k_out = k_in if inplace else _heads(k, "k", 4)
+            k = torch.empty_like(k) if stream is None else _empty(stream, k, k.shape, k.dtype)
+            k_out = _heads(k, "k", 4)
     call(q_in, k_in, q_out, k_out, positions, start, phases, mscale, B, S, D, rot, interleaved,
          stream if stream is not None else _stream(None, ref))
     return q, k

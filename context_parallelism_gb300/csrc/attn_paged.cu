@@ -23,7 +23,7 @@
 // kv-head: neighbouring workers read neighbouring heads of the same pages.
 //
 // Two kernels, by the rows that a sequence has for a kv-head:
-//   up to 16 (a decode step): a worker is a single warp with a ring of TMA-fed stages of its own;
+//   up to 16 (a decode step): a worker is a single warp with a ring of stages of its own;
 //   17 and more: a worker is a block of one producer warp and four consumer warps of 16 rows.
 #include <cfloat>
 
@@ -87,13 +87,17 @@ __device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
                               : a / b;
 }
 
+// What starting and ending a piece costs, in tiles: each segment counts as so many tiles more, so
+// that a worker with many short sequences has fewer keys. Tile t of a segment is at kOver + t.
+constexpr uint32_t kOver = 2;
+
 // One group of segments (the prefix: b = -1, or a sequence): its rows and keys.
 struct Group {
   int tok0, n_tok;   // rows of q
   int keys;
   uint32_t segs;     // row tiles x kv-heads
-  uint32_t cost;     // tiles per segment, at least one (a segment without keys still writes)
-  __device__ __forceinline__ uint64_t tiles() const { return static_cast<uint64_t>(segs) * cost; }
+  uint32_t cost;     // kOver + tiles per segment, at least one (a segment without keys still writes)
+  __device__ __forceinline__ uint32_t tiles() const { return segs * cost; }  // host: below 2^32
 };
 
 template <int KS, int MT>
@@ -118,7 +122,7 @@ __device__ __forceinline__ Group load_group(const PagedArgs& a, int b, bool repo
     g.keys = min(max(len, 0), a.cap);
   }
   g.segs = (static_cast<uint32_t>(g.n_tok * a.G) + (MT - 1)) / MT * a.Hkv;
-  g.cost = max((static_cast<uint32_t>(g.keys) + (KS - 1)) / KS, 1u);
+  g.cost = kOver + max((static_cast<uint32_t>(g.keys) + (KS - 1)) / KS, 1u);
   return g;
 }
 
@@ -132,29 +136,34 @@ struct Walk {
   int k_lo, k_hi;            // the piece's keys
 
   // Cuts all tiles into the workers' shares (of at least `least` tiles) and finds this worker's
-  // start. Sequences are taken 32 at a time, one per lane.
-  __device__ __forceinline__ void init(const PagedArgs& a, int lane, int worker_, int n_workers,
-                                       uint32_t least) {
-    worker = worker_;
+  // start. Sequences are taken 32 at a time, one per lane. A block has up to `most` workers, and
+  // as many as are needed, so that few shares go to as many SMs; the workers of a block take
+  // neighbouring shares.
+  __device__ __forceinline__ void init(const PagedArgs& a, int lane, uint32_t in_block,
+                                       uint32_t most, uint32_t least) {
     left = group_seg = seg = kt = 0;
-    kvh = row0 = 0;
+    kvh = row0 = worker = 0;
     b = -1;
+    const bool report = blockIdx.x == 0 && in_block == 0;
     Group mine;  // sequence `lane`, kept for the second pass
     mine.segs = mine.cost = 0;
-    if (lane < a.B) mine = load_group<KS, MT>(a, lane, worker == 0);
+    if (lane < a.B) mine = load_group<KS, MT>(a, lane, report);
     g = load_group<KS, MT>(a, -1, false);
-    uint64_t total = mine.tiles();
+    uint32_t total = mine.tiles();
     for (int b0 = lane + 32; b0 < a.B; b0 += 32)
-      total += load_group<KS, MT>(a, b0, worker == 0).tiles();
+      total += load_group<KS, MT>(a, b0, report).tiles();
 #pragma unroll
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
     total += g.tiles();
-    const uint64_t sh = total + n_workers - 1;
-    share = max(static_cast<uint32_t>((sh >> 32) ? sh / n_workers : static_cast<uint32_t>(sh) / n_workers),
-                least);
-    uint64_t x = static_cast<uint64_t>(worker) * share;
-    if (x >= total) return;
-    left = static_cast<uint32_t>(min(static_cast<uint64_t>(share), total - x));
+    if (total == 0) return;
+    uint32_t per_block = most;
+    if (total < static_cast<uint64_t>(least) * gridDim.x * most)
+      per_block = min(((total - 1) / least) / gridDim.x + 1, most);
+    share = max((total - 1) / (gridDim.x * per_block) + 1, least);
+    worker = static_cast<int>(blockIdx.x * per_block + in_block);
+    if (in_block >= per_block || static_cast<uint64_t>(worker) * share >= total) return;
+    uint32_t x = worker * share;
+    left = min(share, total - x);
     if (x >= g.tiles()) {
       x -= g.tiles();
       group_seg = g.segs;
@@ -163,11 +172,10 @@ struct Walk {
           mine.segs = mine.cost = 0;
           if (b0 + lane < a.B) mine = load_group<KS, MT>(a, b0 + lane, false);
         }
-        uint64_t ws = mine.tiles();  // inclusive sums over the lanes
-        uint32_t ns = mine.segs;
+        uint32_t ws = mine.tiles(), ns = mine.segs;  // inclusive sums over the lanes
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
-          const uint64_t u = __shfl_up_sync(0xffffffffu, ws, s);
+          const uint32_t u = __shfl_up_sync(0xffffffffu, ws, s);
           const uint32_t v = __shfl_up_sync(0xffffffffu, ns, s);
           if (lane >= s) {
             ws += u;
@@ -195,8 +203,8 @@ struct Walk {
         }
       }
     }
-    seg = static_cast<uint32_t>((x >> 32) ? x / g.cost : static_cast<uint32_t>(x) / g.cost);
-    kt = static_cast<uint32_t>(x - static_cast<uint64_t>(seg) * g.cost);
+    seg = x / g.cost;
+    kt = x - seg * g.cost;
     const uint32_t rt = seg / a.Hkv;
     kvh = static_cast<int>(seg - rt * a.Hkv);
     row0 = static_cast<int>(rt) * MT;
@@ -212,9 +220,15 @@ struct Walk {
       if (++b >= a.B) return false;
       g = load_group<KS, MT>(a, b, false);
     }
-    const uint32_t n = min(g.cost - kt, left);
-    k_lo = min(static_cast<int>(kt * KS), g.keys);
-    k_hi = static_cast<int>(min((kt + n) * KS, static_cast<uint32_t>(g.keys)));
+    if (kt < kOver) {
+      const uint32_t n = min(kOver - kt, left);
+      kt += n;
+      left -= n;
+      if (left == 0) return false;
+    }
+    const uint32_t n = min(g.cost - kt, left), t0 = kt - kOver;
+    k_lo = min(static_cast<int>(t0 * KS), g.keys);
+    k_hi = static_cast<int>(min((t0 + n) * KS, static_cast<uint32_t>(g.keys)));
     p->tok0 = g.tok0;
     p->slot = static_cast<int64_t>(group_seg) + seg + worker;
     p->row0 = row0;
@@ -224,10 +238,10 @@ struct Walk {
     p->keys = k_hi - k_lo;
     p->n_kt = (p->keys + KS - 1) / KS;
     p->before = g.keys - g.n_tok - k_lo;
-    p->first = kt == 0;
+    p->first = t0 == 0;
     // workers from the segment's first tile to its last (known where the segment starts)
     const uint32_t rest = g.cost - kt - n;
-    p->parts = kt == 0 ? 1 + static_cast<int>(rest ? (rest + share - 1) / share : 0u) : 2;
+    p->parts = t0 == 0 ? 1 + static_cast<int>(rest ? (rest + share - 1) / share : 0u) : 2;
     left -= n;
     kt += n;
     if (kt == g.cost) {
@@ -315,8 +329,8 @@ __device__ __forceinline__ int row_limit(const PagedArgs& a, const Piece& p, int
 //
 // S^T = K Q^T and O^T += V^T P^T: keys and features fill the instruction's 16 rows, the few query
 // rows its 8 columns (NR column tiles). The warp keeps its piece's rows in registers and issues
-// the TMA copies into its ring itself, each stage's next one as soon as it has read it, running
-// on into the pieces that follow: no producer, no barrier but a stage's own, nothing to meet at.
+// the copies into its ring itself, each stage's next one as soon as it has read it, running on
+// into the pieces that follow: no producer, no barrier but a stage's own, nothing to meet at.
 constexpr int kWarps = 8;
 
 template <int D, int NR>
@@ -332,8 +346,7 @@ struct DLayout {
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
+    paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   using L = DLayout<D, NR>;
   constexpr int MT = 8 * NR, KS = L::kKeys, NS = L::kStages;
   constexpr int kHalf = KS * 128;      // bytes of a stage's 64 features of K or V
@@ -348,10 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   launch_dependents();
   if (lane == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(full + i, 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < NS; ++i) mbar_init(full + i, 32);  // every lane's copies
   }
   {
     // the tables, on their way to L2 while the lengths are read
@@ -365,37 +375,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   // ---- the copies: a place in the share that runs ahead of the computation ----
   Walk<KS, MT> wk;
-  // neighbouring shares on neighbouring SMs; few shares on one warp each
-  wk.init(a, lane, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x),
-          static_cast<int>(gridDim.x) * kWarps, static_cast<uint32_t>(a.least));
-  // A tile is KS / bx boxes of bx page rows, two lanes' halves of the features each. Pages are
-  // looked up 32 boxes at a time, one a lane, so that a tile's copy waits for no load.
-  const int bx = a.box_rows;  // 16 or 32: divides page_size and the tile's keys
-  const int shift = bx == 16 ? 4 : 5;
-  const int box = lane / (D / 64), half = lane % (D / 64);
-  const bool mine = box * bx < KS;
-  const uint32_t off = half * kHalf + box * bx * 128;
+  wk.init(a, lane, warp, kWarps, static_cast<uint32_t>(a.least));
+  // Copies are 16 bytes a lane (cp.async): a row of a page is D / 8 lanes, a warp instruction
+  // kRows rows. Pages are looked up for 32 runs of 16 keys at a time, one a lane, so that a tile's
+  // copies wait for no load. (TMA boxes of 16 page rows, the smallest page, moved a quarter less:
+  // 2.1 GB of 16-token pages in 468 against 3xx us.)
+  constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+  const int c_row = lane / kChunks, c_col = lane % kChunks;
+  const uint32_t dst0 = (c_col >> 3) * kHalf + c_row * 128 + (((c_col & 7) ^ c_row) << 4);
+  const int64_t row_step = 2 * kRows * a.slot_stride;  // bytes
+  const int64_t v_minus_k = reinterpret_cast<const char*>(a.vc) - reinterpret_cast<const char*>(a.kc);
+  const char* k0_ptr = nullptr;  // this lane's part of a row of the piece's head
   uint32_t n_cp = 0, n_pc = 0;  // tiles copied and pieces published so far
   int left = 0;                 // tiles of the piece that are still to be copied
-  int key0 = 0, kvh = 0;
-  int win = 0, win_page = -1, win_slot = 0;  // first key of the 32 boxes looked up; this lane's
+  int key0 = 0;
+  int win = 0;                  // first key of the 32 runs looked up
+  int64_t win_at = -1;          // this lane's: offset of the run's first row in the caches
   const int32_t* pages = nullptr;
   bool more = true;
-  // A box past the keys, or of a page that does not exist, lies outside the tensor map (page -1)
-  // and reads as zeros; nothing outside the caches is touched.
   auto look_up = [&]() {
     win = key0;
-    const int key = key0 + lane * bx;
-    win_page = -1;
-    win_slot = 0;
+    const int key = key0 + lane * 16;
+    win_at = -1;  // past the keys, or a page that does not exist: zeros
     if (key < wk.k_hi) {
       const uint32_t pg = static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size);
-      win_page = pages[pg];
-      win_slot = key - static_cast<int>(pg) * a.page_size;
-      if (win_page < 0 || win_page >= a.n_pages) {
-        win_page = -1;
+      const int page = pages[pg];
+      if (page >= 0 && page < a.n_pages)
+        win_at = page * a.page_stride + (key - static_cast<int>(pg) * a.page_size) * a.slot_stride;
+      else
         atomicOr(a.err, kErrBadPage);
-      }
     }
   };
   // Publishes the next piece (one without keys too).
@@ -409,88 +417,113 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     left = more ? p.n_kt : 0;
     if (left == 0) return;
     key0 = wk.k_lo;
-    kvh = p.kvh;
+    k0_ptr = reinterpret_cast<const char*>(a.kc + p.kvh * a.head_stride + c_row * a.slot_stride +
+                                           c_col * 8);
     pages = p.own ? a.table + wk.b * a.table_stride : a.ptable;
     look_up();
+    // the piece's rows of q, on their way to L2 before they are needed: a load that has to wait
+    // behind all the keys and values in flight takes microseconds
+    constexpr int kLines = D / 64;
+    if (lane < MT * kLines) {
+      const __nv_bfloat16* qp = q_row(a, p, lane / kLines);
+      if (qp) prefetch_l2(qp + lane % kLines * 64);
+    }
   };
-  // Copies the next tile, if there is one, into the stage that the tile kStages before it has left,
-  // publishing pieces on the way as long as there is room for them.
-  auto copy_next = [&](uint32_t n_done) {
+  // Copies the next tile into the stage that the tile kStages before it has left, publishing pieces
+  // on the way as long as there is room for them; false if there is nothing to copy now. Rows past
+  // the keys become zeros (whatever their slots hold: 0 * inf is not 0), and nothing outside the
+  // caches is touched.
+  auto copy_next = [&](uint32_t n_done) -> bool {
     while (left == 0) {
-      if (!more || n_pc - n_done >= static_cast<uint32_t>(L::kPieces)) return;
+      if (!more || n_pc - n_done >= static_cast<uint32_t>(L::kPieces)) return false;
       publish();
     }
-    if (((key0 - win) >> shift) + KS / bx > 32) look_up();
+    if (((key0 - win) >> 4) + KS / 16 > 32) look_up();
     const int s = static_cast<int>(n_cp % NS);
-    const int src = (((key0 - win) >> shift) + box) & 31;
-    const int page = __shfl_sync(0xffffffffu, win_page, src);
-    const int slot = __shfl_sync(0xffffffffu, win_slot, src);
-    if (lane == 0) mbar_arrive_expect_tx(full + s, L::kStage);
-    __syncwarp();
-    if (mine) {
-      const uint32_t dst = ring + s * L::kStage + off;
-      tma_load_4d(dst, &tm_k, half * 64, slot, kvh, page, full + s);
-      tma_load_4d(dst + kVoff, &tm_v, half * 64, slot, kvh, page, full + s);
+    const uint32_t dst = ring + s * L::kStage + dst0;
+#pragma unroll
+    for (int g = 0; g < KS / 16; ++g) {
+      const int64_t at = __shfl_sync(0xffffffffu, win_at, (((key0 - win) >> 4) + g) & 31);
+      const int rows = at < 0 ? 0 : wk.k_hi - key0 - g * 16;  // of this run's 16
+      const char* k = k0_ptr + (at < 0 ? 0 : 2 * at);
+      // row g * 16 + i * kRows + c_row: its 16-byte chunks are permuted by the row's last bits
+      if (rows >= 16) {
+#pragma unroll
+        for (int i = 0; i < 16 / kRows; ++i) {
+          const uint32_t d = (dst + (g * 16 + i * kRows) * 128) ^ (((i * kRows) & 7) << 4);
+          cp_async16(d, k);
+          cp_async16(d + kVoff, k + v_minus_k);
+          k += row_step;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 16 / kRows; ++i) {
+          const uint32_t d = (dst + (g * 16 + i * kRows) * 128) ^ (((i * kRows) & 7) << 4);
+          const bool in = i * kRows + c_row < rows;
+          const char* from = in ? k + i * row_step : reinterpret_cast<const char*>(a.kc);
+          cp_async16_zfill(d, from, in ? 16 : 0);
+          cp_async16_zfill(d + kVoff, in ? from + v_minus_k : from, in ? 16 : 0);
+        }
+      }
     }
+    cp_async_arrive(full + s);
     ++n_cp;
     --left;
     key0 += KS;
+    return true;
   };
 
   uint32_t n_it = 0, n_done = 0;  // tiles and pieces computed
-  publish();
-  bool ok = true;
-  while (ok) {
-    const Piece p = pieces[n_done % L::kPieces];
-    if (p.n_kt < 0) break;
-    // B fragments of Q^T: row lane/4 of each tile, features (lane%4)*2 and +8 of each 16
-    uint32_t qf[NR][D / 16][2];
-    int lim[NR][2];  // key limits of this thread's two statistics rows of each tile
-#pragma unroll
-    for (int c = 0; c < NR; ++c) {
-      const __nv_bfloat16* qp = q_row(a, p, c * 8 + (lane >> 2));
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          qf[c][k][e] = qp ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + e * 8 + (lane & 3) * 2) : 0u;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) lim[c][e] = row_limit(a, p, c * 8 + (lane & 3) * 2 + e);
+  Piece p;                        // the one being computed, tile j of it next
+  p.n_kt = 0;
+  int j = 0;
+  bool fresh = true, ok = true;
+  uint32_t qf[NR][D / 16][2];
+  int lim[NR][2];  // key limits of this thread's two statistics rows of each tile
+  float o[NR][D / 16][4];
+  float m[NR][2], lb[NR][2], lf[NR][2];
+  // One turn: fill the ring, then a tile. (Each part stands in the code once: what a step runs for
+  // the first time comes from L2 instruction by instruction, and a short step is mostly that.)
+  while (true) {
+#pragma unroll 1
+    while (n_cp - n_it < static_cast<uint32_t>(NS) && copy_next(n_done)) {
     }
-    float o[NR][D / 16][4];
-    float m[NR][2], lb[NR][2], lf[NR][2];
+    if (fresh) {
+      fresh = false;
+      j = 0;
+      p = pieces[n_done % L::kPieces];
+      if (p.n_kt < 0) break;
+      // B fragments of Q^T: row lane/4 of each tile, features (lane%4)*2 and +8 of each 16
 #pragma unroll
-    for (int c = 0; c < NR; ++c) {
+      for (int c = 0; c < NR; ++c) {
+        const __nv_bfloat16* qp = q_row(a, p, c * 8 + (lane >> 2));
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n)
+        for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[c][n][e] = 0.f;
+          for (int e = 0; e < 2; ++e)
+            qf[c][k][e] = qp ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + e * 8 + (lane & 3) * 2) : 0u;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[c][e] = -INFINITY;
-        lb[c][e] = lf[c][e] = 0.f;
+        for (int e = 0; e < 2; ++e) lim[c][e] = row_limit(a, p, c * 8 + (lane & 3) * 2 + e);
+      }
+#pragma unroll
+      for (int c = 0; c < NR; ++c) {
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][n][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[c][e] = -INFINITY;
+          lb[c][e] = lf[c][e] = 0.f;
+        }
       }
     }
-    // the first copies, behind the loads of q
-    if (n_done == 0)
-      for (int i = 0; i < NS; ++i) copy_next(0);
-    for (int j = 0; j < p.n_kt; ++j, ++n_it) {
+    if (j < p.n_kt) {
       const int s = static_cast<int>(n_it % NS);
       ok = __all_sync(0xffffffffu, mbar_wait(full + s, (n_it / NS) & 1));
       if (!ok) break;
       const uint32_t sk = ring + s * L::kStage, sv = sk + kVoff;
       const int k0 = j * KS;
-      // Values past the piece's last key (slots of its last page that no token fills) may be
-      // anything, infinities and NaN among them, and 0 * inf is not 0: they are cleared.
-      if (k0 + KS > p.keys) {
-        for (int x = lane; x < KS * (D / 8); x += 32) {
-          const int r = x / (D / 8), ch = x % (D / 8);
-          if (r >= p.keys - k0)
-            st_shared_v4(sv + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();  // before TMA may fill the stage again
-        __syncwarp();
-      }
       float sc[NR][KS / 16][4], sd[NR][KS / 16][4];  // two chains of sums: half the latency
 #pragma unroll
       for (int c = 0; c < NR; ++c)
@@ -576,9 +609,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mma16816(o[c][d], va, __float_as_uint(sc[c][t][0]), __float_as_uint(sc[c][t][1]));
         }
       __syncwarp();
-      copy_next(n_done);
+      ++n_it;
+      if (++j < p.n_kt) continue;
     }
-    if (!ok) break;
     // statistics over the lanes that share a row
 #pragma unroll
     for (int c = 0; c < NR; ++c)
@@ -617,12 +650,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     ++n_done;
-    // the room for pieces may have held the copies up; at least the next piece is published here
-    while (n_cp - n_it < static_cast<uint32_t>(NS) && (left > 0 || (more && n_pc - n_done < static_cast<uint32_t>(L::kPieces)))) {
-      const uint32_t before = n_cp;
-      copy_next(n_done);
-      if (n_cp == before) break;
-    }
+    fresh = true;
   }
   if (!ok) {  // a copy did not arrive within the limit
     if (lane == 0) atomicOr(a.err, kErrWaitTimeout | 0x10000u);
@@ -716,8 +744,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = r < KS;
     const uint32_t off = half * kHalf + r * 128;
     Walk<KS, MT> wk;
-    wk.init(a, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x),
-            static_cast<uint32_t>(a.least));
+    wk.init(a, lane, 0, 1, static_cast<uint32_t>(a.least));
     uint32_t n_it = 0, n_pc = 0;
     bool ok = true;
     while (ok) {
@@ -1102,15 +1129,14 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 }
 
 template <int D, int NR>
-cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
-                          cudaStream_t stream) {
+cudaError_t launch_decode(const PagedArgs& a, cudaStream_t stream) {
   using L = DLayout<D, NR>;
   const cudaError_t e = ensure_smem_attr(
       reinterpret_cast<const void*>(&paged_decode_kernel<D, NR>), L::kBytes);
   if (e != cudaSuccess) return e;
   // beside the prefix kernel, if there is one
   return launch_after(paged_decode_kernel<D, NR>, dim3(a.grid), dim3(kWarps * 32), L::kBytes,
-                      stream, a.splits_x != 0, km, vm, a);
+                      stream, a.splits_x != 0, a);
 }
 
 template <int D>
@@ -1156,6 +1182,8 @@ void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   // segments: every sequence's rows fill whole tiles and one that is not full
   const int64_t segs = (rows_p / a->mt + a->B) * a->Hkv;
   const int64_t segs_p = a->prefix && !a->splits_x ? (rows_p + a->mt - 1) / a->mt * a->Hkv : 0;
+  a->segs = segs;
+  a->segs_p = segs_p;
   // Workers: eight warps on each SM, or two blocks; fewer where there are fewer shares. A share is
   // at least 64 keys of a decode step: shorter ones cost more in the join than they save.
   const bool warps = a->mt != 64;
@@ -1167,18 +1195,18 @@ void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   a->n_slots = segs + segs_p + static_cast<int64_t>(a->grid) * (warps ? kWarps : 1);
 }
 
-cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
-                              const CUtensorMap& v_map, cudaStream_t stream) {
+cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap* k_map,
+                              const CUtensorMap* v_map, cudaStream_t stream) {
   launch_begin(13, stream);
   cudaError_t e;
   if (a.D == 128)
-    e = a.mt == 8    ? launch_decode<128, 1>(a, k_map, v_map, stream)
-        : a.mt == 16 ? launch_decode<128, 2>(a, k_map, v_map, stream)
-                     : launch_rows<128>(a, k_map, v_map, stream);
+    e = a.mt == 8    ? launch_decode<128, 1>(a, stream)
+        : a.mt == 16 ? launch_decode<128, 2>(a, stream)
+                     : launch_rows<128>(a, *k_map, *v_map, stream);
   else
-    e = a.mt == 8    ? launch_decode<64, 1>(a, k_map, v_map, stream)
-        : a.mt == 16 ? launch_decode<64, 2>(a, k_map, v_map, stream)
-                     : launch_rows<64>(a, k_map, v_map, stream);
+    e = a.mt == 8    ? launch_decode<64, 1>(a, stream)
+        : a.mt == 16 ? launch_decode<64, 2>(a, stream)
+                     : launch_rows<64>(a, *k_map, *v_map, stream);
   launch_end(13, stream);
   return e;
 }

@@ -347,6 +347,8 @@ cudaError_t make_tmap_pages(CUtensorMap* map, const void* base, int D, int page_
 struct PagedArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
+  const __nv_bfloat16 *kc, *vc;          // the caches
+  int64_t page_stride, slot_stride, head_stride;
   int64_t q_b, q_s, q_h, o_b, o_s, o_h;  // element strides (packed rows use q_s, o_s alone)
   float* lse;                // [B][Hq][T] ([Hq][rows] with cu) or NULL
   int64_t rows;              // rows of q: B * T, or the packed rows
@@ -376,6 +378,7 @@ struct PagedArgs {
   float4* slot_ml;
   int2* desc;
   int64_t n_slots;
+  int64_t segs, segs_p;      // segments at most: of the own keys, of the prefix
   int mt;                    // rows per tile: 8, 16 or 64
   int ks;                    // keys per tile
   int least;                 // tiles of the smallest share
@@ -384,8 +387,9 @@ struct PagedArgs {
 };
 // Plan of one call (host arithmetic): tiles, splits and slots from the sizes and the hints.
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len);
-cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap& k_map,
-                              const CUtensorMap& v_map, cudaStream_t stream);
+// The maps are used for tiles of 64 rows alone.
+cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap* k_map,
+                              const CUtensorMap* v_map, cudaStream_t stream);
 cudaError_t launch_attn_prefix(const PagedArgs& a, const CUtensorMap& k_map,
                                const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);

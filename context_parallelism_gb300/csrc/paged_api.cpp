@@ -454,6 +454,11 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   a.o_b = o->stride_b;
   a.o_s = o->stride_s;
   a.o_h = o->stride_h;
+  a.kc = static_cast<const __nv_bfloat16*>(cache->k);
+  a.vc = static_cast<const __nv_bfloat16*>(cache->v);
+  a.page_stride = cache->stride_page;
+  a.slot_stride = cache->stride_slot;
+  a.head_stride = cache->stride_head;
   a.lse = lse;
   a.T = S;
   a.cu = cu_rows;
@@ -465,6 +470,13 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   a.cap = static_cast<int>(max_pages > cap_most / cache->page_size
                                ? cap_most
                                : max_pages * cache->page_size);
+  // the kernels count tiles in 32 bits
+  const double tiles = static_cast<double>(a.segs) * (a.cap / a.ks + 1.0) +
+                       static_cast<double>(a.segs_p) * (static_cast<double>(prefix_len) / a.ks + 1.0);
+  if (tiles >= 4294967296.0)
+    return pfail(UPIPE_ERR_UNSUPPORTED,
+                 "%lld row tiles of up to %d keys: more than 2^32 tiles (use narrower page tables)",
+                 (long long)a.segs, a.cap);
   a.seq_len = seq_len;
   a.ptable = prefix_table;
   a.page_size = cache->page_size;
@@ -494,9 +506,11 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
     PAGED_CUDA(maps(&km, &vm, a.box_rows));
     PAGED_CUDA(launch_attn_prefix(a, km, vm, stream));
   }
-  a.box_rows = gcd(cache->page_size, a.ks);
-  PAGED_CUDA(maps(&km, &vm, a.box_rows));
-  PAGED_CUDA(launch_attn_paged(a, km, vm, stream));
+  if (a.mt == 64) {
+    a.box_rows = gcd(cache->page_size, a.ks);
+    PAGED_CUDA(maps(&km, &vm, a.box_rows));
+  }
+  PAGED_CUDA(launch_attn_paged(a, &km, &vm, stream));
   PAGED_CUDA(launch_paged_merge(a, stream));
   return UPIPE_OK;
 }

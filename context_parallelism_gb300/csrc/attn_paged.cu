@@ -359,7 +359,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPiece) + warp * L::kPieces;
   const uint32_t ring = smem_u32(smem) + warp * NS * L::kStage;
 
-  launch_dependents();
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(full + i, 32);  // every lane's copies
   }
@@ -656,8 +655,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (lane == 0) atomicOr(a.err, kErrWaitTimeout | 0x10000u);
     for (uint32_t j = n_it; j < n_cp; ++j) mbar_wait(full + j % NS, (j / NS) & 1, 100000000ull);
   }
-  // the prefix kernel that this one may have started beside is done before this one is, so that
-  // what follows this one follows both
+  // The join may start as blocks end (its own start in the middle of the work, waiting beside it,
+  // cost 12 of 113 us over 131072 keys). The prefix kernel that this one may have started beside is
+  // done before this one is, so that what follows this one follows both.
+  launch_dependents();
   grid_dependency_wait();
 }
 
@@ -701,7 +702,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  launch_dependents();
   if (threadIdx.x == 128) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
@@ -969,8 +969,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  // the prefix kernel that this one may have started beside is done before this one is, so that
-  // what follows this one follows both
+  // The join may start as blocks end (its own start in the middle of the work, waiting beside it,
+  // cost 12 of 113 us over 131072 keys). The prefix kernel that this one may have started beside is
+  // done before this one is, so that what follows this one follows both.
+  launch_dependents();
   grid_dependency_wait();
 }
 

@@ -14,7 +14,10 @@
 //
 // Bound: HBM. Each element is read and written once (4 bytes); a thread owns 8 frequencies (two
 // 16-byte vectors of a head) and applies them to kHeads heads of one token, so the eight
-// sincospif are shared by 64 elements.
+// sincospif are shared by 64 elements. Measured: 131072 tokens of 32 + 8 heads of 128 (2.7 GB) in
+// 387 us, 6.9 TB/s (2 heads a thread 464 us, 6 heads 410); 8192 tokens 30.8 us, of which the ramp
+// is 5. Blocks of 64 threads end and start evenly: 256 cost 3 %. Streaming loads and stores changed
+// nothing.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -23,8 +26,14 @@
 namespace upipe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 constexpr int kHeads = 4;  // heads of one token per thread
+
+// a / b for 0 <= a, 0 < b; 32-bit where it can be (the 64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -100,14 +109,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       i = tok - first;
       if (i < 0) return;
     } else {
-      b = tok / a.S;
+      b = a.B == 1 ? 0 : div_fl(tok, a.S);
       i = tok - b * a.S;
       n = static_cast<int>(a.S);
     }
     const int64_t j = static_cast<int64_t>(a.seq_len[b]) - n + i;
     pos = a.pos ? a.pos[tok] : a.pos0 + j;
     if (j >= 0) {
-      const int64_t pg = j / a.page_size;
+      const int64_t pg = div_fl(j, a.page_size);
       const int64_t page = pg < a.max_pages ? a.table[b * a.table_stride + pg] : -1;
       if (page >= 0 && page < a.n_pages)
         slot_k = page * a.page_stride + (j - pg * a.page_size) * a.slot_stride;
@@ -119,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       i = tok;
     }
   } else {
-    b = tok / a.S;
+    b = a.B == 1 ? 0 : div_fl(tok, a.S);
     i = tok - b * a.S;
     pos = a.pos ? a.pos[tok] : a.pos0 + i;
   }

@@ -182,42 +182,46 @@ __global__ void __launch_bounds__(threads(kPair), 1)
     }
   } else if (warp == 8) {
     // ---------------- products ----------------
-    if (lane == 0) {
+    // The warp stays converged, one lane issues: operands in uniform registers.
+    {
+      auto wait_all = [&](uint64_t* br, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(br, parity));
+      };
       const uint32_t id_s = idesc_bf16(128, 128, false, false);
       const uint32_t id_o = idesc_bf16(128, D, false, true);
       const uint64_t base_k = kdesc0(smem_u32(smem));
       const uint64_t base_mn = mndesc0(smem_u32(smem));
       constexpr uint32_t kTileU = kTile >> 4;
-      bool ok = wait(q_full, 0);
+      bool ok = wait_all(q_full, 0);
       auto issue_s = [&](int w, int j) -> bool {
         const int s = j % NS;
-        if ((!kPair || w == 0) && !wait(k_full + s, (j / NS) & 1)) return false;
+        if ((!kPair || w == 0) && !wait_all(k_full + s, (j / NS) & 1)) return false;
         tc_fence_after();
-        const uint64_t bk = opaque_u64(base_k);
+        const uint64_t bk = base_k;
         const uint32_t uq = (L::kQ >> 4) + (kPair ? w * kTileU : 0u);
         const uint32_t uk = (L::kK >> 4) + s * kTileU;
 #pragma unroll
         for (int k16 = 0; k16 < D / 16; ++k16)
-          umma_f16_ss(tmem + 128 * w, bk + (uq + kstep(k16)), bk + (uk + kstep(k16)), id_s,
+          umma_f16_ss_warp(tmem + 128 * w, bk + (uq + kstep(k16)), bk + (uk + kstep(k16)), id_s,
                       k16 > 0 ? 1u : 0u);
-        umma_commit(s_full + w);
-        if (!kPair || w == 1 || !two) umma_commit(k_empty + s);
+        umma_commit_warp(s_full + w);
+        if (!kPair || w == 1 || !two) umma_commit_warp(k_empty + s);
         return true;
       };
       // n: how many tiles tile/stream w has taken before this one
       auto issue_pv = [&](int w, int j, int n, bool last) -> bool {
         const int s = j % NS;
-        if (!wait(p_full + w, n & 1)) return false;
-        if ((!kPair || w == 0) && !wait(v_full + s, (j / NS) & 1)) return false;
+        if (!wait_all(p_full + w, n & 1)) return false;
+        if ((!kPair || w == 0) && !wait_all(v_full + s, (j / NS) & 1)) return false;
         tc_fence_after();
-        const uint64_t bmn = opaque_u64(base_mn);
+        const uint64_t bmn = base_mn;
         const uint32_t uv = (L::kV >> 4) + s * kTileU;
 #pragma unroll
         for (int k16 = 0; k16 < 8; ++k16)
-          umma_f16_ts(tmem + 256 + 128 * w, tmem + 128 * w + k16 * 8, bmn + (uv + mnstep(k16)),
+          umma_f16_ts_warp(tmem + 256 + 128 * w, tmem + 128 * w + k16 * 8, bmn + (uv + mnstep(k16)),
                       id_o, (k16 > 0 || n > 0) ? 1u : 0u);
-        if (last) umma_commit(o_done + w);
-        if (!kPair || w == 1 || !two) umma_commit(v_empty + s);
+        if (last) umma_commit_warp(o_done + w);
+        if (!kPair || w == 1 || !two) umma_commit_warp(v_empty + s);
         return true;
       };
       if (kPair) {
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
         }
       }
       if (!ok) {
-        umma_commit(drain);
+        umma_commit_warp(drain);
         mbar_wait(drain, 0, 100000000ull);
       }
     }

@@ -11,8 +11,14 @@
 //   S_w = Q_w K_j^T          tcgen05 (M 128, N 128, K D) -> TMEM S[w]
 //   P_w = exp2(S_w c - m_w)  bf16, over S[w]'s first 64 columns
 //   O_w += P_w V_j           tcgen05 with A from TMEM
-// One thread issues every product; PV_w(j) goes before S_w's next tile, so the commit that
-// publishes that S also says that O_w is settled and may be rescaled.
+// One warp issues every product. Where P lies over S, PV_w(j) goes before S_w's next tile, so the
+// commit that publishes that S also says that O_w is settled and may be rescaled. With two row tiles
+// of D 64 tensor memory has room for P beside S: then S_w's next tile is computed while this one's
+// weights are (65536 keys, 128 sequences x 2 tokens, 64 q-heads: 384 -> 348 us). D 128 has that
+// room only with 64-key tiles, whose smaller products cost more than they hide (877 -> 1200 us for
+// 96 x 5 tokens on 131000 keys), as does Q in tensor memory there (1390 us). What bounds two row
+// tiles of D 128: the chain of one of them, softmax 1650 cycles, its two products 1200, and the
+// waits between them 700; the other one's runs in its gaps.
 //
 // Threads: warps 0-3 and 4-7 softmax (and the load of Q), warp 8 products, warp 9 (and 10) TMA: one
 // lane per box of page rows, its page looked up while the stage is still in use.
@@ -32,6 +38,8 @@ constexpr float kRescaleLog2 = 8.0f;
 
 template <int D, bool kPair>
 struct XLayout {
+  // P in columns of its own, where tensor memory has room for them (two row tiles of D 64)
+  static constexpr bool kOwnP = kPair && D == 64;
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kQTiles = kPair ? 2 : 1;
   static constexpr int kStages = D == 128 ? (kPair ? 2 : 3) : (kPair ? 5 : 6);
@@ -39,10 +47,14 @@ struct XLayout {
   static constexpr int kK = kQTiles * kTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBar = kV + kStages * kTile;
-  static constexpr int kNumBars = 1 + 4 * kStages + 2 + 2 + 2 + 1;
+  static constexpr int kNumBars = 1 + 4 * kStages + 2 + 2 + 2 + 2 + 1;
   static constexpr int kSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kSlot + 4;
   static constexpr int kBytes = kAbort + 4 + 1024;
+  // TMEM columns: S[2], P[2] (two bf16 a column) if it is not over S, O[2]
+  static constexpr int tP = kOwnP ? 256 : 0, tPStep = kOwnP ? 64 : 128;
+  static constexpr int tO = kOwnP ? 384 : 256;
+  static_assert(tO + 2 * D <= 512, "tensor memory has 512 columns");
 };
 
 template <int D, bool kPair, bool kLse>
@@ -52,6 +64,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
   using L = XLayout<D, kPair>;
   constexpr int NS = L::kStages;
   constexpr int kTile = L::kTile;
+  constexpr bool kOwnP = L::kOwnP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -62,8 +75,9 @@ __global__ void __launch_bounds__(threads(kPair), 1)
   uint64_t* v_empty = k_empty + NS;
   uint64_t* s_full = v_empty + NS;  // [2]
   uint64_t* p_full = s_full + 2;    // [2]
-  uint64_t* o_done = p_full + 2;    // [2]
-  uint64_t* drain = o_done + 2;
+  uint64_t* o_done = p_full + 2;    // [2] with P in its own columns after every PV_w, else the last
+  uint64_t* s_free = o_done + 2;    // [2] with P in its own columns: S_w is in registers
+  uint64_t* drain = s_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -95,6 +109,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(o_done + i, 1);
+      mbar_init(s_free + i, 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -196,6 +211,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
       auto issue_s = [&](int w, int j) -> bool {
         const int s = j % NS;
         if ((!kPair || w == 0) && !wait_all(k_full + s, (j / NS) & 1)) return false;
+        if (kOwnP && j > 0 && !wait_all(s_free + w, (j - 1) & 1)) return false;
         tc_fence_after();
         const uint64_t bk = base_k;
         const uint32_t uq = (L::kQ >> 4) + (kPair ? w * kTileU : 0u);
@@ -203,7 +219,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
 #pragma unroll
         for (int k16 = 0; k16 < D / 16; ++k16)
           umma_f16_ss_warp(tmem + 128 * w, bk + (uq + kstep(k16)), bk + (uk + kstep(k16)), id_s,
-                      k16 > 0 ? 1u : 0u);
+                           k16 > 0 ? 1u : 0u);
         umma_commit_warp(s_full + w);
         if (!kPair || w == 1 || !two) umma_commit_warp(k_empty + s);
         return true;
@@ -218,13 +234,25 @@ __global__ void __launch_bounds__(threads(kPair), 1)
         const uint32_t uv = (L::kV >> 4) + s * kTileU;
 #pragma unroll
         for (int k16 = 0; k16 < 8; ++k16)
-          umma_f16_ts_warp(tmem + 256 + 128 * w, tmem + 128 * w + k16 * 8, bmn + (uv + mnstep(k16)),
-                      id_o, (k16 > 0 || n > 0) ? 1u : 0u);
-        if (last) umma_commit_warp(o_done + w);
+          umma_f16_ts_warp(tmem + L::tO + D * w, tmem + L::tP + L::tPStep * w + k16 * 8,
+                           bmn + (uv + mnstep(k16)), id_o, (k16 > 0 || n > 0) ? 1u : 0u);
+        if (kOwnP || last) umma_commit_warp(o_done + w);
         if (!kPair || w == 1 || !two) umma_commit_warp(v_empty + s);
         return true;
       };
-      if (kPair) {
+      if (kOwnP) {
+        // S_w(j + 1) as soon as S_w(j) is in registers, while its weights are computed; in the
+        // order in which the two groups, half a tile apart, are ready
+        if (ok && n_kt > 0) ok = issue_s(0, 0) && (!two || issue_s(1, 0));
+        for (int j = 0; ok && j < n_kt; ++j) {
+          const bool more = j + 1 < n_kt;
+          if (more) ok = issue_s(0, j + 1);
+          if (ok && two && j > 0) ok = issue_pv(1, j - 1, j - 1, false);
+          if (ok && two && more) ok = issue_s(1, j + 1);
+          if (ok) ok = issue_pv(0, j, j, !more);
+        }
+        if (ok && two && n_kt > 0) ok = issue_pv(1, n_kt - 1, n_kt - 1, true);
+      } else if (kPair) {
         if (ok && n_kt > 0) ok = issue_s(0, 0) && (!two || issue_s(1, 0));
         for (int j = 0; ok && j < n_kt; ++j) {
           const bool more = j + 1 < n_kt;
@@ -282,11 +310,17 @@ __global__ void __launch_bounds__(threads(kPair), 1)
     const int w = warp >> 2;
     const int t128 = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + 128 * w, tO = tmem + 256 + 128 * w;
+    const uint32_t tS = tmem + 128 * w, tP = tmem + L::tP + L::tPStep * w, tO = tmem + L::tO + D * w;
     const int64_t row = row0 + (kPair ? 128 * w : 0) + t128;
     // a warp without rows only keeps the barriers going: its TMEM lanes reach no output
     const bool work = row - (threadIdx.x & 31) < n_rows;
     float m_used = -INFINITY, lb = 0.f, lf = 0.f;
+    // the scores are in registers: S_w may be overwritten with the next tile's
+    auto s_read = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free + w);
+    };
     bool good = true;
     int n = 0;
     const int j0 = kPair ? 0 : w, dj = kPair ? 1 : 2;
@@ -315,6 +349,7 @@ __global__ void __launch_bounds__(threads(kPair), 1)
         tmem_ld64_nowait(tS + lane_off + 64, rb);
         tmem_wait_ld_dep64(ra);
         tmem_reg_dep64(rb);
+        if constexpr (kOwnP) s_read();
         if (valid < 128) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) {
@@ -362,6 +397,12 @@ __global__ void __launch_bounds__(threads(kPair), 1)
           rb[i] = pack_bf16(e0, e1);
           add_bf16x2(s2, s3, rb[i]);
         }
+        // P's own columns and O are free once PV_w of the tile before has run
+        if (kOwnP && n > 0) {
+          good = __all_sync(0xffffffffu, wait(o_done + w, (n - 1) & 1));
+          if (!good) break;
+          tc_fence_after();
+        }
         {
           uint32_t pa[32], pb[32];
 #pragma unroll
@@ -369,8 +410,8 @@ __global__ void __launch_bounds__(threads(kPair), 1)
             pa[i] = ra[i];
             pb[i] = rb[i];
           }
-          tmem_st32(tS + lane_off, pa);
-          tmem_st32(tS + lane_off + 32, pb);
+          tmem_st32(tP + lane_off, pa);
+          tmem_st32(tP + lane_off + 32, pb);
         }
         if (n > 0 && __any_sync(0xffffffffu, upd)) {
 #pragma unroll
@@ -389,13 +430,20 @@ __global__ void __launch_bounds__(threads(kPair), 1)
           lf += g0 + g1;
         }
         tmem_wait_st();
+      } else {
+        if constexpr (kOwnP) {
+          s_read();
+          // as the others: no arrival on p_full for this tile before the one before it is complete
+          if (n > 0) good = __all_sync(0xffffffffu, wait(o_done + w, (n - 1) & 1));
+          if (!good) break;
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + w);
     }
     if (good && n > 0) {
-      good = __all_sync(0xffffffffu, wait(o_done + w, 0));
+      good = __all_sync(0xffffffffu, wait(o_done + w, kOwnP ? (n - 1) & 1 : 0));
       if (good) tc_fence_after();
     }
     if (good && work) {

@@ -10,6 +10,7 @@ fails with an error that says how to build it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as _np  # noqa: F401  (kept for users that pass numpy-backed pinned buffers)
@@ -365,6 +366,7 @@ def upipe_kv_append(q, q_out, k, v, cache, page_table, table_stride, max_pages, 
                                 _stream(stream, page_table)), "upipe_kv_append")
 
 
+@functools.lru_cache(maxsize=4096)
 def upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, prefix_len, max_q, max_len):
     return int(_lib.upipe_attn_paged_workspace_bytes(B, rows, Hq, Hkv, D, prefix_len, max_q,
                                                      max_len))

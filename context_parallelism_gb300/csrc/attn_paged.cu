@@ -139,19 +139,30 @@ struct Walk {
   // start. Sequences are taken 32 at a time, one per lane. A block has up to `most` workers, and
   // as many as are needed, so that few shares go to as many SMs; the workers of a block take
   // neighbouring shares.
+  // first: what the first two rounds load (sequences lane and lane + 32), asked for at the
+  // kernel's very start, before anything that a load cannot pass.
+  struct First {
+    Group g[2];
+  };
+  __device__ __forceinline__ static First begin(const PagedArgs& a, int lane, bool report) {
+    First f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f.g[i].segs = f.g[i].cost = 0;
+      if (lane + 32 * i < a.B) f.g[i] = load_group<KS, MT>(a, lane + 32 * i, report);
+    }
+    return f;
+  }
   __device__ __forceinline__ void init(const PagedArgs& a, int lane, uint32_t in_block,
-                                       uint32_t most, uint32_t least) {
+                                       uint32_t most, uint32_t least, const First& first) {
     left = group_seg = seg = kt = 0;
     kvh = row0 = worker = 0;
     b = -1;
-    const bool report = blockIdx.x == 0 && in_block == 0;
-    Group mine;  // sequence `lane`, kept for the second pass
-    mine.segs = mine.cost = 0;
-    if (lane < a.B) mine = load_group<KS, MT>(a, lane, report);
+    Group mine = first.g[0];  // the round's sequence of this lane
     g = load_group<KS, MT>(a, -1, false);
-    uint32_t total = mine.tiles();
-    for (int b0 = lane + 32; b0 < a.B; b0 += 32)
-      total += load_group<KS, MT>(a, b0, report).tiles();
+    uint32_t total = mine.tiles() + first.g[1].tiles();
+    for (int b0 = lane + 64; b0 < a.B; b0 += 32)
+      total += load_group<KS, MT>(a, b0, blockIdx.x == 0 && in_block == 0).tiles();
 #pragma unroll
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
     total += g.tiles();
@@ -168,7 +179,9 @@ struct Walk {
       x -= g.tiles();
       group_seg = g.segs;
       for (int b0 = 0;; b0 += 32) {
-        if (b0 > 0) {
+        if (b0 == 32) {
+          mine = first.g[1];
+        } else if (b0 > 32) {
           mine.segs = mine.cost = 0;
           if (b0 + lane < a.B) mine = load_group<KS, MT>(a, b0 + lane, false);
         }
@@ -359,6 +372,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPiece) + warp * L::kPieces;
   const uint32_t ring = smem_u32(smem) + warp * NS * L::kStage;
 
+  const auto first = Walk<KS, MT>::begin(a, lane, blockIdx.x == 0 && warp == 0);
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(full + i, 32);  // every lane's copies
   }
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   // ---- the copies: a place in the share that runs ahead of the computation ----
   Walk<KS, MT> wk;
-  wk.init(a, lane, warp, kWarps, static_cast<uint32_t>(a.least));
+  wk.init(a, lane, warp, kWarps, static_cast<uint32_t>(a.least), first);
   // Copies are 16 bytes a lane (cp.async): a row of a page is D / 8 lanes, a warp instruction
   // kRows rows. Pages are looked up for 32 runs of 16 keys at a time, one a lane, so that a tile's
   // copies wait for no load. (TMA boxes of 16 page rows, the smallest page, moved a quarter less:
@@ -747,7 +761,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = r < KS;
     const uint32_t off = half * kHalf + r * 128;
     Walk<KS, MT> wk;
-    wk.init(a, lane, 0, 1, static_cast<uint32_t>(a.least));
+    wk.init(a, lane, 0, 1, static_cast<uint32_t>(a.least),
+            Walk<KS, MT>::begin(a, lane, blockIdx.x == 0));
     uint32_t n_it = 0, n_pc = 0;
     bool ok = true;
     while (ok) {

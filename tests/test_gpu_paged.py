@@ -126,6 +126,41 @@ def test_decode(case, head_major):
     b.check(*b.attend())
 
 
+PREFIX = {  # (rows a kv-head) row tiles of the prefix kernel: one, two, two and a part of a third
+    "one_tile_d64": ([1] * 25, [b % 9 for b in range(25)], 8, 2, 64, 32, 777),
+    "one_tile": ([1] * 32, [b % 5 + 1 for b in range(32)], 8, 2, 128, 16, 1025),
+    "two_tiles_d64": ([2] * 30, [b % 7 + 2 for b in range(30)], 8, 2, 64, 64, 1300),
+    "third_alone": ([1] * 75, [1] * 75, 4, 1, 128, 16, 600),
+    "third_alone_d64": ([1] * 75, [2] * 75, 4, 1, 64, 128, 600),
+    "many_d64": ([3] * 40, [b + 3 for b in range(40)], 16, 2, 64, 16, 391),
+}
+
+
+@pytest.mark.parametrize("with_lse", [True, False])
+@pytest.mark.parametrize("case", list(PREFIX))
+def test_prefix_row_tiles(case, with_lse):
+    counts, lens, Hq, Hkv, D, page, prefix = PREFIX[case]
+    b = Batch(counts, lens, Hq, Hkv, D, page, prefix, seed=30 + len(case))
+    o, lse = b.attend()
+    if with_lse:
+        b.check(o, lse)
+        return
+    # without lse (other weight sums are kept) the same o
+    o2, none = up.paged_attention(b.q, b.kp, b.vp, b.table, b.seq_len, prefix_table=b.ptable,
+                                  prefix_len=prefix)
+    up.upipe_sync_status()
+    assert none is None
+    b.check(o2, lse)
+
+
+@pytest.mark.parametrize("prefix", [100, 4000])
+def test_one_row_on_long_own_pages_and_on_a_long_prefix(prefix):
+    b = Batch([1], [3000], 8, 2, 128, 16, prefix, seed=33)
+    b.check(*b.attend())
+    b = Batch([1] * 2, [3000, 1], 4, 4, 64, 48, prefix, seed=34)
+    b.check(*b.attend())
+
+
 MULTI = {
     "draft": ([3] * 4, [3, 10, 67, 130], 8, 2, 128, 16, 140),
     "draft_d64": ([5] * 3, [5, 64, 65], 4, 4, 64, 16, 0),

@@ -1170,15 +1170,28 @@ cudaError_t launch_rows(const PagedArgs& a, const CUtensorMap& km, const CUtenso
                       a.splits_x != 0, km, vm, a);
 }
 
-// Rows beyond which the prefix goes to the tensor-core kernel with 128-row tiles.
-bool prefix_on_tc(const PagedArgs& a) { return a.prefix >= 128 && a.rows * a.G > 16; }
+// Whether the prefix goes to the tensor-core kernel with its 128-row tiles, or to the kernels here
+// together with the own keys, in tiles of 16 (or 64) rows that read it again from L2 each. The extra
+// launch and the wider partial results cost about 5 us, so it takes rows x keys to pay (32 q-heads
+// on 8 kv-heads, D 128, 200 own keys, one new token; us there / here):
+//     rows a kv-head    32           64           128          256          512
+//     prefix   512      18 / 15      19 / 16      21 / 16      25 / 22      35 / 34
+//     prefix  2048      21 / 20      23 / 19      25 / 25      29 / 33      39 / 58
+//     prefix  4096      22 / 20      25 / 26      28 / 32      32 / 50      43 / 92
+//     prefix 16384      32 / 35      36 / 49      39 / 83      44 / 144     65 / 268
+// (the same border with 16 heads of 64). With 64-row tiles the border lies higher: 128 rows on 4096
+// keys 28 / 24, on 16384 39 / 49; 256 rows on 4096 31 / 37.
+bool prefix_on_tc(const PagedArgs& a, int64_t rows_o) {
+  const int64_t rows = a.rows * a.G;
+  return a.prefix >= 128 && rows > 16 && rows * a.prefix >= (int64_t(1) << (rows_o > 16 ? 20 : 18));
+}
 
 }  // namespace
 
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   const int64_t rows_o = max_q * a->G, rows_p = a->rows * a->G;
   a->splits_x = a->splits_p = a->tiles_p = 0;
-  if (prefix_on_tc(*a)) {
+  if (prefix_on_tc(*a, rows_o)) {
     // One CTA per SM: waves of items, each as long as its share of key tiles and about four
     // tiles' time of start and end. The fewest splits of the shortest time.
     const bool pair = rows_p > 128;
@@ -1197,8 +1210,9 @@ void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
     }
     a->splits_p = a->splits_x * (pair ? 1 : 2);
   }
+  // a sequence's own rows choose the kernel; a prefix beside them takes several row tiles
   const int64_t most = a->prefix && !a->splits_x ? rows_p : rows_o;
-  a->mt = most <= 8 ? 8 : most <= 16 ? 16 : 64;
+  a->mt = rows_o > 16 ? 64 : most <= 8 ? 8 : 16;
   // segments: every sequence's rows fill whole tiles and one that is not full
   const int64_t segs = (rows_p / a->mt + a->B) * a->Hkv;
   const int64_t segs_p = a->prefix && !a->splits_x ? (rows_p + a->mt - 1) / a->mt * a->Hkv : 0;

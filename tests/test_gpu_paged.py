@@ -126,13 +126,15 @@ def test_decode(case, head_major):
     b.check(*b.attend())
 
 
-PREFIX = {  # (rows a kv-head) row tiles of the prefix kernel: one, two, two and a part of a third
-    "one_tile_d64": ([1] * 25, [b % 9 for b in range(25)], 8, 2, 64, 32, 777),
-    "one_tile": ([1] * 32, [b % 5 + 1 for b in range(32)], 8, 2, 128, 16, 1025),
-    "two_tiles_d64": ([2] * 30, [b % 7 + 2 for b in range(30)], 8, 2, 64, 64, 1300),
-    "third_alone": ([1] * 75, [1] * 75, 4, 1, 128, 16, 600),
-    "third_alone_d64": ([1] * 75, [2] * 75, 4, 1, 64, 128, 600),
-    "many_d64": ([3] * 40, [b + 3 for b in range(40)], 16, 2, 64, 16, 391),
+PREFIX = {  # shapes that the tensor-core kernel takes: one row tile, two, two and part of a third
+    "one_tile_d64": ([1] * 25, [b % 9 for b in range(25)], 8, 2, 64, 32, 10777),
+    "one_tile": ([1] * 32, [b % 5 + 1 for b in range(32)], 8, 2, 128, 16, 8321),
+    "one_tile_small": ([3], [5], 8, 1, 128, 64, 44000),
+    "two_tiles_d64": ([2] * 30, [b % 7 + 2 for b in range(30)], 8, 2, 64, 64, 4500),
+    "two_tiles": ([1] * 18, [b % 3 for b in range(18)], 40, 4, 128, 256, 6001),
+    "third_alone": ([1] * 75, [1] * 75, 4, 1, 128, 16, 900),
+    "third_alone_d64": ([1] * 75, [2] * 75, 4, 1, 64, 128, 900),
+    "many_d64": ([3] * 40, [b + 3 for b in range(40)], 16, 2, 64, 16, 1391),
 }
 
 

@@ -146,16 +146,18 @@ def _stream(stream, *tensors):
 
 
 _torch = None
-_raw_stream = None
+_raw_stream = _raw_alloc = _raw_delete = None
 
 
 def _lazy_torch():
     """torch, imported once: the calls for single tokens are bound by the host's time."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _raw_alloc, _raw_delete
     if _torch is None:
         import torch
-        _torch = torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+        _raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+        _torch = torch
     return _torch
 
 
@@ -655,17 +657,20 @@ def _phases(phases):
     return 2 * phases.shape[0]
 
 
-def _rope(call, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
+def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
     torch = _torch or _lazy_torch()
     ref = q if q is not None else k
     if ref is None or ref.dim() != 4:
         raise ValueError("q and k must be [B, S, heads, D] (one may be None)")
-    B, S, _, D = ref.shape
-    if k is not None and k is not ref and (k.dim() != 4 or k.shape[:2] != ref.shape[:2] or
-                                           k.shape[3] != D):
-        raise ValueError("q and k must agree in B, S and D")
+    B, S, _, D = shape = ref.shape
+    if k is not None and k is not ref:
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != B or ks[1] != S or ks[3] != D:
+            raise ValueError("q and k must agree in B, S and D")
+    pos = None
     if positions is not None:
-        _dense(positions, torch.int64, ref.shape[:2], "positions")
+        _dense(positions, torch.int64, shape[:2], "positions")
+        pos = positions.data_ptr()
     rot = _phases(phases)
     q_in = q_out = k_in = k_out = None
     if q is not None:
@@ -678,8 +683,10 @@ def _rope(call, q, k, phases, mscale, interleaved, positions, start, inplace, st
         if not inplace:
             k = torch.empty_like(k) if stream is None else _empty(stream, k, k.shape, k.dtype)
             k_out = _heads(k, "k", 4)
-    call(q_in, k_in, q_out, k_out, positions, start, phases, mscale, B, S, D, rot, interleaved,
-         stream if stream is not None else _stream(None, ref))
+    st = fn(q_in, k_in, q_out, k_out, pos, start, phases.data_ptr(), mscale, B, S, D, rot,
+            1 if interleaved else 0, _stream(stream, ref))
+    if st:
+        raise UpipeError(st, where)
     return q, k
 
 
@@ -688,38 +695,45 @@ def rope_forward(q, k, phases, mscale=1.0, interleaved=False, positions=None, st
     """q, k (bf16 [B, S, heads, D], any strides with contiguous D; one may be None) with their
     first 2 * len(phases) features rotated by their positions: positions (int64 [B, S]) or
     start + s. phases, mscale: rope_phases. inplace writes the inputs. Returns (q, k)."""
-    return _rope(upipe_rope_fwd, q, k, phases, mscale, interleaved, positions, start, inplace,
-                 stream)
+    return _rope(_lib.upipe_rope_fwd, "upipe_rope_fwd", q, k, phases, mscale, interleaved,
+                 positions, start, inplace, stream)
 
 
 def rope_backward(dq, dk, phases, mscale=1.0, interleaved=False, positions=None, start=0,
                   inplace=False, stream=None):
     """The gradients with respect to rope_forward's inputs, from those of its outputs."""
-    return _rope(upipe_rope_bwd, dq, dk, phases, mscale, interleaved, positions, start, inplace,
-                 stream)
+    return _rope(_lib.upipe_rope_bwd, "upipe_rope_bwd", dq, dk, phases, mscale, interleaved,
+                 positions, start, inplace, stream)
 
 
 def _batch(q, cu_seqlens, seq_len):
-    """B, S and dimensions of a padded [B, S, heads, D] or packed [S, heads, D] batch."""
-    torch = _torch or _lazy_torch()
-    B = seq_len.numel()
-    _dense(seq_len, torch.int32, (B,), "seq_len")
+    """B, S, dimensions and leading shape of a padded [B, S, heads, D] or packed [S, heads, D]
+    batch, and the pointers of its two integer vectors."""
+    int32 = (_torch or _lazy_torch()).int32
+    lens = seq_len.shape
+    if seq_len.dtype is not int32 or len(lens) != 1 or not seq_len.is_contiguous():
+        raise ValueError("seq_len must be a contiguous int32 vector")
+    B, shape = lens[0], q.shape
     if cu_seqlens is None:
-        if q.dim() != 4 or q.shape[0] != B:
-            raise ValueError(f"a padded batch is [{B}, S, heads, D], not {tuple(q.shape)}")
-        return B, q.shape[1], 4
-    _dense(cu_seqlens, torch.int32, (B + 1,), "cu_seqlens")
-    if q.dim() != 3:
-        raise ValueError(f"a packed batch is [rows, heads, D], not {tuple(q.shape)}")
-    return B, q.shape[0], 3
+        if len(shape) != 4 or shape[0] != B:
+            raise ValueError(f"a padded batch is [{B}, S, heads, D], not {tuple(shape)}")
+        return B, shape[1], 4, seq_len.data_ptr(), None
+    if cu_seqlens.dtype is not int32 or cu_seqlens.shape != (B + 1,) or \
+            not cu_seqlens.is_contiguous():
+        raise ValueError(f"cu_seqlens must be a contiguous int32 vector of {B + 1}")
+    if len(shape) != 3:
+        raise ValueError(f"a packed batch is [rows, heads, D], not {tuple(shape)}")
+    return B, shape[0], 3, seq_len.data_ptr(), cu_seqlens.data_ptr()
 
 
 def _table(page_table, B):
     torch = _torch or _lazy_torch()
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or \
-            page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be int32 [{B}, max_pages] with contiguous rows")
-    return page_table.stride(0), page_table.shape[1]
+    shape = page_table.shape
+    if page_table.dtype is torch.int32 and len(shape) == 2 and shape[0] == B:
+        st = page_table.stride()
+        if st[1] == 1 or shape[1] <= 1:
+            return page_table.data_ptr(), st[0], shape[1]
+    raise ValueError(f"page_table must be int32 [{B}, max_pages] with contiguous rows")
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, phases=None,
@@ -733,27 +747,34 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, p
     D); page_table: int32 [B, max_pages]; seq_len: int32 [B], each sequence's tokens in its own
     pages with the new ones. Positions: positions (int64, one a row), or start + a token's index
     in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place)."""
-    torch = _torch or _lazy_torch()
-    B, S, dims = _batch(k, cu_seqlens, seq_len)
-    lead, D = k.shape[:-2], k_pages.shape[-1]
-    if k.shape[-1] != D or v.shape != k.shape:
-        raise ValueError(f"k and v must have one shape with {D} features, not {tuple(k.shape)} "
+    B, S, dims, lens, cu = _batch(k, cu_seqlens, seq_len)
+    shape = k.shape
+    lead, D = shape[:-2], k_pages.shape[-1]
+    if shape[-1] != D or v.shape != shape:
+        raise ValueError(f"k and v must have one shape with {D} features, not {tuple(shape)} "
                          f"and {tuple(v.shape)}")
-    ts, mp = _table(page_table, B)
+    table, ts, mp = _table(page_table, B)
+    pos = None
     if positions is not None:
-        _dense(positions, torch.int64, lead, "positions")
+        _dense(positions, (_torch or _lazy_torch()).int64, lead, "positions")
+        pos = positions.data_ptr()
+    rot = ph = None
+    if phases is not None:
+        rot, ph = _phases(phases), phases.data_ptr()
     qv = qo = None
     if q is not None:
         if q_out is None:  # rows of no sequence are not written
-            q_out = _empty(stream, q, q.shape, q.dtype, zero=cu_seqlens is not None)
+            q_out = _empty(stream, q, q.shape, q.dtype, zero=cu is not None)
         if q.shape[:-2] != lead or q.shape[-1] != D or q_out.shape != q.shape:
             raise ValueError(f"q and q_out must be {tuple(lead)} + [heads, {D}], not "
                              f"{tuple(q.shape)} and {tuple(q_out.shape)}")
         qv, qo = _heads(q, "q", dims), _heads(q_out, "q_out", dims)
-    upipe_kv_append(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims), _pages(k_pages, v_pages),
-                    page_table, ts, mp, seq_len, cu_seqlens, positions, start, phases, mscale, B,
-                    S, _phases(phases) if phases is not None else 0, interleaved,
-                    stream if stream is not None else _stream(None, k))
+    st = _lib.upipe_kv_append(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims),
+                              _pages(k_pages, v_pages), table, ts, mp, lens, cu, pos, start, ph,
+                              mscale, B, S, rot or 0, 1 if interleaved else 0,
+                              _stream(stream, k))
+    if st:
+        raise UpipeError(st, "upipe_kv_append")
     return q_out if q is not None else None
 
 
@@ -770,42 +791,61 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, prefix_table=None,
     (default: the most that the tensors allow). lse: float32 [B, Hq, S] (packed: [Hq, rows]),
     returned when given or with_lse, else None."""
     torch = _torch or _lazy_torch()
-    B, S, dims = _batch(q, cu_seqlens, seq_len)
+    B, S, dims, lens, cu = _batch(q, cu_seqlens, seq_len)
     cache = _pages(k_pages, v_pages)
-    Hq, D = q.shape[-2:]
+    shape = q.shape
+    Hq, D = shape[-2], shape[-1]
     if D != cache.D:
         raise ValueError(f"q has D={D}, the cache {cache.D}")
-    ts, mp = _table(page_table, B)
+    table, ts, mp = _table(page_table, B)
+    ptable = None
     if prefix_len:
         if prefix_table is None:
             raise ValueError("prefix_len without prefix_table")
         _dense(prefix_table, torch.int32, (prefix_table.numel(),), "prefix_table")
-        if prefix_table.numel() * cache.page_size < prefix_len:
+        if prefix_table.shape[0] * cache.page_size < prefix_len:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages of "
                              f"{cache.page_size} for {prefix_len} tokens")
-    packed = cu_seqlens is not None
-    if packed:
+        ptable = prefix_table.data_ptr()
+    if cu is not None:
         rows, mq = S, S if max_q is None else max_q
     else:
         rows, mq = B * S, S
     ml = max_len if max_len is not None else max(1, mp * cache.page_size)
     # rows of no sequence are not written: zeros in what is made here
     if out is None:
-        out = _empty(stream, q, q.shape, q.dtype, zero=packed)
-    elif out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
-    if lse is not None:
-        _dense(lse, torch.float32, (Hq, S) if packed else (B, Hq, S), "lse")
-    elif with_lse:
-        lse = _empty(stream, q, (Hq, S) if packed else (B, Hq, S), torch.float32, zero=packed)
-    wb = None
-    if workspace is None:
-        wb = 0
-        if rows:
-            wb = max(256, upipe_attn_paged_workspace_bytes(B, rows, Hq, cache.heads, D, prefix_len,
-                                                           mq, ml))
+        out = _empty(stream, q, shape, q.dtype, zero=cu is not None)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
+    lse_ptr = None
+    if lse is not None or with_lse:
+        ls = (Hq, S) if cu is not None else (B, Hq, S)
+        if lse is None:
+            lse = _empty(stream, q, ls, torch.float32, zero=cu is not None)
+        else:
+            _dense(lse, torch.float32, ls, "lse")
+        lse_ptr = lse.data_ptr()
+    qh, oh, sp = _heads(q, "q", dims), _heads(out, "out", dims), _stream(stream, q)
+    wb, ws, own = 0, None, False
+    if workspace is not None:
+        wb, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    elif rows:
+        wb = max(256, upipe_attn_paged_workspace_bytes(B, rows, Hq, cache.heads, D, prefix_len, mq,
+                                                       ml))
+        # torch's allocator without a tensor around the block (8 us less of a call's 21 on the
+        # host), for the stream that the call runs on
+        own = _raw_delete is not None and q.is_cuda and q.get_device() == torch.cuda.current_device()
+        if own:
+            ws = _raw_alloc(wb, sp)
+        else:
             workspace = _empty(stream, q, (wb,), torch.uint8)
-    upipe_attn_paged_fwd(_heads(q, "q", dims), _heads(out, "out", dims), lse, cache, page_table,
-                         ts, mp, seq_len, cu_seqlens, prefix_table, prefix_len, B, S, mq, ml,
-                         workspace, wb, stream if stream is not None else _stream(None, q))
+            ws = workspace.data_ptr()
+    try:
+        st = _lib.upipe_attn_paged_fwd(qh, oh, lse_ptr, cache, table, ts, mp, lens, cu, ptable,
+                                       prefix_len, B, S, mq, ml, ws, wb, sp)
+    finally:
+        if own:
+            _raw_delete(ws)
+    if st:
+        raise UpipeError(st, "upipe_attn_paged_fwd")
     return out, lse

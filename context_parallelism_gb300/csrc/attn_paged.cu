@@ -89,7 +89,7 @@ __device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
 
 // What starting and ending a piece costs, in tiles: each segment counts as so many tiles more, so
 // that a worker with many short sequences has fewer keys. Tile t of a segment is at kOver + t.
-constexpr uint32_t kOver = 2;
+constexpr uint32_t kOver = kSegmentCost;
 
 // One group of segments (the prefix: b = -1, or a sequence): its rows and keys.
 struct Group {

@@ -344,6 +344,10 @@ cudaError_t make_tmap_pages(CUtensorMap* map, const void* base, int D, int page_
                             int64_t n_pages, int64_t slot_stride, int64_t head_stride,
                             int64_t page_stride, int box_rows);
 
+// What a segment (a row tile of a sequence with its keys) counts beside its key tiles when all tiles
+// are cut into shares; the host bounds the sum.
+constexpr uint32_t kSegmentCost = 2;
+
 struct PagedArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;

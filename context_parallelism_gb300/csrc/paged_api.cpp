@@ -340,6 +340,8 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
   const bool has_q = present(q);
   if (has_q && (!present(q_out) || q_out->heads != q->heads))
     return pfail(UPIPE_ERR_INVALID_ARG, "q_out is missing or differs from q in heads");
+  if (2 * static_cast<int64_t>(k->heads) + (has_q ? q->heads : 0) > 65536)
+    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
   if (max_pages < 1 || (B > 1 && table_stride < max_pages))
     return pfail(UPIPE_ERR_INVALID_ARG, "max_pages=%lld table_stride=%lld", (long long)max_pages,
                  (long long)table_stride);
@@ -441,6 +443,18 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   if (st == UPIPE_OK && prefix_len) st = p.add(prefix_table, "prefix_table", 4);
   if (st == UPIPE_OK) st = p.add(workspace, "workspace", 256);
   if (st != UPIPE_OK) return st;
+  const int64_t cap_most = 0x7fffffff - 63;
+  a.cap = static_cast<int>(max_pages > cap_most / cache->page_size
+                               ? cap_most
+                               : max_pages * cache->page_size);
+  // the kernels count in 32 bits: a segment's tiles (rounded up) and kSegmentCost more
+  const double tiles =
+      static_cast<double>(a.segs) * (a.cap / a.ks + 1.0 + kSegmentCost) +
+      static_cast<double>(a.segs_p) * (static_cast<double>(prefix_len) / a.ks + 1.0 + kSegmentCost);
+  if (tiles >= 4294967296.0)
+    return pfail(UPIPE_ERR_UNSUPPORTED,
+                 "%lld row tiles of up to %d keys: more than 2^32 tiles (use narrower page tables)",
+                 (long long)a.segs, a.cap);
   if (workspace_bytes < plan.total)
     return pfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes,
                  plan.total);
@@ -466,17 +480,6 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   a.table_stride = table_stride;
   a.max_pages = max_pages;
   a.n_pages = cache->n_pages;
-  const int64_t cap_most = 0x7fffffff - 63;
-  a.cap = static_cast<int>(max_pages > cap_most / cache->page_size
-                               ? cap_most
-                               : max_pages * cache->page_size);
-  // the kernels count tiles in 32 bits
-  const double tiles = static_cast<double>(a.segs) * (a.cap / a.ks + 1.0) +
-                       static_cast<double>(a.segs_p) * (static_cast<double>(prefix_len) / a.ks + 1.0);
-  if (tiles >= 4294967296.0)
-    return pfail(UPIPE_ERR_UNSUPPORTED,
-                 "%lld row tiles of up to %d keys: more than 2^32 tiles (use narrower page tables)",
-                 (long long)a.segs, a.cap);
   a.seq_len = seq_len;
   a.ptable = prefix_table;
   a.page_size = cache->page_size;

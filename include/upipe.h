@@ -354,7 +354,7 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
  * Rows. B sequences with S new tokens each (cu_rows = NULL; q, k, v, o are [B, S, heads, D]), or
  * a packed batch of S rows in all (cu_rows: device int32 [B + 1], not decreasing; sequence b
  * owns rows cu_rows[b] .. cu_rows[b+1]-1; stride_b is not used). Packed rows that no sequence
- * owns are neither read nor written. A sequence may have no row.
+ * owns have no effect and are not written. A sequence may have no row.
  * Own tokens. seq_len[b] (device int32) counts sequence b's tokens in its own pages, this
  * call's n_b new ones among them: new token i has index j = seq_len[b] - n_b + i, and lies in
  * slot j % page_size of page page_table[b * table_stride + j / page_size] (device int32,
@@ -405,9 +405,11 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
  *   workspace: device, 256-byte aligned, >= upipe_attn_paged_workspace_bytes(...) for the same
  *   sizes (rows = B * S, or S for a packed batch); contents on entry ignored, on exit undefined.
  *   Calls (and captured graphs) that may run at the same time need workspaces of their own.
+ * o is q itself or does not overlap it.
  * Supported: D 64 or 128, Hq a multiple of Hkv, page_size a multiple of 16, up to 2^24 rows,
- * prefix_len up to 2^30. B = 0 or S = 0 does nothing. One key order per shape: results repeat
- * bitwise for the same sizes and hints.
+ * prefix_len up to 2^30, and (each sequence's row tiles x Hkv) x (16-key tiles that max_pages
+ * allows) below 2^32. B = 0 or S = 0 does nothing. One key order per shape: results repeat bitwise
+ * for the same sizes and hints.
  */
 size_t upipe_attn_paged_workspace_bytes(int B, int64_t rows, int Hq, int Hkv, int D,
                                         int64_t prefix_len, int64_t max_q, int64_t max_len);

@@ -436,6 +436,71 @@ def test_steps_captured_into_a_graph_and_two_graphs_with_their_own_workspaces():
             b.q = q
 
 
+@pytest.mark.parametrize("counts,prefix", [([1] * 4, 0), ([1] * 4, 300), ([40] * 4, 0),
+                                           ([3] * 48, 2100)])
+def test_output_in_the_place_of_q(counts, prefix):
+    """o may be q: rows finished by the first kernel, joined ones, and the tensor-core prefix."""
+    b = Batch(counts, ([41, 500, 64, 45] * 12)[:len(counts)], 8, 1, 128, 16, prefix, seed=30)
+    o, lse = b.attend()
+    b.check(o, lse)
+    q = b.q.clone()
+    o2, lse2 = b.attend(out=b.q)
+    assert o2 is b.q and torch.equal(o2, o) and torch.equal(lse2, lse)
+    b.q = q
+
+
+def test_sequences_that_name_the_same_pages():
+    """Two continuations of one history read the same full pages and write their own last one."""
+    b = Batch([1] * 2, [100, 105], 8, 2, 64, 16, 40, seed=31)
+    b.table_np[1, :6] = b.table_np[0, :6]
+    b.table = torch.tensor(b.table_np, dtype=torch.int32, device=DEV)
+    b.check(*b.attend())
+
+
+def test_calls_from_two_threads_on_two_streams():
+    """Each call takes a workspace of its own: results do not depend on what runs beside them."""
+    import threading
+    bs = [Batch([1] * 6, [500, 30, 64, 1, 0, 2000], 16, 4, 128, 16, 1000, seed=32 + i)
+          for i in range(2)]
+    want = [b.attend() for b in bs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(bs[i].attend(stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_workspace_of_a_captured_call():
+    """A workspace made inside a capture belongs to the graph: eager calls between the replays
+    do not get its memory."""
+    b = Batch([1] * 5, [3, 1300, 200, 0, 17], 8, 2, 128, 16, 150, seed=34)
+    want = b.attend()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = b.attend()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        g.replay()
+        other = b.attend(stream=side)
+    torch.cuda.synchronize()
+    for x, y in (want, other):
+        assert torch.equal(o, x) and torch.equal(lse, y)
+
+
 def test_missing_pages_are_reported_and_stay_inside_the_cache():
     """A table entry that names no page (the kernels check it before they follow it): the append
     drops the token, attention reads zeros there, and the status word says so once."""

@@ -111,6 +111,21 @@ def test_attend_refusals(kw, status):
     assert up.upipe_last_error_message()
 
 
+@pytest.mark.parametrize("pages,status", [
+    (2045 * 4, UNS),                              # (2^21 + 1) row tiles, each 2045 + 3: 2^32 and more
+    (2044 * 4, up.UPIPE_ERR_WORKSPACE_TOO_SMALL)  # below: the next check
+])
+def test_tiles_are_counted_in_32_bits(pages, status):
+    """2^24 rows of 8 q-heads on one kv-head: 64-row tiles, 64-key tiles; each row tile counts two
+    tiles more than its keys fill, and the table's last tile may be a part of one."""
+    assert _attend(q=H(8), o=H(8), cache=C(heads=1), B=1, S=1 << 24, mp=pages, prefix=0,
+                   max_len=1) == status, up.upipe_last_error_message()
+
+
+def test_append_refuses_more_heads_than_a_launch_counts():
+    assert _append(k=H(40000), v=H(40000), cache=C(heads=40000)) == UNS
+
+
 @pytest.mark.parametrize("args", [
     (0, 4, 8, 2, 64, 0, 1, 64), (1, 0, 8, 2, 64, 0, 1, 64), (1, 4, 6, 4, 64, 0, 1, 64),
     (1, 4, 8, 2, 96, 0, 1, 64), (1, 4, 8, 2, 64, -1, 1, 64), (1, 4, 8, 2, 64, 0, 0, 64),

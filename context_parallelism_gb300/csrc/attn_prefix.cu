@@ -17,8 +17,10 @@
 // weights are (65536 keys, 128 sequences x 2 tokens, 64 q-heads: 384 -> 348 us). D 128 has that
 // room only with 64-key tiles, whose smaller products cost more than they hide (877 -> 1200 us for
 // 96 x 5 tokens on 131000 keys), as does Q in tensor memory there (1390 us). What bounds two row
-// tiles of D 128: the chain of one of them, softmax 1650 cycles, its two products 1200, and the
-// waits between them 700; the other one's runs in its gaps.
+// tiles of D 128: the chain of one of them, its softmax (about 1500 cycles), its two products (1200)
+// and the waits between them (700); the other one's runs in its gaps. Two threads a row (875 -> 929
+// us) and scores read 32 columns at a time (949 us: each read waits behind the products' traffic to
+// tensor memory) made the chain no shorter.
 //
 // Threads: warps 0-3 and 4-7 softmax (and the load of Q), warp 8 products, warp 9 (and 10) TMA: one
 // lane per box of page rows, its page looked up while the stage is still in use.
@@ -34,7 +36,15 @@ namespace {
 // issues both held 16-token pages to 402 us for 2.1 GB, against 335; where the tensor pipe sets
 // the speed the eleventh warp costs 5 %).
 constexpr int threads(bool pair) { return pair ? 320 : 352; }
-constexpr float kRescaleLog2 = 8.0f;
+// A row's weights are exp2(s - m) with m some 24 above the largest score of its first tile: below
+// 2^-24 then, where a float and a bf16 are as exact as near 1. m need not follow the maximum, so a
+// tile's weights wait for no maximum of their own; a tile whose weights sum to more than 1 (its
+// maximum is 17 or more above what m was made from) is done again with a new m, and O and the sums
+// are scaled. Taking every tile's maximum first, and rescaling from 8 above m on, held 96 x 5 tokens
+// on 131000 keys, where a few keys stand out, to 890 us against 850.
+constexpr float kHeadroom = 24.0f;
+constexpr float kLargeSum = 1.0f;
+constexpr float kLowest = -3.0e38f;  // m of a row that has only -inf so far: any score is done again
 
 template <int D, bool kPair>
 struct XLayout {
@@ -344,58 +354,69 @@ __global__ void __launch_bounds__(threads(kPair), 1)
         fence_proxy_async_smem();
       }
       if (work) {
-        uint32_t ra[64], rb[64];
-        tmem_ld64_nowait(tS + lane_off, ra);
-        tmem_ld64_nowait(tS + lane_off + 64, rb);
-        tmem_wait_ld_dep64(ra);
-        tmem_reg_dep64(rb);
-        if constexpr (kOwnP) s_read();
-        if (valid < 128) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (i >= valid) ra[i] = __float_as_uint(-INFINITY);
-            if (64 + i >= valid) rb[i] = __float_as_uint(-INFINITY);
-          }
-        }
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], __uint_as_float(ra[i]), __uint_as_float(ra[i + 1]));
-          mq[((i >> 1) + 2) & 3] =
-              fmax3(mq[((i >> 1) + 2) & 3], __uint_as_float(rb[i]), __uint_as_float(rb[i + 1]));
-        }
-        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        const float m_new = fmaxf(m_used, mx * a.scale_log2);
         float alpha = 1.f;
-        const bool upd = m_new > m_used + kRescaleLog2;
-        if (upd) {
-          alpha = ex2_approx(m_used - m_new);
-          m_used = m_new;
-        }
-        lb *= alpha;
-        lf *= alpha;
-        const float mb = (m_used == -INFINITY) ? 0.f : m_used;
-        const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
-        const uint64_t nm2 = f2_pack(-mb, -mb);
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        uint64_t f0 = 0, f1 = 0;  // pairs of sums of the fp32 weights, for lse alone
+        bool upd = false;
+        uint32_t ra[64], rb[64];
+        float sum;
+        uint64_t f0, f1;  // pairs of sums of the fp32 weights, for lse alone
+        bool fresh = n == 0;  // m is to be made
+        while (true) {
+          tmem_ld64_nowait(tS + lane_off + 64, rb);
+          tmem_ld64_nowait(tS + lane_off, ra);
+          tmem_wait_ld_dep64(ra);
+          tmem_reg_dep64(rb);
+          if (valid < 128) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x0, x1;
-          f2_unpack(ffma2(f2_pack_u(ra[2 * i], ra[2 * i + 1]), sl2, nm2), x0, x1);
-          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          if (kLse) f0 = fadd2(f0, f2_pack(e0, e1));
-          ra[i] = pack_bf16(e0, e1);
-          add_bf16x2(s0, s1, ra[i]);
-        }
+            for (int i = 0; i < 64; ++i) {
+              if (i >= valid) ra[i] = __float_as_uint(-INFINITY);
+              if (64 + i >= valid) rb[i] = __float_as_uint(-INFINITY);
+            }
+          }
+          if (fresh) {
+            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x0, x1;
-          f2_unpack(ffma2(f2_pack_u(rb[2 * i], rb[2 * i + 1]), sl2, nm2), x0, x1);
-          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          if (kLse) f1 = fadd2(f1, f2_pack(e0, e1));
-          rb[i] = pack_bf16(e0, e1);
-          add_bf16x2(s2, s3, rb[i]);
+            for (int i = 0; i < 64; ++i)
+              mq[i & 3] = fmax3(mq[i & 3], __uint_as_float(ra[i]), __uint_as_float(rb[i]));
+            const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+            const float to = fmaxf(mx * a.scale_log2 + kHeadroom, kLowest);
+            if (to > m_used) {
+              alpha = ex2_approx(m_used - to);
+              m_used = to;
+              upd = true;
+            }
+          }
+          const uint64_t sl2 = f2_pack(a.scale_log2, a.scale_log2);
+          const uint64_t nm2 = f2_pack(-m_used, -m_used);
+          float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+          f0 = f1 = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1;
+            f2_unpack(ffma2(f2_pack_u(ra[2 * i], ra[2 * i + 1]), sl2, nm2), x0, x1);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            if (kLse) f0 = fadd2(f0, f2_pack(e0, e1));
+            ra[i] = pack_bf16(e0, e1);
+            add_bf16x2(sa[2 * (i & 1)], sa[2 * (i & 1) + 1], ra[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1;
+            f2_unpack(ffma2(f2_pack_u(rb[2 * i], rb[2 * i + 1]), sl2, nm2), x0, x1);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            if (kLse) f1 = fadd2(f1, f2_pack(e0, e1));
+            rb[i] = pack_bf16(e0, e1);
+            add_bf16x2(sb[2 * (i & 1)], sb[2 * (i & 1) + 1], rb[i]);
+          }
+          sum = ((sa[0] + sa[1]) + (sb[0] + sb[1])) + ((sa[2] + sa[3]) + (sb[2] + sb[3]));
+          if (fresh || !__any_sync(0xffffffffu, sum > kLargeSum)) break;
+          fresh = true;
+        }
+        if constexpr (kOwnP) s_read();
+        lb = lb * alpha + sum;
+        if (kLse) {
+          float g0, g1;
+          f2_unpack(fadd2(f0, f1), g0, g1);
+          lf = lf * alpha + (g0 + g1);
         }
         // P's own columns and O are free once PV_w of the tile before has run
         if (kOwnP && n > 0) {
@@ -422,12 +443,6 @@ __global__ void __launch_bounds__(threads(kPair), 1)
             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
             tmem_st32(tO + lane_off + c * 32, r);
           }
-        }
-        lb += (s0 + s1) + (s2 + s3);
-        if (kLse) {
-          float g0, g1;
-          f2_unpack(fadd2(f0, f1), g0, g1);
-          lf += g0 + g1;
         }
         tmem_wait_st();
       } else {

@@ -217,6 +217,19 @@ def test_large_scores_and_dominant_keys():
     b.check(*b.attend())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G,prefix", [(40, 16, 1500), (24, 4, 4000)])
+def test_scores_that_rise_along_the_prefix(n, G, prefix, D):
+    """Two row tiles, and two key streams, of the tensor-core kernel: later keys whose scores lie tens,
+    hundreds and thousands above all before them, for single heads' rows or for all."""
+    b = Batch([1] * n, [9] * n, G, 1, D, 16, prefix, seed=12)
+    up.upipe_sync_status()
+    for at, by in ((200, 6.0), (300, 30.0), (301, 30.0), (700, 60.0), (1100, 400.0), (1400, 900.0)):
+        b.kp[int(b.ptable_np[at // 16]), at % 16] *= by
+    b.q[::3] *= 0.01
+    b.check(*b.attend())
+
+
 def test_strided_q_and_output():
     b = Batch([2] * 3, [5, 70, 33], 8, 2, 64, 16, 90, seed=10)
     o, lse = b.attend()

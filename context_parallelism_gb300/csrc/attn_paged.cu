@@ -994,16 +994,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   grid_dependency_wait();
 }
 
-// Joins the parts of a row: kWarps warps per (row, head), warp u taking the parts u, u + kWarps,
-// ... of each 32; up to eight numerators are in flight per warp. The order of the sums is fixed.
-// A row's parts are the prefix kernel's, then the pieces that desc names for the prefix and for
-// its own keys. Bound: latency (a few dependent loads) for few rows, L2 for many.
+// Joins the parts of a row: kWarps warps per (row, head), warp u taking the parts u, u + kWarps, ...,
+// their statistics 32 at a time (one a lane) with a running maximum, their numerators eight at a
+// time; the warps' sums are joined in shared memory. The order of the sums is fixed. A row's parts
+// are the prefix kernel's, then the pieces that desc names for the prefix and for its own keys.
+// Bound: latency (dependent loads) for few rows, L2 for many. The prefix kernel's parts lie where the
+// row says, so their statistics and the first eight numerators are asked for together with desc.
 template <int D, int kWarps>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
   constexpr int E = D / 32;
   constexpr int kRows = 8 / kWarps;  // rows per block
-  constexpr int kQ = 32 / kWarps < 8 ? 32 / kWarps : 8;  // parts in flight per warp
-  __shared__ float red[kWarps > 1 ? 8 : 1][D + 2];
+  constexpr int kQ = 8;              // numerators in flight per warp
+  __shared__ float red[kWarps > 1 ? 8 : 1][D + 3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = warp % kWarps;
   const int64_t x = blockIdx.x * int64_t(kRows) + warp / kWarps;
@@ -1014,19 +1016,32 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
   grid_dependency_wait();
   const int64_t step = a.rows * a.Hq;
   const int64_t at = t * a.Hq + h;
-  int n_x = 0, n_p = 0, n_o = 0;
+  const int n_x = live && a.splits_x ? a.splits_p : 0;
+  int n_p = 0, n_o = 0;
   int64_t first_p = 0, first_o = 0;
+  auto load = [&](const float* o, float (&r)[E]) {
+    if (E == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(o + lane * E);
+      r[0] = f.x; r[1] = f.y; r[E - 2] = f.z; r[E - 1] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(o + lane * E);
+      r[0] = f.x; r[1] = f.y;
+    }
+  };
+  int2 own = make_int2(0, 0), pre = make_int2(0, 0);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float r[kQ][E];
   if (live) {
-    const int2 own = a.desc[step + at];
+    own = a.desc[step + at];
+    if (a.prefix && !a.splits_x) pre = a.desc[at];
+    if (lane * kWarps + u < n_x) v = a.part_ml[(lane * kWarps + u) * step + at];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)  // one that was not written (no keys) is passed over below
+      if (q * kWarps + u < n_x) load(a.part_o + ((q * kWarps + u) * step + at) * D, r[q]);
     first_o = own.x;
     n_o = own.y;
-    if (a.splits_x) {
-      n_x = a.splits_p;
-    } else if (a.prefix) {
-      const int2 pre = a.desc[at];
-      first_p = pre.x;
-      n_p = pre.y;
-    }
+    first_p = pre.x;
+    n_p = pre.y;
     live = n_o != 0;  // finished by the kernel before
     // stay inside the slots whatever desc holds (cu_rows that decrease)
     const int64_t top = a.n_slots * a.mt;
@@ -1035,8 +1050,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
   }
   if (kWarps == 1 && !live) return;
   const int parts = live ? n_x + n_p + n_o : 0;
-  // row of statistics and numerators of part p
-  auto where = [&](int p, const float4** ml, const float** o) {
+  const int mine = parts > u ? (parts - u + kWarps - 1) / kWarps : 0;
+  // row of statistics and numerators of this warp's i-th part
+  auto where = [&](int i, const float4** ml, const float** o) {
+    const int p = i * kWarps + u;
     if (p < n_x) {
       *ml = a.part_ml + p * step + at;
       *o = a.part_o + (p * step + at) * D;
@@ -1047,66 +1064,49 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
       *o = a.slot_o + s * D;
     }
   };
-  float M = -INFINITY;
-  for (int p = lane; p < parts; p += 32) {
-    const float4* ml;
-    const float* o;
-    where(p, &ml, &o);
-    const float4 v = *ml;
-    if (v.z != 0.f) M = fmaxf(M, v.x);
-  }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float lb = 0.f, lf = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    // lane p: the weight of part p0 + p; a part without keys (sum exactly 0) has written no
-    // numerator and is passed over, one with NaN is not
-    float w = -1.f;
-    if (p0 + lane < parts) {
-      const float4* ml;
-      const float* o;
-      where(p0 + lane, &ml, &o);
-      const float4 v = *ml;
-      if (v.z != 0.f) {
-        w = ex2_approx(v.x - M);
-        if (lane % kWarps == u) {
-          lb += w * v.y;
-          lf += w * v.z;
-        }
-      }
+  float M = -INFINITY, lb = 0.f, lf = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const float4* ml;
+    const float* o;
+    if (i0 + lane < mine && (i0 || lane * kWarps + u >= n_x)) {
+      where(i0 + lane, &ml, &o);
+      v = *ml;
     }
+    // lane i: the weight of part i0 + i; a part without keys (sum exactly 0) has written no
+    // numerator and is passed over, one with NaN is not
+    const bool has = i0 + lane < mine && v.z != 0.f;
+    float top = has ? fmaxf(M, v.x) : M;
 #pragma unroll
-    for (int q0 = 0; q0 < 32; q0 += kQ * kWarps) {
-      float r[kQ][E], wq[kQ];
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float old = M == -INFINITY ? 0.f : ex2_approx(M - top);
+    M = top;
+    const float w = has ? ex2_approx(v.x - M) : -1.f;
+    lb = lb * old + (has ? w * v.y : 0.f);
+    lf = lf * old + (has ? w * v.z : 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+#pragma unroll 1
+    for (int q0 = 0; q0 < 32 && i0 + q0 < mine; q0 += kQ) {
+      float wq[kQ];
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
-        const int p = q0 + q * kWarps + u;
-        wq[q] = __shfl_sync(0xffffffffu, w, p);
-        if (wq[q] >= 0.f || wq[q] != wq[q]) {
-          const float4* ml;
-          const float* o;
-          where(p0 + p, &ml, &o);
-          if (E == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(o + lane * E);
-            r[q][0] = f.x; r[q][1] = f.y; r[q][E - 2] = f.z; r[q][E - 1] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(o + lane * E);
-            r[q][0] = f.x; r[q][1] = f.y;
-          }
-        } else {
-          wq[q] = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) r[q][e] = 0.f;
+        wq[q] = __shfl_sync(0xffffffffu, w, q0 + q);
+        const bool there = wq[q] >= 0.f || wq[q] != wq[q];
+        if (there && (i0 + q0 || q * kWarps + u >= n_x)) {
+          where(i0 + q0 + q, &ml, &o);
+          load(o, r[q]);
         }
+        if (!there) wq[q] = -1.f;
       }
 #pragma unroll
       for (int q = 0; q < kQ; ++q)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wq[q] * r[q][e];
-      if (p0 + q0 + kQ * kWarps >= parts) break;
+        for (int e = 0; e < E; ++e)
+          if (!(wq[q] < 0.f)) acc[e] += wq[q] * r[q][e];
     }
   }
 #pragma unroll
@@ -1120,6 +1120,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     if (lane == 0) {
       red[warp % 8][D] = lb;
       red[warp % 8][D + 1] = lf;
+      red[warp % 8][D + 2] = M;
     }
     __syncthreads();
     if (u != 0 || !live) return;
@@ -1127,11 +1128,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
+    for (int v2 = 0; v2 < kWarps; ++v2) M = fmaxf(M, red[(warp + v2) % 8][D + 2]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += red[(warp + v) % 8][lane * E + e];
-      lb += red[(warp + v) % 8][D];
-      lf += red[(warp + v) % 8][D + 1];
+    for (int v2 = 0; v2 < kWarps; ++v2) {
+      const float* rv = red[(warp + v2) % 8];
+      const float w = rv[D + 2] == -INFINITY ? 0.f : ex2_approx(rv[D + 2] - M);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * rv[lane * E + e];
+      lb += w * rv[D];
+      lf += w * rv[D + 1];
     }
   }
   const float inv = lb == 0.f ? 0.f : 1.f / lb;  // no key in sight: zeros

@@ -16,7 +16,8 @@
 // of D 64 tensor memory has room for P beside S: then S_w's next tile is computed while this one's
 // weights are (65536 keys, 128 sequences x 2 tokens, 64 q-heads: 384 -> 348 us). D 128 has that
 // room only with 64-key tiles, whose smaller products cost more than they hide (877 -> 1200 us for
-// 96 x 5 tokens on 131000 keys), as does Q in tensor memory there (1390 us). What bounds two row
+// 96 x 5 tokens on 131000 keys), as does Q in tensor memory there (1390 us), and as do two products
+// of 64 keys a tile, the first one's columns filled while P lies over the second's (1103 us). What bounds two row
 // tiles of D 128: the chain of one of them, its softmax (about 1500 cycles), its two products (1200)
 // and the waits between them (700); the other one's runs in its gaps. Two threads a row (875 -> 929
 // us) and scores read 32 columns at a time (949 us: each read waits behind the products' traffic to

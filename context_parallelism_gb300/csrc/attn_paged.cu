@@ -338,6 +338,12 @@ __device__ __forceinline__ int row_limit(const PagedArgs& a, const Piece& p, int
   return min(p.keys, p.before + i + 1);
 }
 
+template <typename T>
+__device__ __forceinline__ T* shfl_ptr(T* p, int src) {
+  return reinterpret_cast<T*>(
+      __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
+}
+
 // ---- up to 16 rows: one warp a worker --------------------------------------------------------
 //
 // S^T = K Q^T and O^T += V^T P^T: keys and features fill the instruction's 16 rows, the few query
@@ -506,17 +512,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       j = 0;
       p = pieces[n_done % L::kPieces];
       if (p.n_kt < 0) break;
+      // Rows are found once, lane r row r, and handed on: the code of a step is short.
+      const __nv_bfloat16* my_q = q_row(a, p, lane % MT);
+      const int my_lim = row_limit(a, p, lane % MT);
       // B fragments of Q^T: row lane/4 of each tile, features (lane%4)*2 and +8 of each 16
 #pragma unroll
       for (int c = 0; c < NR; ++c) {
-        const __nv_bfloat16* qp = q_row(a, p, c * 8 + (lane >> 2));
+        const __nv_bfloat16* qp = shfl_ptr(my_q, c * 8 + (lane >> 2));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             qf[c][k][e] = qp ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + e * 8 + (lane & 3) * 2) : 0u;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) lim[c][e] = row_limit(a, p, c * 8 + (lane & 3) * 2 + e);
+        for (int e = 0; e < 2; ++e)
+          lim[c][e] = __shfl_sync(0xffffffffu, my_lim, c * 8 + (lane & 3) * 2 + e);
       }
 #pragma unroll
       for (int c = 0; c < NR; ++c) {
@@ -636,32 +646,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           lf[c][e] += __shfl_xor_sync(0xffffffffu, lf[c][e], x);
         }
     // row (lane%4)*2 + e of a tile: this lane has features lane/4 + 8 i of it
+    RowOut mine = {nullptr, nullptr, nullptr, nullptr};
+    if (p.row0 + lane % MT < p.n_rows) mine = row_out(a, p, lane % MT, MT, D, lane < MT);
+    const bool sole = __any_sync(0xffffffffu, mine.o != nullptr);
+    const int d0 = lane >> 2;
+    if (sole) {
 #pragma unroll
-    for (int c = 0; c < NR; ++c)
+      for (int c = 0; c < NR; ++c)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = c * 8 + (lane & 3) * 2 + e;
-        if (p.row0 + r >= p.n_rows) continue;
-        const int d0 = lane >> 2;
-        const RowOut w = row_out(a, p, r, MT, D, d0 == 0);
-        if (w.o) {
+        for (int e = 0; e < 2; ++e) {
+          __nv_bfloat16* to = shfl_ptr(mine.o, c * 8 + (lane & 3) * 2 + e);
+          float* to_lse = shfl_ptr(mine.lse, c * 8 + (lane & 3) * 2 + e);
+          if (!to) continue;
           const float inv = lb[c][e] == 0.f ? 0.f : 1.f / lb[c][e];
 #pragma unroll
           for (int n = 0; n < D / 16; ++n)
 #pragma unroll
             for (int f = 0; f < 2; ++f)
-              w.o[n * 16 + f * 8 + d0] = __float2bfloat16_rn(o[c][n][2 * f + e] * inv);
-          if (w.lse && d0 == 0) *w.lse = (m[c][e] + log2f(lf[c][e])) * 0.69314718055994530942f;
-        } else if (w.part) {
+              to[n * 16 + f * 8 + d0] = __float2bfloat16_rn(o[c][n][2 * f + e] * inv);
+          if (to_lse && d0 == 0) *to_lse = (m[c][e] + log2f(lf[c][e])) * 0.69314718055994530942f;
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NR; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* to = shfl_ptr(mine.part, c * 8 + (lane & 3) * 2 + e);
+          float4* to_ml = shfl_ptr(mine.ml, c * 8 + (lane & 3) * 2 + e);
+          if (!to) continue;
           if (lf[c][e] != 0.f) {  // NaN goes through
 #pragma unroll
             for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-              for (int f = 0; f < 2; ++f) w.part[n * 16 + f * 8 + d0] = o[c][n][2 * f + e];
+              for (int f = 0; f < 2; ++f) to[n * 16 + f * 8 + d0] = o[c][n][2 * f + e];
           }
-          if (d0 == 0) *w.ml = make_float4(m[c][e], lb[c][e], lf[c][e], 0.f);
+          if (d0 == 0) *to_ml = make_float4(m[c][e], lb[c][e], lf[c][e], 0.f);
         }
-      }
+    }
     ++n_done;
     fresh = true;
   }

@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     // row (lane%4)*2 + e of a tile: this lane has features lane/4 + 8 i of it
     RowOut mine = {nullptr, nullptr, nullptr, nullptr};
     if (p.row0 + lane % MT < p.n_rows) mine = row_out(a, p, lane % MT, MT, D, lane < MT);
-    const bool sole = __any_sync(0xffffffffu, mine.o != nullptr);
+    const bool sole = p.parts == 1 && a.prefix == 0;
     const int d0 = lane >> 2;
     if (sole) {
 #pragma unroll
@@ -873,11 +873,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int r_lo = lane >> 2;
       uint32_t qf[D / 16][4];
       int lim[2];
+      const int my_row = warp * 16 + (lane & 15);  // found here once for the warp
+      const __nv_bfloat16* my_q = q_row(a, p, my_row);
+      const int my_lim = row_limit(a, p, my_row);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = warp * 16 + r_lo + 8 * e;
-        const __nv_bfloat16* qp = q_row(a, p, r);
-        lim[e] = row_limit(a, p, r);
+        const __nv_bfloat16* qp = shfl_ptr(my_q, r_lo + 8 * e);
+        lim[e] = __shfl_sync(0xffffffffu, my_lim, r_lo + 8 * e);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -980,30 +982,36 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(empty + s);
       }
       if (!ok) break;
+      RowOut mine = {nullptr, nullptr, nullptr, nullptr};
+      if (p.row0 + my_row < p.n_rows) mine = row_out(a, p, my_row, MT, D, lane < 16);
+      const bool sole = p.parts == 1 && a.prefix == 0;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         lb[e] += __shfl_xor_sync(0xffffffffu, lb[e], 1);
         lb[e] += __shfl_xor_sync(0xffffffffu, lb[e], 2);
         lf[e] += __shfl_xor_sync(0xffffffffu, lf[e], 1);
         lf[e] += __shfl_xor_sync(0xffffffffu, lf[e], 2);
-        const int r = warp * 16 + r_lo + 8 * e;
-        if (p.row0 + r >= p.n_rows) continue;
-        const RowOut w = row_out(a, p, r, MT, D, (lane & 3) == 0);
-        if (w.o) {
+        if (sole) {
+          __nv_bfloat16* to = shfl_ptr(mine.o, r_lo + 8 * e);
+          float* to_lse = shfl_ptr(mine.lse, r_lo + 8 * e);
+          if (!to) continue;
           const float inv = lb[e] == 0.f ? 0.f : 1.f / lb[e];
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<uint32_t*>(w.o + n * 8 + (lane & 3) * 2) =
+            *reinterpret_cast<uint32_t*>(to + n * 8 + (lane & 3) * 2) =
                 pack_bf16(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-          if (w.lse && (lane & 3) == 0) *w.lse = (m[e] + log2f(lf[e])) * 0.69314718055994530942f;
-        } else if (w.part) {
+          if (to_lse && (lane & 3) == 0) *to_lse = (m[e] + log2f(lf[e])) * 0.69314718055994530942f;
+        } else {
+          float* to = shfl_ptr(mine.part, r_lo + 8 * e);
+          float4* to_ml = shfl_ptr(mine.ml, r_lo + 8 * e);
+          if (!to) continue;
           if (lf[e] != 0.f) {  // NaN goes through
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<float2*>(w.part + n * 8 + (lane & 3) * 2) =
+              *reinterpret_cast<float2*>(to + n * 8 + (lane & 3) * 2) =
                   make_float2(o[n][2 * e], o[n][2 * e + 1]);
           }
-          if ((lane & 3) == 0) *w.ml = make_float4(m[e], lb[e], lf[e], 0.f);
+          if ((lane & 3) == 0) *to_ml = make_float4(m[e], lb[e], lf[e], 0.f);
         }
       }
     }
@@ -1249,10 +1257,19 @@ void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
   const bool warps = a->mt != 64;
   const int ks = a->ks = warps ? 2048 / a->D : 64;
   a->least = warps ? 64 / ks : 1;
-  const int64_t tiles = segs * ((max_len + ks - 1) / ks) + segs_p * ((a->prefix + ks - 1) / ks);
+  const int64_t t_o = (max_len + ks - 1) / ks, t_p = (a->prefix + ks - 1) / ks;
+  const int64_t tiles = segs * t_o + segs_p * t_p;
   const int64_t want = (tiles + a->least - 1) / a->least, most_blocks = warps ? kSms : 2 * kSms;
   a->grid = static_cast<unsigned>(want < most_blocks ? want : most_blocks);
-  a->n_slots = segs + segs_p + static_cast<int64_t>(a->grid) * (warps ? kWarps : 1);
+  const int64_t workers = static_cast<int64_t>(a->grid) * (warps ? kWarps : 1);
+  a->n_slots = segs + segs_p + workers;
+  // The join takes eight warps a row where rows are few and have many parts each (us of a step of
+  // 32 q-heads on 8 kv-heads of 128, one warp / eight: 8 rows with 13 parts 18.5 / 16.5, 16 rows
+  // with 34 parts 24.8 / 22.7; 24 rows with 5 parts 14.7 / 18.2).
+  const int64_t all = segs * (kOver + t_o) + segs_p * (kOver + t_p);
+  const int64_t share = all / workers > a->least ? all / workers : a->least;
+  const int64_t parts = a->splits_p + (segs_p ? (kOver + t_p) / share + 1 : 0) + (kOver + t_o) / share + 1;
+  a->wide = a->rows * a->Hq < 1024 && parts > 8;
 }
 
 cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap* k_map,
@@ -1272,9 +1289,8 @@ cudaError_t launch_attn_paged(const PagedArgs& a, const CUtensorMap* k_map,
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
-  // Eight warps a row where rows alone would leave most of the GPU's warps idle.
   const int64_t rows = a.rows * a.Hq;
-  const bool wide = rows < 1024;
+  const bool wide = a.wide;
   const int64_t blocks = wide ? rows : (rows + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 n(static_cast<unsigned>(blocks)), th(256);

@@ -386,6 +386,7 @@ struct PagedArgs {
   int mt;                    // rows per tile: 8, 16 or 64
   int ks;                    // keys per tile
   int least;                 // tiles of the smallest share
+  bool wide;                 // eight warps a row in the join
   unsigned grid;
   uint32_t* err;
 };

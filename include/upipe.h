@@ -404,7 +404,8 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
  *   results.
  *   workspace: device, 256-byte aligned, >= upipe_attn_paged_workspace_bytes(...) for the same
  *   sizes (rows = B * S, or S for a packed batch); contents on entry ignored, on exit undefined.
- *   Calls (and captured graphs) that may run at the same time need workspaces of their own.
+ *   Calls (and captured graphs) that may run at the same time need workspaces of their own, which
+ *   live as long as the graph.
  * o is q itself or does not overlap it.
  * Supported: D 64 or 128, Hq a multiple of Hkv, page_size a multiple of 16, up to 2^24 rows,
  * prefix_len up to 2^30, and (each sequence's row tiles x Hkv) x (16-key tiles that max_pages

@@ -411,7 +411,7 @@ def test_steps_captured_into_a_graph_and_two_graphs_with_their_own_workspaces():
     """A captured step follows lengths, tables and inputs that change between replays; two graphs
     with workspaces of their own replay side by side."""
     up.upipe_sync_status()
-    runs = []
+    runs, kept = [], []
     for seed in (40, 50):
         b = Batch([1] * 5, [3, 64, 200, 0, 17], 8, 2, 128, 16, 150, seed=seed)
         k, v = _bf((5, 1, 2, 128), seed + 5), _bf((5, 1, 2, 128), seed + 6)
@@ -431,6 +431,7 @@ def test_steps_captured_into_a_graph_and_two_graphs_with_their_own_workspaces():
         with torch.cuda.graph(g):
             step()
         runs.append((b, k, v, qn, o, lse, g))
+        kept.append((ph, ws))  # a graph does not own what it was given
     for lens in ([3, 64, 200, 0, 17], [4, 61, 201, 0, 1]):
         streams = [torch.cuda.Stream(), torch.cuda.Stream()]
         for (b, k, v, qn, o, lse, g), s in zip(runs, streams):

@@ -1223,6 +1223,7 @@ bool prefix_on_tc(const PagedArgs& a, int64_t rows_o) {
 }  // namespace
 
 void plan_paged(PagedArgs* a, int64_t max_q, int64_t max_len) {
+  if (max_len > 0x7fffffff) max_len = 0x7fffffff;  // lengths are 32-bit; a hint may be anything
   const int64_t rows_o = max_q * a->G, rows_p = a->rows * a->G;
   a->splits_x = a->splits_p = a->tiles_p = 0;
   if (prefix_on_tc(*a, rows_o)) {

@@ -152,6 +152,13 @@ def test_workspace_is_bounded_by_the_rows_and_the_blocks():
             most + 16 * rows * Hq + 5 * 256
 
 
+@pytest.mark.parametrize("hint", [1 << 31, 1 << 40, 1 << 58, (1 << 63) - 1])
+def test_length_hints_of_any_size(hint):
+    for args in [(64, 64, 32, 8, 128, 1000, 1), (1, 1, 32, 8, 64, 0, 1 << 62), (3, 40, 8, 8, 64, 0, 40)]:
+        assert up.upipe_attn_paged_workspace_bytes(*args, hint) == \
+            up.upipe_attn_paged_workspace_bytes(*args, (1 << 31) - 1) > 0
+
+
 def _t(*shape, dtype=torch.bfloat16):
     return torch.zeros(shape, dtype=dtype)
 

@@ -344,6 +344,33 @@ __device__ __forceinline__ T* shfl_ptr(T* p, int src) {
       __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
 }
 
+// Values that some row of a tile must not see. A key beyond a row's causal limit has weight 0, and
+// 0 * v is 0 only for a finite v: an infinity or NaN there (a later drafted token's) would reach
+// rows that end before it. So where a limit lies inside the tile, its V is looked over from the
+// first such key on, and if anything is not finite the tile's products are taken key by key, each
+// row adding only what it sees.
+
+// Whether rows [r0, KS) of a stage's V hold an infinity or NaN; the same in every lane.
+template <int D, int KS>
+__device__ __forceinline__ bool any_not_finite(uint32_t sv, int r0, int lane) {
+  constexpr uint32_t kLo = 0x7f80u, kHi = 0x7f800000u;  // exponents of the two halves
+  bool bad = false;
+  for (int x = r0 * (D / 8) + lane; x < KS * (D / 8); x += 32) {
+    const int r = x / (D / 8), ch = x % (D / 8);
+    uint32_t w[4];
+    ld_shared_v4(w, sv + (ch >> 3) * (KS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad = bad || (w[i] & kLo) == kLo || (w[i] & kHi) == kHi;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+// Address of feature f (of an even pair) of row r in a stage's V.
+template <int KS>
+__device__ __forceinline__ uint32_t v_at(uint32_t sv, int r, int f) {
+  return sv + (f >> 6) * (KS * 128) + r * 128 + ((((f >> 3) & 7) ^ (r & 7)) << 4) + (f & 7) * 2;
+}
+
 // ---- up to 16 rows: one warp a worker --------------------------------------------------------
 //
 // S^T = K Q^T and O^T += V^T P^T: keys and features fill the instruction's 16 rows, the few query
@@ -363,7 +390,10 @@ struct DLayout {
   static constexpr int kBytes = kPiece + kWarps * kPieces * static_cast<int>(sizeof(Piece)) + 1024;
 };
 
-template <int D, int NR>
+// kSeveral: a sequence may have several new tokens, so a row may end before the others. (With one
+// token each no limit lies inside a tile; the branch before the products, which they cannot be moved
+// across, cost 1.5 % of 131072 keys.)
+template <int D, int NR, bool kSeveral>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   using L = DLayout<D, NR>;
@@ -499,6 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   bool fresh = true, ok = true;
   uint32_t qf[NR][D / 16][2];
   int lim[NR][2];  // key limits of this thread's two statistics rows of each tile
+  int lim_min = 0;  // the least of the tile's rows
   float o[NR][D / 16][4];
   float m[NR][2], lb[NR][2], lf[NR][2];
   // One turn: fill the ring, then a tile. (Each part stands in the code once: what a step runs for
@@ -515,6 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       // Rows are found once, lane r row r, and handed on: the code of a step is short.
       const __nv_bfloat16* my_q = q_row(a, p, lane % MT);
       const int my_lim = row_limit(a, p, lane % MT);
+      if (kSeveral) lim_min = __reduce_min_sync(0xffffffffu, my_q ? my_lim : p.keys);
       // B fragments of Q^T: row lane/4 of each tile, features (lane%4)*2 and +8 of each 16
 #pragma unroll
       for (int c = 0; c < NR; ++c) {
@@ -619,18 +651,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           sc[c][t][1] = __uint_as_float(pb[1]);
         }
       }
+      if (kSeveral && min(k0 + KS, p.keys) > lim_min &&
+          any_not_finite<D, KS>(sv, max(lim_min - k0, 0), lane)) {
+#pragma unroll 1
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int t = 0; t < KS / 16; ++t)
+          for (int c = 0; c < NR; ++c) {
+            uint32_t w = 0;  // the word of P^T that holds key k
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          const int r = t * 16 + ((lane >> 4) << 3) + (lane & 7);
-          const int ch = (d & 3) * 2 + ((lane >> 3) & 1);
-          uint32_t va[4];
-          ldsm4_t(va, sv + (d >> 2) * kHalf + r * 128 + ((ch ^ (r & 7)) << 4));
+            for (int x = 0; x < KS / 8; ++x)
+              if (x == k >> 3) w = __float_as_uint(sc[c][x >> 1][x & 1]);
+            float pk[2];
 #pragma unroll
-          for (int c = 0; c < NR; ++c)
-            mma16816(o[c][d], va, __float_as_uint(sc[c][t][0]), __float_as_uint(sc[c][t][1]));
-        }
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t u = __shfl_sync(0xffffffffu, w, ((lane & 3) * 2 + e) * 4 + ((k & 7) >> 1));
+              pk[e] = __uint_as_float(k & 1 ? u & 0xffff0000u : u << 16);
+            }
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              const float v = __uint_as_float(static_cast<uint32_t>(
+                                  ld_shared_u16(v_at<KS>(sv, k, d * 8 + (lane >> 2)))) << 16);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (k0 + k < lim[c][e]) o[c][d >> 1][2 * (d & 1) + e] += pk[e] * v;
+            }
+          }
+      } else {
+#pragma unroll
+        for (int t = 0; t < KS / 16; ++t)
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const int r = t * 16 + ((lane >> 4) << 3) + (lane & 7);
+            const int ch = (d & 3) * 2 + ((lane >> 3) & 1);
+            uint32_t va[4];
+            ldsm4_t(va, sv + (d >> 2) * kHalf + r * 128 + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+            for (int c = 0; c < NR; ++c)
+              mma16816(o[c][d], va, __float_as_uint(sc[c][t][0]), __float_as_uint(sc[c][t][1]));
+          }
+      }
       __syncwarp();
       ++n_it;
       if (++j < p.n_kt) continue;
@@ -876,6 +935,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int my_row = warp * 16 + (lane & 15);  // found here once for the warp
       const __nv_bfloat16* my_q = q_row(a, p, my_row);
       const int my_lim = row_limit(a, p, my_row);
+      const int lim_min = __reduce_min_sync(0xffffffffu, my_q ? my_lim : p.keys);
+      const int lim_max = __reduce_max_sync(0xffffffffu, my_lim);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const __nv_bfloat16* qp = shfl_ptr(my_q, r_lo + 8 * e);
@@ -967,17 +1028,47 @@ __global__ void __launch_bounds__(kThreads, 2)
             pf[n >> 1][(n & 1) * 2 + e] = p;
           }
         }
+        if (k0 >= lim_max) {
+          // no row of the warp sees a key of the tile: no weights, and no values to look over (a first
+          // chunk of 8192 tokens has half its tiles here)
+        } else if (min(k0 + KS, p.keys) > lim_min &&
+                   any_not_finite<D, KS>(sv, max(lim_min - k0, 0), lane)) {
+#pragma unroll 1
+          for (int k = 0; k < KS; ++k) {
+            float pk[2];
 #pragma unroll
-        for (int kg = 0; kg < KS / 16; ++kg)
+            for (int e = 0; e < 2; ++e) {
+              uint32_t w = 0;  // the word of P that holds key k
 #pragma unroll
-          for (int dp = 0; dp < D / 16; ++dp) {
-            const int r = kg * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
-            const int ch = (dp & 3) * 2 + (lane >> 4);
-            uint32_t vb[4];
-            ldsm4_t(vb, sv + (dp >> 2) * (kHalf) + r * 128 + ((ch ^ (r & 7)) << 4));
-            mma16816(o[2 * dp], pf[kg], vb[0], vb[1]);
-            mma16816(o[2 * dp + 1], pf[kg], vb[2], vb[3]);
+              for (int x = 0; x < KS / 8; ++x)
+                if (x == k >> 3) w = pf[x >> 1][(x & 1) * 2 + e];
+              w = __shfl_sync(0xffffffffu, w, (lane & ~3) | ((k & 7) >> 1));
+              pk[e] = __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+            }
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              const uint32_t v = ld_shared_u32(v_at<KS>(sv, k, n * 8 + (lane & 3) * 2));
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (k0 + k < lim[e]) {
+                  o[n][2 * e] += pk[e] * __uint_as_float(v << 16);
+                  o[n][2 * e + 1] += pk[e] * __uint_as_float(v & 0xffff0000u);
+                }
+            }
           }
+        } else {
+#pragma unroll
+          for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+            for (int dp = 0; dp < D / 16; ++dp) {
+              const int r = kg * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
+              const int ch = (dp & 3) * 2 + (lane >> 4);
+              uint32_t vb[4];
+              ldsm4_t(vb, sv + (dp >> 2) * (kHalf) + r * 128 + ((ch ^ (r & 7)) << 4));
+              mma16816(o[2 * dp], pf[kg], vb[0], vb[1]);
+              mma16816(o[2 * dp + 1], pf[kg], vb[2], vb[3]);
+            }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + s);
       }
@@ -1182,15 +1273,21 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
   }
 }
 
-template <int D, int NR>
-cudaError_t launch_decode(const PagedArgs& a, cudaStream_t stream) {
+template <int D, int NR, bool kSeveral>
+cudaError_t launch_decode_of(const PagedArgs& a, cudaStream_t stream) {
   using L = DLayout<D, NR>;
   const cudaError_t e = ensure_smem_attr(
-      reinterpret_cast<const void*>(&paged_decode_kernel<D, NR>), L::kBytes);
+      reinterpret_cast<const void*>(&paged_decode_kernel<D, NR, kSeveral>), L::kBytes);
   if (e != cudaSuccess) return e;
   // beside the prefix kernel, if there is one
-  return launch_after(paged_decode_kernel<D, NR>, dim3(a.grid), dim3(kWarps * 32), L::kBytes,
-                      stream, a.splits_x != 0, a);
+  return launch_after(paged_decode_kernel<D, NR, kSeveral>, dim3(a.grid), dim3(kWarps * 32),
+                      L::kBytes, stream, a.splits_x != 0, a);
+}
+
+template <int D, int NR>
+cudaError_t launch_decode(const PagedArgs& a, cudaStream_t stream) {
+  return a.cu || a.T > 1 ? launch_decode_of<D, NR, true>(a, stream)
+                         : launch_decode_of<D, NR, false>(a, stream);
 }
 
 template <int D>

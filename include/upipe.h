@@ -397,8 +397,9 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
  * the pages prefix_table (device int32, ceil(prefix_len / page_size) entries; unused and may be
  * NULL when prefix_len = 0), the same for every row and read once for all of them, then its
  * sequence's own keys 0 .. j. lse (device float32, [B][Hq][S], or [Hq][S] for a packed batch;
- * or NULL) = ln sum exp(scores). A row that sees no key gets o = 0 and lse = -inf. What slots
- * outside prefix_len and seq_len hold does not matter, NaN included.
+ * or NULL) = ln sum exp(scores). A row that sees no key gets o = 0 and lse = -inf. What keys and
+ * values that a row does not see hold does not matter to it, NaN included: slots outside prefix_len
+ * and seq_len, and the new tokens behind its own.
  *   max_q (new tokens of the longest sequence; S is taken in a padded batch) and max_len (the
  *   largest seq_len) only choose the tile and the number of blocks; any value >= 1 gives right
  *   results.

@@ -627,8 +627,9 @@ def _empty(stream, like, shape, dtype, zero=False):
         if shape is like.shape:
             return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    if isinstance(stream, int):  # handle 0 as an ExternalStream would be a stream of torch's pool
+        stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                  else torch.cuda.default_stream(like.device))
     with torch.cuda.stream(stream):
         return _empty(None, like, shape, dtype, zero)
 

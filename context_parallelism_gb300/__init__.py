@@ -619,13 +619,14 @@ def _dense(t, dtype, shape, name):
 
 def _empty(stream, like, shape, dtype, zero=False):
     """An uninitialised (or zeroed) tensor beside `like`, allocated for the stream that the call
-    runs on, so that its memory is not handed to other work before that stream is done with it."""
+    runs on, so that its memory is not handed to other work before that stream is done with it.
+    shape None: like's own, and its layout."""
     torch = _torch or _lazy_torch()
     if stream is None:
+        if shape is None:
+            return torch.empty_like(like)
         if zero:
             return torch.zeros(shape, dtype=dtype, device=like.device)
-        if shape is like.shape:
-            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):  # handle 0 as an ExternalStream would be a stream of torch's pool
         stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
@@ -677,12 +678,12 @@ def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplac
     if q is not None:
         q_in = q_out = _heads(q, "q", 4)
         if not inplace:
-            q = torch.empty_like(q) if stream is None else _empty(stream, q, q.shape, q.dtype)
+            q = torch.empty_like(q) if stream is None else _empty(stream, q, None, q.dtype)
             q_out = _heads(q, "q", 4)
     if k is not None:
         k_in = k_out = _heads(k, "k", 4)
         if not inplace:
-            k = torch.empty_like(k) if stream is None else _empty(stream, k, k.shape, k.dtype)
+            k = torch.empty_like(k) if stream is None else _empty(stream, k, None, k.dtype)
             k_out = _heads(k, "k", 4)
     st = fn(q_in, k_in, q_out, k_out, pos, start, phases.data_ptr(), mscale, B, S, D, rot,
             1 if interleaved else 0, _stream(stream, ref))

@@ -65,3 +65,20 @@ def test_the_default_streams_handle():
     torch.cuda.synchronize()
     assert torch.equal(a, b)
     up.upipe_sync_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", [up.rope_forward, up.rope_backward])
+def test_rotary_outputs_keep_the_inputs_layout_on_any_stream(call):
+    ph, _ = up.rope_phases(64)
+    q = torch.randn((2, 4, 30, 64), device=DEV).bfloat16().transpose(1, 2)  # head-major
+    k = torch.randn((2, 30, 12, 64), device=DEV).bfloat16()[:, :, 3:5]
+    want = call(q, k, ph)
+    assert want[0].stride() == q.stride()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream, 0):
+        got = call(q, k, ph, stream=stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b) and a.stride() == b.stride()

@@ -239,6 +239,25 @@ int attn_plan(int B, int64_t rows, int Hq, int Hkv, int D, int64_t prefix_len, i
   return UPIPE_OK;
 }
 
+// f / (2 pi) modulo 1 in units of 2^-64, rounded to nearest. A double holds 11 bits too few for it, so
+// the quotient is kept as a sum q + e of two: e = (f - q 2 pi) / 2 pi, with 2 pi as a sum of two
+// doubles and the remainder by fused multiply-adds (the first of which is exact). q + e is then
+// within 2^-103 of itself: less than 2^-2 units for every |f| below 2^40.
+uint64_t phase_of(double f) {
+  const double p = 6.283185307179586, p_low = 2.4492935982947064e-16;
+  const double x = std::fabs(f);
+  double q = x / p;
+  double e = std::fma(-q, p_low, std::fma(-q, p, x)) / p;
+  // whole turns do not count: both steps are exact
+  q -= std::floor(q);
+  e -= std::rint(e);
+  const double units = std::ldexp(q, 64), whole = std::floor(units);
+  double rest = std::rint((units - whole) + std::ldexp(e, 64));
+  if (rest >= 0x1p63) rest -= 0x1p64;
+  const uint64_t w = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(rest));
+  return f < 0.0 ? 0 - w : w;
+}
+
 }  // namespace
 }  // namespace upipe
 
@@ -282,13 +301,10 @@ int upipe_rope_phases(const double* inv_freq, uint64_t* phase, int n) {
   set_last_error("");
   if (!inv_freq || !phase) return pfail(UPIPE_ERR_INVALID_ARG, "inv_freq or phase is NULL");
   if (n < 1) return pfail(UPIPE_ERR_INVALID_ARG, "n=%d", n);
-  const double two_pi = 6.28318530717958647692;
   for (int i = 0; i < n; ++i) {
     if (!std::isfinite(inv_freq[i]))
       return pfail(UPIPE_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
-    double t = inv_freq[i] / two_pi;
-    t -= std::floor(t);  // whole turns do not count: exact, and t < 1
-    phase[i] = t >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(t, 64));
+    phase[i] = phase_of(inv_freq[i]);
   }
   return UPIPE_OK;
 }

@@ -9,8 +9,9 @@
 // so p * phase modulo 2^64 is the fractional turn of the angle, exactly, for every 64-bit
 // position: one integer multiply instead of a 64-bit floating-point range reduction or a table
 // over positions. Read as a signed number it is the angle in half turns times 2^63, which
-// sincospif takes without further reduction. The phase's own rounding (2^-65 of a turn) reaches
-// 2^-25 of a turn, a float's resolution, only at position 2^40.
+// sincospif takes without further reduction. The phase's own rounding (within 2^-64 of a turn:
+// upipe_rope_phases divides in two doubles) reaches 2^-25 of a turn, a float's resolution, only at
+// position 2^39.
 //
 // Bound: HBM. Each element is read and written once (4 bytes); a thread owns 8 frequencies (two
 // 16-byte vectors of a head) and applies them to kHeads heads of one token, so the eight

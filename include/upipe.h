@@ -297,9 +297,11 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
  *   c = mscale cos(p f_i), s = mscale sin(p f_i);  y1 = x1 c - x2 s,  y2 = x2 c + x1 s,
  * (x1, x2) = (x_i, x_{i + rot/2}) (interleaved = 0) or (x_{2i}, x_{2i+1}) (interleaved = 1);
  * features rot..D-1 are copied. Backward: the gradient with respect to x of <dy, y>, the same
- * map with -s. bf16 in and out, fp32 arithmetic, one rounding. The angle is exact for every
- * 64-bit position, whatever its size: frequencies are kept as phases, 64-bit fixed-point
- * fractions of a turn a position, and p * phase modulo 2^64 is the angle's fraction of a turn.
+ * map with -s. bf16 in and out, fp32 arithmetic, one rounding. Frequencies are kept as phases,
+ * 64-bit fixed-point fractions of a turn a position, and p * phase modulo 2^64, computed without
+ * rounding for every 64-bit position, is the angle's fraction of a turn. A phase is within 2^-64 of
+ * a turn of the frequency given (upipe_rope_phases), so p f_i is met to |p| 2^-64 of a turn: less than
+ * a float's 2^-25 up to position 2^39.
  */
 
 /* A strided [B, S, heads, D] tensor of bf16: element (b, s, h, d) at
@@ -323,8 +325,9 @@ enum { UPIPE_ROPE_PLAIN = 0, UPIPE_ROPE_LINEAR = 1, UPIPE_ROPE_NTK = 2, UPIPE_RO
 int upipe_rope_frequencies(double* inv_freq, double* mscale, int rot_dim, double theta,
                            int scaling, double factor, double trained_len, double turns_fast,
                            double turns_slow);
-/* Host arithmetic: phase[i] = frac(inv_freq[i] / (2 pi)) 2^64 (host memory). Copy the result to
- * the device once; the calls below take that copy. */
+/* Host arithmetic: phase[i] = frac(inv_freq[i] / (2 pi)) 2^64, to the nearest integer or the next
+ * (|inv_freq[i]| below 2^40; host memory). Copy the result to the device once; the calls below take
+ * that copy. */
 int upipe_rope_phases(const double* inv_freq, uint64_t* phase, int n);
 
 /*

@@ -94,7 +94,8 @@ constexpr uint32_t kOver = kSegmentCost;
 // One group of segments (the prefix: b = -1, or a sequence): its rows and keys.
 struct Group {
   int tok0, n_tok;   // rows of q
-  int keys;
+  int keys;          // that the table holds
+  int len;           // own tokens as given: more than keys where the table is too narrow
   uint32_t segs;     // row tiles x kv-heads
   uint32_t cost;     // kOver + tiles per segment, at least one (a segment without keys still writes)
   __device__ __forceinline__ uint32_t tiles() const { return segs * cost; }  // host: below 2^32
@@ -107,7 +108,7 @@ __device__ __forceinline__ Group load_group(const PagedArgs& a, int b, bool repo
   if (b < 0) {
     g.tok0 = 0;
     g.n_tok = a.splits_x || !a.prefix ? 0 : a.cu ? min(rows, max(a.cu[a.B], 0)) : rows;
-    g.keys = static_cast<int>(a.prefix);
+    g.len = g.keys = static_cast<int>(a.prefix);
   } else {
     const int len = a.seq_len[b];
     if (a.cu) {
@@ -119,7 +120,8 @@ __device__ __forceinline__ Group load_group(const PagedArgs& a, int b, bool repo
       g.n_tok = static_cast<int>(a.T);
     }
     if (report && len > a.cap) atomicOr(a.err, kErrBadPage);
-    g.keys = min(max(len, 0), a.cap);
+    g.len = max(len, 0);
+    g.keys = min(g.len, a.cap);
   }
   g.segs = (static_cast<uint32_t>(g.n_tok * a.G) + (MT - 1)) / MT * a.Hkv;
   g.cost = kOver + max((static_cast<uint32_t>(g.keys) + (KS - 1)) / KS, 1u);
@@ -203,7 +205,8 @@ struct Walk {
           group_seg += __shfl_sync(0xffffffffu, ns - mine.segs, l);
           g.tok0 = __shfl_sync(0xffffffffu, mine.tok0, l);
           g.n_tok = __shfl_sync(0xffffffffu, mine.n_tok, l);
-          g.keys = __shfl_sync(0xffffffffu, mine.keys, l);
+          g.len = __shfl_sync(0xffffffffu, mine.len, l);
+          g.keys = min(g.len, a.cap);
           g.segs = __shfl_sync(0xffffffffu, mine.segs, l);
           g.cost = __shfl_sync(0xffffffffu, mine.cost, l);
           break;
@@ -250,7 +253,7 @@ struct Walk {
     p->own = b >= 0;
     p->keys = k_hi - k_lo;
     p->n_kt = (p->keys + KS - 1) / KS;
-    p->before = g.keys - g.n_tok - k_lo;
+    p->before = g.len - g.n_tok - k_lo;
     p->first = t0 == 0;
     // workers from the segment's first tile to its last (known where the segment starts)
     const uint32_t rest = g.cost - kt - n;

@@ -364,9 +364,10 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
  * max_pages entries a sequence). A row with j < 0 has no place in the cache: the append skips
  * it, and attention sees no own key there; so a padded batch row is one of length 0.
  * Pages. A page-table entry is followed only where a key is read or written. One that names no
- * page (or a length beyond max_pages * page_size) never leads outside the cache: the append
- * drops the token, attention reads zeros, and the next upipe_sync_status returns
- * UPIPE_ERR_PAGE.
+ * page never leads outside the cache: the append drops the token, attention reads zeros, and the
+ * next upipe_sync_status returns UPIPE_ERR_PAGE. A length beyond max_pages * page_size is reported
+ * the same way: the append drops the tokens behind the table, and attention takes those that the
+ * table holds (a row's limit j counts the others).
  * Both calls use the device's status word: make the first one on a device (of any call that
  * uses it) before a stream capture. They are asynchronous, deterministic and may be captured.
  */

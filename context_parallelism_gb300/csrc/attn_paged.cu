@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int32_t* pages = nullptr;
   bool more = true;
   auto look_up = [&]() {
+    static_assert(kMaxOwnKeys <= 0x7fffffff - 31 * 16, "a key behind the last one has a number");
     win = key0;
     const int key = key0 + lane * 16;
     win_at = -1;  // past the keys, or a page that does not exist: zeros

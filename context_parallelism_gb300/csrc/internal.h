@@ -348,6 +348,10 @@ cudaError_t make_tmap_pages(CUtensorMap* map, const void* base, int D, int page_
 // are cut into shares; the host bounds the sum.
 constexpr uint32_t kSegmentCost = 2;
 
+// Own keys of a sequence at most: the kernels number them in 32 bits with sign and look up pages for
+// runs of 16 keys, 32 runs at a time, so up to 496 keys behind the last one have numbers too.
+constexpr int kMaxOwnKeys = 0x7fffffff - 1023;
+
 struct PagedArgs {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
@@ -360,7 +364,7 @@ struct PagedArgs {
   const int32_t* cu;         // [B + 1] or NULL
   const int32_t* table;      // [B][table_stride]
   int64_t table_stride, max_pages, n_pages;
-  int cap;                   // keys that a row of the table holds, at most 2^31 - 64
+  int cap;                   // keys that a row of the table holds, at most kMaxOwnKeys
   const int32_t* seq_len;    // [B]
   const int32_t* ptable;     // [ceil(prefix / page_size)]
   int64_t prefix;

@@ -459,10 +459,9 @@ int upipe_attn_paged_fwd(const upipe_heads* q, const upipe_heads* o, float* lse,
   if (st == UPIPE_OK && prefix_len) st = p.add(prefix_table, "prefix_table", 4);
   if (st == UPIPE_OK) st = p.add(workspace, "workspace", 256);
   if (st != UPIPE_OK) return st;
-  const int64_t cap_most = 0x7fffffff - 63;
-  a.cap = static_cast<int>(max_pages > cap_most / cache->page_size
-                               ? cap_most
-                               : max_pages * cache->page_size);
+  a.cap = max_pages > kMaxOwnKeys / cache->page_size
+              ? kMaxOwnKeys
+              : static_cast<int>(max_pages * cache->page_size);
   // the kernels count in 32 bits: a segment's tiles (rounded up) and kSegmentCost more
   const double tiles =
       static_cast<double>(a.segs) * (a.cap / a.ks + 1.0 + kSegmentCost) +

@@ -413,9 +413,9 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
  *   live as long as the graph.
  * o is q itself or does not overlap it.
  * Supported: D 64 or 128, Hq a multiple of Hkv, page_size a multiple of 16, up to 2^24 rows,
- * prefix_len up to 2^30, and (each sequence's row tiles x Hkv) x (16-key tiles that max_pages
- * allows) below 2^32. B = 0 or S = 0 does nothing. One key order per shape: results repeat bitwise
- * for the same sizes and hints.
+ * prefix_len up to 2^30, seq_len up to 2^31 - 1024 (a longer one is reported as beyond the table),
+ * and (each sequence's row tiles x Hkv) x (16-key tiles that max_pages allows) below 2^32. B = 0 or
+ * S = 0 does nothing. One key order per shape: results repeat bitwise for the same sizes and hints.
  */
 size_t upipe_attn_paged_workspace_bytes(int B, int64_t rows, int Hq, int Hkv, int D,
                                         int64_t prefix_len, int64_t max_q, int64_t max_len);

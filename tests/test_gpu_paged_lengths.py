@@ -1,4 +1,5 @@
 """Lengths at and beyond what the page table holds (needs an sm_103a GPU)."""
+import numpy as np
 import pytest
 import torch
 
@@ -39,3 +40,30 @@ def test_attention_with_a_length_beyond_the_table(case, beyond):
         one.table, one.table_np = b.table, b.table_np
         one.ptable, one.ptable_np = b.ptable, b.ptable_np
         one.check(o[:, i:i + 1], lse[:, :, i:i + 1])
+
+
+def test_the_longest_sequence():
+    """2^31 - 1024 own keys, the most that is supported: 64 pages named in turn by a table that is
+    exactly as wide, so each of their 1024 keys counts 2^21 - 1 times. One more is reported.
+
+    Tolerance: 1216 warps sum 1.77 million keys each. A lane's sum of weights takes 4 of a tile's 32
+    keys one after the other, 2^-24 a step; a numerator 2 steps a tile, 2^-23 each: 220753 2^-24 and
+    110377 2^-23 of the sums, 0.0264, beside the weights' own 2^-8."""
+    up.upipe_sync_status()
+    n = (1 << 31) - 1024
+    g = torch.Generator(device=DEV).manual_seed(5)
+    kp, vp, q = (torch.randn(s, generator=g, device=DEV).bfloat16()
+                 for s in ((64, 16, 1, 64), (64, 16, 1, 64), (1, 1, 2, 64)))
+    table = (torch.arange(n // 16, dtype=torch.int32, device=DEV) % 64)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    o, lse = up.paged_attention(q, kp, vp, table, lens, with_lse=True)
+    up.upipe_sync_status()
+    k, v = kp.view(-1, 64).double().cpu(), vp.view(-1, 64).double().cpu()
+    s = q[0, 0].double().cpu() @ k.t() / 8
+    want = torch.softmax(s, -1) @ v
+    off = 220753 * 2.0 ** -24 + 110377 * 2.0 ** -23 + 2.0 ** -8
+    assert (o[0, 0].double().cpu() - want).abs().max() <= 2 * off * v.abs().max()
+    assert (lse[0, :, 0].double().cpu() - torch.logsumexp(s, -1) - np.log(n // 1024)).abs().max() <= 2 * off
+    lens += 1
+    up.paged_attention(q, kp, vp, table, lens)
+    _page_error()

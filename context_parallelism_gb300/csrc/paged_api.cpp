@@ -62,6 +62,27 @@ struct Placed {
   int n = 0;
 };
 
+// Whether rows of D elements at all combinations of three strides may overlap: unless each stride, in
+// rising order, steps over all that the smaller ones span. (Layouts whose rows mesh without meeting
+// are refused too; no permutation, slice or interleaving of dense tensors is one.)
+bool may_overlap(const int64_t (&stride)[3], const int64_t (&extent)[3], int D) {
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[order[j]] > stride[order[j + 1]]) {
+        const int t = order[j];
+        order[j] = order[j + 1];
+        order[j + 1] = t;
+      }
+  unsigned __int128 span = D;
+  for (int i : order) {
+    if (extent[i] <= 1) continue;
+    if (static_cast<unsigned __int128>(stride[i]) < span) return true;
+    span += static_cast<unsigned __int128>(stride[i]) * (extent[i] - 1);
+  }
+  return false;
+}
+
 // One strided [B, S, heads, D] tensor. Written ones must not overlap themselves.
 int check_heads(const upipe_heads* t, const char* name, int64_t B, int64_t S, int D, bool written,
                 Placed* p) {
@@ -76,6 +97,8 @@ int check_heads(const upipe_heads* t, const char* name, int64_t B, int64_t S, in
     if (written && st[i] < D)
       return pfail(UPIPE_ERR_INVALID_ARG, "%s: a written tensor's strides must be at least D", name);
   }
+  if (written && may_overlap(st, ext, D))
+    return pfail(UPIPE_ERR_INVALID_ARG, "%s: a written tensor must not overlap itself", name);
   return p->add(t->data, name, 16);
 }
 
@@ -126,6 +149,8 @@ int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const up
   if ((has_q && !present(q_out)) || (has_k && !present(k_out)))
     return pfail(UPIPE_ERR_INVALID_ARG, "an input without its output");
   if (B == 0 || S == 0) return UPIPE_OK;
+  if ((has_q ? static_cast<int64_t>(q->heads) : 0) + (has_k ? k->heads : 0) > 65536)
+    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
   Placed p;
   RopeArgs a{};
   bool in_place = true;
@@ -142,8 +167,8 @@ int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const up
     set_view(&a, i, in[i], out[i]);
     in_place = in_place && same_place(in[i], out[i]);
   }
-  if (static_cast<int64_t>(a.heads[0]) + a.heads[1] > 65536)
-    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
+  if (has_q && has_k && q_out->data == k_out->data)
+    return pfail(UPIPE_ERR_INVALID_ARG, "q_out and k_out are one tensor");
   st = p.add(phase, "phase", 16);
   if (st == UPIPE_OK && pos) st = p.add(pos, "pos", 8);
   if (st == UPIPE_OK) st = p.resolve();
@@ -361,6 +386,9 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
   if (max_pages < 1 || (B > 1 && table_stride < max_pages))
     return pfail(UPIPE_ERR_INVALID_ARG, "max_pages=%lld table_stride=%lld", (long long)max_pages,
                  (long long)table_stride);
+  if (may_overlap({cache->stride_page, cache->stride_slot, cache->stride_head},
+                  {cache->n_pages, cache->page_size, cache->heads}, D))
+    return pfail(UPIPE_ERR_INVALID_ARG, "cache: pages, slots or heads overlap");
   if (B == 0 || S == 0) return UPIPE_OK;
   const int64_t vb = cu_rows ? 1 : B;
   RopeArgs a{};

@@ -306,8 +306,8 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
 
 /* A strided [B, S, heads, D] tensor of bf16: element (b, s, h, d) at
  * data[b * stride_b + s * stride_s + h * stride_h + d]. data is 16-byte aligned; strides of
- * extents above 1 are multiples of 8 elements, not negative, and at least D in tensors that are
- * written. heads = 0 (or a NULL pointer to this struct): the tensor is absent. */
+ * extents above 1 are multiples of 8 elements and not negative. Tensors that are written do not
+ * overlap themselves: each stride steps over all that the smaller ones span. heads = 0 (or a NULL pointer to this struct): the tensor is absent. */
 typedef struct {
   void* data;
   int64_t stride_b, stride_s, stride_h;
@@ -332,9 +332,9 @@ int upipe_rope_phases(const double* inv_freq, uint64_t* phase, int n);
 
 /*
  * q and k (either may be absent) are rotated into q_out and k_out. An output is its input (same
- * data and strides: in place) or does not overlap it. pos: device [B][S] positions, or NULL for
- * pos0 + s. phase: device, rot_dim / 2 words. Supported: D a multiple of 8 up to 1024, rot_dim
- * a multiple of 16 up to D. B = 0 or S = 0 does nothing. The backward takes the gradients of
+ * data and strides: in place) or does not overlap it, and the outputs do not overlap each other.
+ * pos: device [B][S] positions, or NULL for pos0 + s. phase: device, rot_dim / 2 words. Supported:
+ * D a multiple of 8 up to 1024, rot_dim a multiple of 16 up to D. B = 0 or S = 0 does nothing. The backward takes the gradients of
  * the outputs and writes those of the inputs. Neither allocates anything or touches the status
  * word, so both may be captured into a graph from their first call on.
  */
@@ -374,7 +374,7 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
 
 /* k and v caches with one set of element strides: element (page, slot, head, d) at
  * page * stride_page + slot * stride_slot + head * stride_head + d. 16-byte aligned; strides
- * multiples of 8, at least D. */
+ * multiples of 8, at least D. The append wants slots that do not overlap, as of tensors above. */
 typedef struct {
   void* k;
   void* v;

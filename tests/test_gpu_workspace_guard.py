@@ -89,3 +89,62 @@ def test_tiled_paths_stay_inside_their_workspace(S, T, host):
     up.mlp_backward(xi, wgu, wdd, dyi, seq_tile=T, workspace=g.ws, dx_on_host=host)
     up.upipe_sync_status()
     g.check()
+
+
+def _paged(counts, lens, Hq, Hkv, D, page, prefix, packed, max_q, max_len):
+    """Paged attention on a workspace of exactly the declared size; its bytes before the call differ
+    from run to run, so that a part read before it is written shows."""
+    g = torch.Generator(device="cuda").manual_seed(sum(lens) + prefix)
+    need = [-(-m // page) for m in lens]
+    shared = -(-prefix // page)
+    n = shared + sum(need)
+    kp, vp = (torch.randn((n, page, Hkv, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.full((len(lens), max(1, max(need))), -1, dtype=torch.int32)
+    at = shared
+    for b, x in enumerate(need):
+        table[b, :x] = torch.arange(at, at + x)
+        at += x
+    rows = sum(counts)
+    shape = (rows + 2, Hq, D) if packed else (len(lens), counts[0], Hq, D)
+    q = torch.randn(shape, generator=g, device="cuda").bfloat16()
+    kw = dict(prefix_table=torch.arange(shared, dtype=torch.int32, device="cuda"), prefix_len=prefix)
+    if packed:
+        cu = torch.zeros(len(counts) + 1, dtype=torch.int32)
+        cu[1:] = torch.tensor(counts).cumsum(0)
+        kw["cu_seqlens"] = cu.cuda()
+    size = up.upipe_attn_paged_workspace_bytes(
+        len(lens), rows + 2 if packed else rows, Hq, Hkv, D, prefix,
+        max_q if packed else counts[0], max_len)
+    got = []
+    for fill in (CANARY, 0xFF, 0x00):
+        gd = Guarded(size)
+        gd.ws.fill_(fill)
+        out, lse = torch.zeros_like(q), torch.zeros(
+            (Hq, rows + 2) if packed else (len(lens), Hq, counts[0]), device="cuda")
+        up.paged_attention(q, kp, vp, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                           max_q=max_q, max_len=max_len, out=out, lse=lse, workspace=gd.ws, **kw)
+        up.upipe_sync_status()
+        gd.check()
+        got.append((out, lse))
+    for out, lse in got:
+        assert torch.isfinite(out).all() and not torch.isnan(lse).any()
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("hint", [(1, 1), (4, 700), (64, 100000)])
+@pytest.mark.parametrize("case", [
+    ([1] * 5, [1, 700, 33, 0, 64], 8, 2, 128, 16, 0),          # own pages in tiles of 8 rows
+    ([3] * 4, [3, 500, 20, 5], 16, 4, 64, 32, 130),            # tiles of 16, a short prefix beside
+    ([1] * 3, [10, 20, 30], 32, 1, 128, 16, 40),               # 64 rows
+    ([50] * 2, [50, 400], 4, 2, 64, 64, 100),
+    ([1] * 24, [9] * 24, 8, 1, 128, 16, 1700),                 # tensor-core prefix, two row tiles
+    ([2] * 6, [2, 9, 600, 33, 4, 5], 8, 2, 128, 64, 5600),     # one row tile, two key streams
+    ([1] * 40, [b + 1 for b in range(40)], 16, 2, 64, 32, 900),
+    ([20] * 2, [30, 90], 32, 2, 128, 128, 3500),               # 64-row tiles beside it
+])
+def test_paged_attention_stays_inside_its_workspace(case, hint, packed):
+    counts, lens, Hq, Hkv, D, page, prefix = case
+    if packed:
+        counts = [n - b % 2 if n > 1 else n for b, n in enumerate(counts)]
+    _paged(counts, lens, Hq, Hkv, D, page, prefix, packed, *hint)

@@ -81,12 +81,6 @@ struct Piece {
 
 static_assert(sizeof(Piece) % 8 == 0, "pieces keep the alignment of their words");
 
-// a / b for 0 <= a, 0 < b; 32-bit where it can be (the 64-bit division is a long subroutine).
-__device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
-  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-                              : a / b;
-}
-
 // What starting and ending a piece costs, in tiles: each segment counts as so many tiles more, so
 // that a worker with many short sequences has fewer keys. Tile t of a segment is at kOver + t.
 constexpr uint32_t kOver = kSegmentCost;

@@ -375,11 +375,11 @@ struct PagedArgs {
   // (max in log2 units, sum of the rounded weights, sum of the weights, 0).
   float* part_o;
   float4* part_ml;
-  int splits_x;              // key splits of launch_attn_prefix; 0: attn_paged_kernel takes the
+  int splits_x;              // key splits of launch_attn_prefix; 0: launch_attn_paged takes the
                              // prefix too
   int splits_p;              // parts that these give each row
   int tiles_p;               // its row tiles
-  // Pieces of attn_paged_kernel: slot s holds mt rows of numerators and statistics; desc[0] and
+  // Pieces of launch_attn_paged: slot s holds mt rows of numerators and statistics; desc[0] and
   // desc[1], [rows][Hq] each, name a row's first slot row and number of pieces (0: the row is
   // finished), for the prefix and for its own keys.
   float* slot_o;

@@ -483,6 +483,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// a / b for 0 <= a, 0 < b; 32-bit where it can be (the 64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

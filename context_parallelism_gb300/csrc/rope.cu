@@ -30,12 +30,6 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kHeads = 4;  // heads of one token per thread
 
-// a / b for 0 <= a, 0 < b; 32-bit where it can be (the 64-bit division is a long subroutine).
-__device__ __forceinline__ int64_t div_fl(int64_t a, int64_t b) {
-  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-                              : a / b;
-}
-
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

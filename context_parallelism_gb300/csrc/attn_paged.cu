@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // Row tiles of 64: one producer warp, which walks the share, publishes each piece and streams its
 // keys and values through a ring of 64-key stages, running ahead into the next pieces, and four
 // consumer warps, each with 16 rows and every stage: S = Q K^T, O += P V. Bound: the consumers'
-// time for a tile, 3500 to 3900 cycles with two blocks an SM (17 of the 23 bytes a cycle that HBM
+// time for a tile, 3400 to 3900 cycles with two blocks an SM (17 of the 23 bytes a cycle that HBM
 // could bring). Warps without rows take part all the same: letting them skip their products made
 // 20 to 40 rows 3 % slower.
 constexpr int kThreads = 160;

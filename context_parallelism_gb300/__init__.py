@@ -32,7 +32,8 @@ UPIPE_ROPE_PLAIN, UPIPE_ROPE_LINEAR, UPIPE_ROPE_NTK, UPIPE_ROPE_BY_PARTS = 0, 1,
 
 KERNEL_CLASSES = ["layout", "attn_fwd", "bwd_pre", "attn_bwd", "dq_convert", "other",
                   "loss_gemm", "loss_merge", "kv_h2d", "dkdv_d2h", "kv_wait", "rope",
-                  "kv_append", "attn_paged", "paged_merge", "attn_prefix"]
+                  "kv_append", "attn_paged", "paged_merge", "attn_prefix", "norm_rope", "embed",
+                  "logp"]
 
 # Every symbol include/upipe.h declares, with (restype, argtypes).
 _vp, _i, _i64, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
@@ -57,6 +58,13 @@ class Pages(ctypes.Structure):
                 ("heads", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
+class Norm(ctypes.Structure):
+    """upipe_norm: the weights of q's and k's norms."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("offset", ctypes.c_double), ("eps", ctypes.c_double), ("wide", ctypes.c_int32)]
+
+
+_pn = ctypes.POINTER(Norm)
 _ph, _pp, _d = ctypes.POINTER(Heads), ctypes.POINTER(Pages), ctypes.c_double
 
 SIGNATURES = {
@@ -96,6 +104,13 @@ SIGNATURES = {
     "upipe_rope_bwd": (_i, [_ph, _ph, _ph, _ph, _vp, _i64, _vp, _d, _i, _i64, _i, _i, _i, _vp]),
     "upipe_kv_append": (_i, [_ph, _ph, _ph, _ph, _pp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
                              _d, _i, _i64, _i, _i, _vp]),
+    "upipe_kv_append_norm": (_i, [_ph, _ph, _ph, _ph, _pn, _pp, _vp, _i64, _i64, _vp, _vp, _vp,
+                                  _i64, _vp, _d, _i, _i64, _i, _i, _vp]),
+    "upipe_norm_rope_fwd": (_i, [_ph, _ph, _ph, _ph, _pn, _vp, _i64, _vp, _d, _i, _i64, _i, _i, _i,
+                                 _vp]),
+    "upipe_norm_rope_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i]),
+    "upipe_norm_rope_bwd": (_i, [_ph, _ph, _ph, _ph, _ph, _ph, _vp, _vp, _pn, _vp, _i64, _vp, _d,
+                                 _i, _i64, _i, _i, _i, _vp, _sz, _vp]),
     "upipe_attn_paged_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i, _i64, _i64, _i64]),
     "upipe_attn_paged_fwd": (_i, [_ph, _ph, _vp, _pp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i,
                                   _i64, _i64, _i64, _vp, _sz, _vp]),
@@ -366,6 +381,44 @@ def upipe_kv_append(q, q_out, k, v, cache, page_table, table_stride, max_pages, 
                                 _ptr(seq_len), _ptr(cu_rows), _ptr(pos), pos0, _ptr(phase),
                                 mscale, B, S, rot_dim, int(interleaved),
                                 _stream(stream, page_table)), "upipe_kv_append")
+
+
+def upipe_kv_append_norm(q, q_out, k, v, norm, cache, page_table, table_stride, max_pages, seq_len,
+                         cu_rows, pos, pos0, phase, mscale, B, S, rot_dim, interleaved,
+                         stream=None):
+    """q, q_out, k, v: Heads or None; norm: Norm; cache: Pages."""
+    _check(_lib.upipe_kv_append_norm(q, q_out, k, v, norm, cache, _ptr(page_table), table_stride,
+                                     max_pages, _ptr(seq_len), _ptr(cu_rows), _ptr(pos), pos0,
+                                     _ptr(phase), mscale, B, S, rot_dim, int(interleaved),
+                                     _stream(stream, page_table)), "upipe_kv_append_norm")
+
+
+def upipe_norm_rope_fwd(q, k, q_out, k_out, norm, pos, pos0, phase, mscale, B, S, D, rot_dim,
+                        interleaved, stream=None):
+    """q, k, q_out, k_out: Heads or None (absent); norm: Norm. Without phase and pos, whose device
+    has a current stream, stream None is the default stream."""
+    _check(_lib.upipe_norm_rope_fwd(q, k, q_out, k_out, norm, _ptr(pos), pos0, _ptr(phase), mscale,
+                                    B, S, D, rot_dim, int(interleaved),
+                                    _stream(stream, phase, pos)), "upipe_norm_rope_fwd")
+
+
+@functools.lru_cache(maxsize=4096)
+def upipe_norm_rope_workspace_bytes(B, S, Hq, Hkv, D):
+    return int(_lib.upipe_norm_rope_workspace_bytes(B, S, Hq, Hkv, D))
+
+
+def upipe_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, norm, pos, pos0, phase,
+                        mscale, B, S, D, rot_dim, interleaved, workspace, workspace_bytes=None,
+                        stream=None):
+    """dq_out, dk_out, q, k, dq, dk: Heads or None (absent); norm: Norm."""
+    wb = workspace_bytes
+    if wb is None:
+        wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.upipe_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, _ptr(dq_weight), _ptr(dk_weight),
+                                    norm, _ptr(pos), pos0, _ptr(phase), mscale, B, S, D, rot_dim,
+                                    int(interleaved), _ptr(workspace), wb,
+                                    _stream(stream, dq_weight, dk_weight, workspace)),
+           "upipe_norm_rope_bwd")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -659,16 +712,23 @@ def _phases(phases):
     return 2 * phases.shape[0]
 
 
-def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
-    torch = _torch or _lazy_torch()
+def _q_or_k(q, k):
+    """B, S, D of the tensors that are there."""
     ref = q if q is not None else k
     if ref is None or ref.dim() != 4:
         raise ValueError("q and k must be [B, S, heads, D] (one may be None)")
-    B, S, _, D = shape = ref.shape
+    B, S, _, D = ref.shape
     if k is not None and k is not ref:
         ks = k.shape
         if len(ks) != 4 or ks[0] != B or ks[1] != S or ks[3] != D:
             raise ValueError("q and k must agree in B, S and D")
+    return ref, B, S, D
+
+
+def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
+    torch = _torch or _lazy_torch()
+    ref, B, S, D = _q_or_k(q, k)
+    shape = ref.shape
     pos = None
     if positions is not None:
         _dense(positions, torch.int64, shape[:2], "positions")
@@ -708,6 +768,113 @@ def rope_backward(dq, dk, phases, mscale=1.0, interleaved=False, positions=None,
                  positions, start, inplace, stream)
 
 
+def _norm(q_weight, k_weight, D, offset, eps):
+    """upipe_norm of two [D] weights of one type (bf16 or float32; None: ones)."""
+    torch = _torch or _lazy_torch()
+    wide, ptr = None, [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is None:
+            continue
+        if w.dtype is not torch.bfloat16 and w.dtype is not torch.float32:
+            raise TypeError(f"a norm's weights must be bfloat16 or float32, not {w.dtype}")
+        if w.shape != (D,) or not w.is_contiguous():
+            raise ValueError(f"a norm's weights must be contiguous [{D}], not {tuple(w.shape)}")
+        if wide is not None and wide != (w.dtype is torch.float32):
+            raise TypeError("q_weight and k_weight must be of one type")
+        wide = w.dtype is torch.float32
+        ptr[i] = w.data_ptr()
+    return Norm(ptr[0], ptr[1], offset, eps, 1 if wide else 0)
+
+
+def _like(x, ref, name):
+    """x must be of ref's shape, in [B, S, heads, D]."""
+    if x.shape != ref.shape:
+        raise ValueError(f"{name} must be {tuple(ref.shape)}, not {tuple(x.shape)}")
+    return x
+
+
+def _rotation(phases, positions, lead):
+    """rot_dim, and the pointers of the phases and of the positions (None: start + place)."""
+    pos = None
+    if positions is not None:
+        _dense(positions, (_torch or _lazy_torch()).int64, lead, "positions")
+        pos = positions.data_ptr()
+    if phases is None:
+        return 0, None, pos
+    return _phases(phases), phases.data_ptr(), pos
+
+
+def norm_rope_forward(q, k, q_weight, k_weight, phases=None, mscale=1.0, eps=1e-6, offset=0.0,
+                      interleaved=False, positions=None, start=0, inplace=False, stream=None):
+    """q, k (bf16 [B, S, heads, D], any strides with contiguous D; one may be None), each head
+    normed by its root mean square, times its weights (bf16 or float32 [D]; None: ones; offset is
+    added to them), and rotated as by rope_forward (phases None: not rotated). Returns (q, k)."""
+    ref, B, S, D = _q_or_k(q, k)
+    rot, ph, pos = _rotation(phases, positions, ref.shape[:2])
+    norm = _norm(q_weight if q is not None else None, k_weight if k is not None else None, D,
+                 offset, eps)
+    q_in = q_out = k_in = k_out = None
+    if q is not None:
+        q_in = q_out = _heads(q, "q", 4)
+        if not inplace:
+            q = _empty(stream, q, None, q.dtype)
+            q_out = _heads(q, "q", 4)
+    if k is not None:
+        k_in = k_out = _heads(k, "k", 4)
+        if not inplace:
+            k = _empty(stream, k, None, k.dtype)
+            k_out = _heads(k, "k", 4)
+    st = _lib.upipe_norm_rope_fwd(q_in, k_in, q_out, k_out, norm, pos, start, ph, mscale, B, S, D,
+                                  rot, 1 if interleaved else 0, _stream(stream, ref))
+    if st:
+        raise UpipeError(st, "upipe_norm_rope_fwd")
+    return q, k
+
+
+def norm_rope_backward(dq, dk, q, k, q_weight, k_weight, phases=None, mscale=1.0, eps=1e-6,
+                       offset=0.0, interleaved=False, positions=None, start=0, inplace=False,
+                       workspace=None, stream=None):
+    """The gradients with respect to norm_rope_forward's inputs q, k and weights, from those of its
+    outputs (dq, dk; inplace writes them). Returns (dq, dk, dq_weight, dk_weight), the last two
+    float32 [D] (None for weights that are None)."""
+    torch = _torch or _lazy_torch()
+    ref, B, S, D = _q_or_k(dq, dk)
+    rot, ph, pos = _rotation(phases, positions, ref.shape[:2])
+    if dq is None:
+        q_weight = None
+    if dk is None:
+        k_weight = None
+    norm = _norm(q_weight, k_weight, D, offset, eps)
+    dq_in = dq_out = q_in = dk_in = dk_out = k_in = None
+    if dq is not None:
+        q_in, dq_in = _heads(_like(q, dq, "q"), "q", 4), _heads(dq, "dq", 4)
+        dq_out = dq_in
+        if not inplace:
+            dq = _empty(stream, dq, None, dq.dtype)
+            dq_out = _heads(dq, "dq", 4)
+    if dk is not None:
+        k_in, dk_in = _heads(_like(k, dk, "k"), "k", 4), _heads(dk, "dk", 4)
+        dk_out = dk_in
+        if not inplace:
+            dk = _empty(stream, dk, None, dk.dtype)
+            dk_out = _heads(dk, "dk", 4)
+    dqw = _empty(stream, ref, (D,), torch.float32) if q_weight is not None else None
+    dkw = _empty(stream, ref, (D,), torch.float32) if k_weight is not None else None
+    ws, wb = None, 0
+    if dqw is not None or dkw is not None:
+        if workspace is None:
+            wb = upipe_norm_rope_workspace_bytes(B, S, dq_in.heads if dq_in else 0,
+                                                 dk_in.heads if dk_in else 0, D)
+            workspace = _empty(stream, ref, (max(wb, 256),), torch.uint8)
+        ws, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _lib.upipe_norm_rope_bwd(dq_in, dk_in, q_in, k_in, dq_out, dk_out, _ptr(dqw), _ptr(dkw),
+                                  norm, pos, start, ph, mscale, B, S, D, rot,
+                                  1 if interleaved else 0, ws, wb, _stream(stream, ref))
+    if st:
+        raise UpipeError(st, "upipe_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
 def _batch(q, cu_seqlens, seq_len):
     """B, S, dimensions and leading shape of a padded [B, S, heads, D] or packed [S, heads, D]
     batch, and the pointers of its two integer vectors."""
@@ -740,7 +907,7 @@ def _table(page_table, B):
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, phases=None,
               mscale=1.0, interleaved=False, positions=None, start=0, cu_seqlens=None,
-              stream=None):
+              stream=None, q_weight=None, k_weight=None, eps=None, offset=0.0):
     """Writes the new tokens' k (rotated) and v into the paged cache; returns q rotated (None
     without q).
 
@@ -748,7 +915,11 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, p
     [B + 1]); k_pages, v_pages: bf16 [n_pages, page_size, heads, D] (any strides with contiguous
     D); page_table: int32 [B, max_pages]; seq_len: int32 [B], each sequence's tokens in its own
     pages with the new ones. Positions: positions (int64, one a row), or start + a token's index
-    in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place)."""
+    in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place).
+    eps: each head of q and k is normed before, with q_weight, k_weight and offset, as by
+    norm_rope_forward."""
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("a norm's weights without its eps")
     B, S, dims, lens, cu = _batch(k, cu_seqlens, seq_len)
     shape = k.shape
     lead, D = shape[:-2], k_pages.shape[-1]
@@ -771,12 +942,19 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, p
             raise ValueError(f"q and q_out must be {tuple(lead)} + [heads, {D}], not "
                              f"{tuple(q.shape)} and {tuple(q_out.shape)}")
         qv, qo = _heads(q, "q", dims), _heads(q_out, "q_out", dims)
-    st = _lib.upipe_kv_append(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims),
-                              _pages(k_pages, v_pages), table, ts, mp, lens, cu, pos, start, ph,
-                              mscale, B, S, rot or 0, 1 if interleaved else 0,
-                              _stream(stream, k))
+    if eps is None:
+        st = _lib.upipe_kv_append(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims),
+                                  _pages(k_pages, v_pages), table, ts, mp, lens, cu, pos, start,
+                                  ph, mscale, B, S, rot or 0, 1 if interleaved else 0,
+                                  _stream(stream, k))
+    else:
+        norm = _norm(q_weight if q is not None else None, k_weight, D, offset, eps)
+        st = _lib.upipe_kv_append_norm(qv, qo, _heads(k, "k", dims), _heads(v, "v", dims), norm,
+                                       _pages(k_pages, v_pages), table, ts, mp, lens, cu, pos,
+                                       start, ph, mscale, B, S, rot or 0, 1 if interleaved else 0,
+                                       _stream(stream, k))
     if st:
-        raise UpipeError(st, "upipe_kv_append")
+        raise UpipeError(st, "upipe_kv_append" if eps is None else "upipe_kv_append_norm")
     return q_out if q is not None else None
 
 

@@ -337,6 +337,31 @@ struct RopeArgs {
 cudaError_t launch_rope(RopeArgs a, bool interleaved, bool append, int64_t tokens,
                         cudaStream_t stream);
 
+// ---- head norms with the rotation (norm_rope.cu) -------------------------------------------
+// r: the tensors, positions and (append) cache as above; the backward's sources are the gradients
+// of the outputs, its destinations those of the inputs x. Tensors 0 and 1 are normed.
+struct NormArgs {
+  RopeArgs r;
+  const void* w[2];         // [D] weights of q's and k's heads, bf16 or (wide) float32; NULL: ones
+  int wide;
+  float offset, eps;        // the weights are offset + w
+  const __nv_bfloat16* x[2];
+  int64_t x_b[2], x_s[2], x_h[2];
+  int64_t tokens;           // backward
+  float* part;              // backward: [blocks][2][D] partial sums of dw, or NULL
+  // set by the launchers
+  int lanes, log_lanes, groups[3];
+  float inv_d;
+};
+cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t tokens,
+                             cudaStream_t stream);
+// Blocks of the backward (host arithmetic); part holds 2 D floats for each.
+constexpr int kNormBwdBlocks = 608;
+int norm_bwd_blocks(int64_t tokens, int D, int heads_q, int heads_k);
+// dq_w, dk_w: float32 [D], written; either may be NULL.
+cudaError_t launch_norm_rope_bwd(NormArgs a, bool interleaved, float* dq_w, float* dk_w,
+                                 cudaStream_t stream);
+
 // ---- attention over a paged cache (attn_paged.cu) -------------------------------------------
 // Builds a 4-D bf16 tensor map [n_pages][heads][page_size][D] over one cache with the given
 // element strides and a box of box_rows slots x 64 features of one head, 128-byte swizzle.

@@ -1,4 +1,4 @@
-// C entries of the rotary positions, the paged key/value cache and the attention over it:
+// C entries of the rotary positions, the head norms, the paged key/value cache and the attention over it:
 // argument checks (all before anything is enqueued), workspace plan and launches.
 #include <cmath>
 #include <cstdarg>
@@ -122,24 +122,28 @@ bool same_place(const upipe_heads* x, const upipe_heads* y) {
 
 bool present(const upipe_heads* t) { return t && t->heads != 0; }
 
-int check_rot(int D, int rot) {
+int check_features(int D) {
   if (D < 8 || D > 1024 || D % 8)
     return pfail(UPIPE_ERR_UNSUPPORTED, "D=%d (supported: multiples of 8 up to 1024)", D);
+  return UPIPE_OK;
+}
+
+int check_rot(int D, int rot) {
+  const int st = check_features(D);
+  if (st != UPIPE_OK) return st;
   if (rot < 16 || rot > D || rot % 16)
     return pfail(UPIPE_ERR_UNSUPPORTED, "rot_dim=%d (supported: multiples of 16 up to D)", rot);
   return UPIPE_OK;
 }
 
-int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
-         const upipe_heads* k_out, const int64_t* pos, int64_t pos0, const uint64_t* phase,
-         double mscale, int B, int64_t S, int D, int rot, int interleaved, bool back,
-         void* stream) {
-  const NvtxRange range(where);
-  set_last_error("");
+// Sizes, rotation (with_rot) and presence of the tensors of a call on q and k.
+int check_rope_sizes(const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+                     const upipe_heads* k_out, double mscale, int B, int64_t S, int D, int rot,
+                     int interleaved, bool with_rot) {
   if (B < 0 || S < 0) return pfail(UPIPE_ERR_INVALID_ARG, "B=%d S=%lld", B, (long long)S);
   if (B > 0 && S > (int64_t(1) << 40) / B)
     return pfail(UPIPE_ERR_UNSUPPORTED, "more than 2^40 tokens");
-  int st = check_rot(D, rot);
+  const int st = with_rot ? check_rot(D, rot) : check_features(D);
   if (st != UPIPE_OK) return st;
   if (interleaved != 0 && interleaved != 1)
     return pfail(UPIPE_ERR_INVALID_ARG, "interleaved must be 0 or 1");
@@ -148,46 +152,90 @@ int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const up
   if (!has_q && !has_k) return pfail(UPIPE_ERR_INVALID_ARG, "neither q nor k");
   if ((has_q && !present(q_out)) || (has_k && !present(k_out)))
     return pfail(UPIPE_ERR_INVALID_ARG, "an input without its output");
-  if (B == 0 || S == 0) return UPIPE_OK;
+  return UPIPE_OK;
+}
+
+// Their tensors and positions into a, their pointers into p (not looked up yet).
+int check_rope_tensors(const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+                       const upipe_heads* k_out, const int64_t* pos, int64_t pos0,
+                       const uint64_t* phase, double mscale, int B, int64_t S, int D, int rot,
+                       bool back, bool with_rot, RopeArgs* a, Placed* p) {
+  const bool has_q = present(q), has_k = present(k);
   if ((has_q ? static_cast<int64_t>(q->heads) : 0) + (has_k ? k->heads : 0) > 65536)
     return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
-  Placed p;
-  RopeArgs a{};
   bool in_place = true;
   const upipe_heads* in[2] = {q, k};
   const upipe_heads* out[2] = {q_out, k_out};
   const char* names[4] = {"q", "k", "q_out", "k_out"};
+  int st = UPIPE_OK;
   for (int i = 0; i < 2; ++i) {
     if (!present(in[i])) continue;
     if (in[i]->heads != out[i]->heads)
       return pfail(UPIPE_ERR_INVALID_ARG, "%s and %s differ in heads", names[i], names[2 + i]);
-    st = check_heads(in[i], names[i], B, S, D, false, &p);
-    if (st == UPIPE_OK) st = check_heads(out[i], names[2 + i], B, S, D, true, &p);
+    st = check_heads(in[i], names[i], B, S, D, false, p);
+    if (st == UPIPE_OK) st = check_heads(out[i], names[2 + i], B, S, D, true, p);
     if (st != UPIPE_OK) return st;
-    set_view(&a, i, in[i], out[i]);
+    set_view(a, i, in[i], out[i]);
     in_place = in_place && same_place(in[i], out[i]);
   }
   if (has_q && has_k && q_out->data == k_out->data)
     return pfail(UPIPE_ERR_INVALID_ARG, "q_out and k_out are one tensor");
-  st = p.add(phase, "phase", 16);
-  if (st == UPIPE_OK && pos) st = p.add(pos, "pos", 8);
+  if (with_rot) st = p->add(phase, "phase", 16);
+  if (st == UPIPE_OK && pos) st = p->add(pos, "pos", 8);
+  a->B = B;
+  a->S = S;
+  a->D = D;
+  a->rot = with_rot ? rot : 0;
+  a->copy_tail = a->rot < D && !in_place;
+  a->pos = pos;
+  a->pos0 = pos0;
+  a->phase = phase;
+  a->mscale = static_cast<float>(mscale);
+  a->sin_scale = back ? -a->mscale : a->mscale;
+  return st;
+}
+
+int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+         const upipe_heads* k_out, const int64_t* pos, int64_t pos0, const uint64_t* phase,
+         double mscale, int B, int64_t S, int D, int rot, int interleaved, bool back,
+         void* stream) {
+  const NvtxRange range(where);
+  set_last_error("");
+  int st = check_rope_sizes(q, k, q_out, k_out, mscale, B, S, D, rot, interleaved, true);
+  if (st != UPIPE_OK || B == 0 || S == 0) return st;
+  Placed p;
+  RopeArgs a{};
+  st = check_rope_tensors(q, k, q_out, k_out, pos, pos0, phase, mscale, B, S, D, rot, back, true,
+                          &a, &p);
   if (st == UPIPE_OK) st = p.resolve();
   if (st != UPIPE_OK) return st;
-  a.B = B;
-  a.S = S;
-  a.D = D;
-  a.rot = rot;
-  a.copy_tail = rot < D && !in_place;
-  a.pos = pos;
-  a.pos0 = pos0;
-  a.phase = phase;
-  a.mscale = static_cast<float>(mscale);
-  a.sin_scale = back ? -a.mscale : a.mscale;
   const DeviceGuard dguard;
   PAGED_CUDA(cudaSetDevice(p.dev));
   PAGED_CUDA(launch_rope(a, interleaved != 0, false, static_cast<int64_t>(B) * S,
                          static_cast<cudaStream_t>(stream)));
   return UPIPE_OK;
+}
+
+// The norm of a call on heads of D features: into a, the weights' pointers into p.
+int check_norm(const upipe_norm* n, bool has_q, bool has_k, int D, NormArgs* a, Placed* p) {
+  if (!n) return pfail(UPIPE_ERR_INVALID_ARG, "norm is NULL");
+  if (D > 512) return pfail(UPIPE_ERR_UNSUPPORTED, "D=%d (a norm takes up to 512)", D);
+  if (!(n->eps >= 0.0) || !std::isfinite(n->eps) || !std::isfinite(n->offset))
+    return pfail(UPIPE_ERR_INVALID_ARG, "norm: eps must be finite and not negative, offset finite");
+  if (n->wide != 0 && n->wide != 1) return pfail(UPIPE_ERR_INVALID_ARG, "norm: wide must be 0 or 1");
+  a->w[0] = has_q ? n->q_weight : nullptr;
+  a->w[1] = has_k ? n->k_weight : nullptr;
+  a->wide = n->wide;
+  a->offset = static_cast<float>(n->offset);
+  a->eps = static_cast<float>(n->eps);
+  int st = UPIPE_OK;
+  if (a->w[0]) st = p->add(a->w[0], "q_weight", 16);
+  if (st == UPIPE_OK && a->w[1]) st = p->add(a->w[1], "k_weight", 16);
+  return st;
+}
+
+size_t norm_workspace(int64_t tokens, int D, int heads_q, int heads_k) {
+  return al256(static_cast<size_t>(norm_bwd_blocks(tokens, D, heads_q, heads_k)) * 2 * D * 4);
 }
 
 int check_pages(const upipe_pages* c, Placed* p) {
@@ -261,6 +309,104 @@ int attn_plan(int B, int64_t rows, int Hq, int Hkv, int D, int64_t prefix_len, i
   p->slot_ml = take(sl * 16);
   p->desc = take(2 * static_cast<size_t>(rows) * Hq * 8);
   p->total = off;
+  return UPIPE_OK;
+}
+
+// New keys (rotated, with_norm: normed before) and values into the cache, q the same into q_out.
+int append(const char* where, bool with_norm, const upipe_norm* norm, const upipe_heads* q,
+           const upipe_heads* q_out, const upipe_heads* k, const upipe_heads* v,
+           const upipe_pages* cache, const int32_t* page_table, int64_t table_stride,
+           int64_t max_pages, const int32_t* seq_len, const int32_t* cu_rows, const int64_t* pos,
+           int64_t pos0, const uint64_t* phase, double mscale, int B, int64_t S, int rot_dim,
+           int interleaved, void* stream) {
+  const NvtxRange range(where);
+  set_last_error("");
+  if (B < 0 || S < 0) return pfail(UPIPE_ERR_INVALID_ARG, "B=%d S=%lld", B, (long long)S);
+  if (S > 0x7fffffff || (B > 0 && S > (int64_t(1) << 40) / B))
+    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 2^31 rows a sequence or 2^40 rows");
+  if (!present(k) || !present(v)) return pfail(UPIPE_ERR_INVALID_ARG, "k or v is missing");
+  if (interleaved != 0 && interleaved != 1)
+    return pfail(UPIPE_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  Placed p;
+  int st = check_pages(cache, &p);
+  if (st != UPIPE_OK) return st;
+  const int D = cache->D;
+  if (phase) {
+    st = check_rot(D, rot_dim);
+    if (st != UPIPE_OK) return st;
+    if (!std::isfinite(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite");
+  } else if ((st = check_features(D)) != UPIPE_OK) {
+    return st;
+  }
+  if (k->heads != cache->heads || v->heads != cache->heads)
+    return pfail(UPIPE_ERR_INVALID_ARG, "k and v have %d and %d heads, the cache %d", k->heads,
+                 v->heads, cache->heads);
+  const bool has_q = present(q);
+  if (has_q && (!present(q_out) || q_out->heads != q->heads))
+    return pfail(UPIPE_ERR_INVALID_ARG, "q_out is missing or differs from q in heads");
+  if (2 * static_cast<int64_t>(k->heads) + (has_q ? q->heads : 0) > 65536)
+    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
+  if (max_pages < 1 || (B > 1 && table_stride < max_pages))
+    return pfail(UPIPE_ERR_INVALID_ARG, "max_pages=%lld table_stride=%lld", (long long)max_pages,
+                 (long long)table_stride);
+  if (may_overlap({cache->stride_page, cache->stride_slot, cache->stride_head},
+                  {cache->n_pages, cache->page_size, cache->heads}, D))
+    return pfail(UPIPE_ERR_INVALID_ARG, "cache: pages, slots or heads overlap");
+  NormArgs na{};
+  if (with_norm) {
+    st = check_norm(norm, has_q, true, D, &na, &p);
+    if (st != UPIPE_OK) return st;
+  }
+  if (B == 0 || S == 0) return UPIPE_OK;
+  const int64_t vb = cu_rows ? 1 : B;
+  RopeArgs& a = na.r;
+  if (has_q) {
+    st = check_heads(q, "q", vb, S, D, false, &p);
+    if (st == UPIPE_OK) st = check_heads(q_out, "q_out", vb, S, D, true, &p);
+    if (st != UPIPE_OK) return st;
+    set_view(&a, 0, q, q_out);
+  }
+  st = check_heads(k, "k", vb, S, D, false, &p);
+  if (st == UPIPE_OK) st = check_heads(v, "v", vb, S, D, false, &p);
+  if (st == UPIPE_OK) st = p.add(page_table, "page_table", 4);
+  if (st == UPIPE_OK) st = p.add(seq_len, "seq_len", 4);
+  if (st == UPIPE_OK && cu_rows) st = p.add(cu_rows, "cu_rows", 4);
+  if (st == UPIPE_OK && pos) st = p.add(pos, "pos", 8);
+  if (st == UPIPE_OK && phase) st = p.add(phase, "phase", 16);
+  if (st == UPIPE_OK) st = p.resolve();
+  if (st != UPIPE_OK) return st;
+  set_view(&a, 1, k, nullptr);
+  set_view(&a, 2, v, nullptr);
+  a.dst[1] = static_cast<__nv_bfloat16*>(cache->k);
+  a.dst[2] = static_cast<__nv_bfloat16*>(cache->v);
+  a.B = B;
+  a.S = S;
+  a.D = D;
+  a.rot = phase ? rot_dim : 0;
+  a.copy_tail = a.rot < D;
+  a.pos = pos;
+  a.pos0 = pos0;
+  a.phase = phase;
+  a.mscale = a.sin_scale = static_cast<float>(mscale);
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  a.page_stride = cache->stride_page;
+  a.slot_stride = cache->stride_slot;
+  a.head_stride = cache->stride_head;
+  a.seq_len = seq_len;
+  a.cu = cu_rows;
+  const DeviceGuard dguard;
+  PAGED_CUDA(cudaSetDevice(p.dev));
+  st = device_status_word(p.dev, &a.err);
+  if (st != UPIPE_OK) return st;
+  const int64_t rows = cu_rows ? S : static_cast<int64_t>(B) * S;
+  if (with_norm)
+    PAGED_CUDA(launch_norm_rope(na, interleaved != 0, true, rows, static_cast<cudaStream_t>(stream)));
+  else
+    PAGED_CUDA(launch_rope(a, interleaved != 0, true, rows, static_cast<cudaStream_t>(stream)));
   return UPIPE_OK;
 }
 
@@ -356,86 +502,122 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
                     const int32_t* cu_rows, const int64_t* pos, int64_t pos0,
                     const uint64_t* phase, double mscale, int B, int64_t S, int rot_dim,
                     int interleaved, void* stream) {
-  const NvtxRange range("upipe_kv_append");
+  return append("upipe_kv_append", false, nullptr, q, q_out, k, v, cache, page_table, table_stride,
+                max_pages, seq_len, cu_rows, pos, pos0, phase, mscale, B, S, rot_dim, interleaved,
+                stream);
+}
+
+int upipe_kv_append_norm(const upipe_heads* q, const upipe_heads* q_out, const upipe_heads* k,
+                         const upipe_heads* v, const upipe_norm* norm, const upipe_pages* cache,
+                         const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                         const int32_t* seq_len, const int32_t* cu_rows, const int64_t* pos,
+                         int64_t pos0, const uint64_t* phase, double mscale, int B, int64_t S,
+                         int rot_dim, int interleaved, void* stream) {
+  return append("upipe_kv_append_norm", true, norm, q, q_out, k, v, cache, page_table,
+                table_stride, max_pages, seq_len, cu_rows, pos, pos0, phase, mscale, B, S, rot_dim,
+                interleaved, stream);
+}
+
+int upipe_norm_rope_fwd(const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+                        const upipe_heads* k_out, const upipe_norm* norm, const int64_t* pos,
+                        int64_t pos0, const uint64_t* phase, double mscale, int B, int64_t S,
+                        int D, int rot_dim, int interleaved, void* stream) {
+  const NvtxRange range("upipe_norm_rope_fwd");
   set_last_error("");
-  if (B < 0 || S < 0) return pfail(UPIPE_ERR_INVALID_ARG, "B=%d S=%lld", B, (long long)S);
-  if (S > 0x7fffffff || (B > 0 && S > (int64_t(1) << 40) / B))
-    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 2^31 rows a sequence or 2^40 rows");
-  if (!present(k) || !present(v)) return pfail(UPIPE_ERR_INVALID_ARG, "k or v is missing");
-  if (interleaved != 0 && interleaved != 1)
-    return pfail(UPIPE_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  const bool with_rot = phase != nullptr;
+  int st = check_rope_sizes(q, k, q_out, k_out, mscale, B, S, D, rot_dim, interleaved, with_rot);
   Placed p;
-  int st = check_pages(cache, &p);
-  if (st != UPIPE_OK) return st;
-  const int D = cache->D;
-  if (phase) {
-    st = check_rot(D, rot_dim);
-    if (st != UPIPE_OK) return st;
-    if (!std::isfinite(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite");
-  } else if (D < 8 || D > 1024 || D % 8) {
-    return pfail(UPIPE_ERR_UNSUPPORTED, "D=%d (supported: multiples of 8 up to 1024)", D);
-  }
-  if (k->heads != cache->heads || v->heads != cache->heads)
-    return pfail(UPIPE_ERR_INVALID_ARG, "k and v have %d and %d heads, the cache %d", k->heads,
-                 v->heads, cache->heads);
-  const bool has_q = present(q);
-  if (has_q && (!present(q_out) || q_out->heads != q->heads))
-    return pfail(UPIPE_ERR_INVALID_ARG, "q_out is missing or differs from q in heads");
-  if (2 * static_cast<int64_t>(k->heads) + (has_q ? q->heads : 0) > 65536)
-    return pfail(UPIPE_ERR_UNSUPPORTED, "more than 65536 heads");
-  if (max_pages < 1 || (B > 1 && table_stride < max_pages))
-    return pfail(UPIPE_ERR_INVALID_ARG, "max_pages=%lld table_stride=%lld", (long long)max_pages,
-                 (long long)table_stride);
-  if (may_overlap({cache->stride_page, cache->stride_slot, cache->stride_head},
-                  {cache->n_pages, cache->page_size, cache->heads}, D))
-    return pfail(UPIPE_ERR_INVALID_ARG, "cache: pages, slots or heads overlap");
-  if (B == 0 || S == 0) return UPIPE_OK;
-  const int64_t vb = cu_rows ? 1 : B;
-  RopeArgs a{};
-  if (has_q) {
-    st = check_heads(q, "q", vb, S, D, false, &p);
-    if (st == UPIPE_OK) st = check_heads(q_out, "q_out", vb, S, D, true, &p);
-    if (st != UPIPE_OK) return st;
-    set_view(&a, 0, q, q_out);
-  }
-  st = check_heads(k, "k", vb, S, D, false, &p);
-  if (st == UPIPE_OK) st = check_heads(v, "v", vb, S, D, false, &p);
-  if (st == UPIPE_OK) st = p.add(page_table, "page_table", 4);
-  if (st == UPIPE_OK) st = p.add(seq_len, "seq_len", 4);
-  if (st == UPIPE_OK && cu_rows) st = p.add(cu_rows, "cu_rows", 4);
-  if (st == UPIPE_OK && pos) st = p.add(pos, "pos", 8);
-  if (st == UPIPE_OK && phase) st = p.add(phase, "phase", 16);
+  NormArgs a{};
+  if (st == UPIPE_OK) st = check_norm(norm, present(q), present(k), D, &a, &p);
+  if (st != UPIPE_OK || B == 0 || S == 0) return st;
+  st = check_rope_tensors(q, k, q_out, k_out, pos, pos0, phase, mscale, B, S, D, rot_dim, false,
+                          with_rot, &a.r, &p);
   if (st == UPIPE_OK) st = p.resolve();
   if (st != UPIPE_OK) return st;
-  set_view(&a, 1, k, nullptr);
-  set_view(&a, 2, v, nullptr);
-  a.dst[1] = static_cast<__nv_bfloat16*>(cache->k);
-  a.dst[2] = static_cast<__nv_bfloat16*>(cache->v);
-  a.B = B;
-  a.S = S;
-  a.D = D;
-  a.rot = phase ? rot_dim : 0;
-  a.copy_tail = a.rot < D;
-  a.pos = pos;
-  a.pos0 = pos0;
-  a.phase = phase;
-  a.mscale = a.sin_scale = static_cast<float>(mscale);
-  a.table = page_table;
-  a.table_stride = table_stride;
-  a.max_pages = max_pages;
-  a.n_pages = cache->n_pages;
-  a.page_size = cache->page_size;
-  a.page_stride = cache->stride_page;
-  a.slot_stride = cache->stride_slot;
-  a.head_stride = cache->stride_head;
-  a.seq_len = seq_len;
-  a.cu = cu_rows;
   const DeviceGuard dguard;
   PAGED_CUDA(cudaSetDevice(p.dev));
-  st = device_status_word(p.dev, &a.err);
+  PAGED_CUDA(launch_norm_rope(a, interleaved != 0, false, static_cast<int64_t>(B) * S,
+                              static_cast<cudaStream_t>(stream)));
+  return UPIPE_OK;
+}
+
+size_t upipe_norm_rope_workspace_bytes(int B, int64_t S, int Hq, int Hkv, int D) {
+  if (B < 1 || S < 1 || S > (int64_t(1) << 40) / B || Hq < 0 || Hkv < 0 ||
+      static_cast<int64_t>(Hq) + Hkv < 1 || static_cast<int64_t>(Hq) + Hkv > 65536 || D < 8 ||
+      D > 512 || D % 8)
+    return 0;
+  return norm_workspace(B * S, D, Hq, Hkv);
+}
+
+int upipe_norm_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const upipe_heads* q,
+                        const upipe_heads* k, const upipe_heads* dq, const upipe_heads* dk,
+                        float* dq_weight, float* dk_weight, const upipe_norm* norm,
+                        const int64_t* pos, int64_t pos0, const uint64_t* phase, double mscale,
+                        int B, int64_t S, int D, int rot_dim, int interleaved, void* workspace,
+                        size_t workspace_bytes, void* stream_) {
+  const NvtxRange range("upipe_norm_rope_bwd");
+  set_last_error("");
+  const bool with_rot = phase != nullptr;
+  int st = check_rope_sizes(dq_out, dk_out, dq, dk, mscale, B, S, D, rot_dim, interleaved,
+                            with_rot);
+  Placed p;
+  NormArgs a{};
+  const bool has[2] = {present(dq_out), present(dk_out)};
+  if (st == UPIPE_OK) st = check_norm(norm, has[0], has[1], D, &a, &p);
   if (st != UPIPE_OK) return st;
-  PAGED_CUDA(launch_rope(a, interleaved != 0, true, cu_rows ? S : static_cast<int64_t>(B) * S,
-                         static_cast<cudaStream_t>(stream)));
+  float* const dw[2] = {dq_weight, dk_weight};
+  const char* const dw_names[2] = {"dq_weight", "dk_weight"};
+  for (int i = 0; i < 2; ++i) {
+    if (!dw[i]) continue;
+    if (!a.w[i]) return pfail(UPIPE_ERR_INVALID_ARG, "%s without the weights", dw_names[i]);
+    st = p.add(dw[i], dw_names[i], 4);
+    if (st != UPIPE_OK) return st;
+  }
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const bool sums = dq_weight || dk_weight;
+  if (B == 0 || S == 0) {  // no token: the weights' gradients are zeros
+    if (!sums) return UPIPE_OK;
+    st = p.resolve();
+    if (st != UPIPE_OK) return st;
+    const DeviceGuard dguard;
+    PAGED_CUDA(cudaSetDevice(p.dev));
+    for (float* w : dw)
+      if (w) PAGED_CUDA(cudaMemsetAsync(w, 0, static_cast<size_t>(D) * 4, stream));
+    return UPIPE_OK;
+  }
+  st = check_rope_tensors(dq_out, dk_out, dq, dk, pos, pos0, phase, mscale, B, S, D, rot_dim, true,
+                          with_rot, &a.r, &p);
+  if (st != UPIPE_OK) return st;
+  const upipe_heads* x[2] = {q, k};
+  const upipe_heads* dy[2] = {dq_out, dk_out};
+  const char* const names[2] = {"the forward's q", "the forward's k"};
+  for (int i = 0; i < 2; ++i) {
+    if (!has[i]) continue;
+    if (!present(x[i]) || x[i]->heads != dy[i]->heads)
+      return pfail(UPIPE_ERR_INVALID_ARG, "%s is missing or differs from its gradient in heads",
+                   names[i]);
+    st = check_heads(x[i], names[i], B, S, D, false, &p);
+    if (st != UPIPE_OK) return st;
+    a.x[i] = static_cast<const __nv_bfloat16*>(x[i]->data);
+    a.x_b[i] = x[i]->stride_b;
+    a.x_s[i] = x[i]->stride_s;
+    a.x_h[i] = x[i]->stride_h;
+  }
+  if (sums) {
+    const size_t need = norm_workspace(static_cast<int64_t>(B) * S, D, a.r.heads[0], a.r.heads[1]);
+    st = p.add(workspace, "workspace", 256);
+    if (st != UPIPE_OK) return st;
+    if (workspace_bytes < need)
+      return pfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes,
+                   need);
+    a.part = static_cast<float*>(workspace);
+  }
+  st = p.resolve();
+  if (st != UPIPE_OK) return st;
+  a.tokens = static_cast<int64_t>(B) * S;
+  const DeviceGuard dguard;
+  PAGED_CUDA(cudaSetDevice(p.dev));
+  PAGED_CUDA(launch_norm_rope_bwd(a, interleaved != 0, dq_weight, dk_weight, stream));
   return UPIPE_OK;
 }
 

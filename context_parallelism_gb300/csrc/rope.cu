@@ -19,10 +19,8 @@
 // 387 us, 6.9 TB/s (2 heads a thread 464 us, 6 heads 410); 8192 tokens 30.8 us, of which the ramp
 // is 5. Blocks of 64 threads end and start evenly: 256 cost 3 %. Streaming loads and stores changed
 // nothing.
-#include <cuda_bf16.h>
-
 #include "internal.h"
-#include "ptx.cuh"
+#include "rope.cuh"
 
 namespace upipe {
 namespace {
@@ -30,46 +28,15 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kHeads = 4;  // heads of one token per thread
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
-}
-
-// Two vectors a, b of one head that hold eight pairs: (a_i, b_i) in the half layout,
-// consecutive elements of a and then of b in the interleaved one.
 template <bool kInter>
 __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float (&c)[8],
                                        const float (&s)[8]) {
   float x[8], y[8];
-  unpack8(a, x);
-  unpack8(b, y);
-  float u[8], v[8];
-  if (kInter) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-      u[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-      v[2 * i] = y[2 * i] * c[4 + i] - y[2 * i + 1] * s[4 + i];
-      v[2 * i + 1] = y[2 * i + 1] * c[4 + i] + y[2 * i] * s[4 + i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[i] = x[i] * c[i] - y[i] * s[i];
-      v[i] = y[i] * c[i] + x[i] * s[i];
-    }
-  }
-  a = pack8(u);
-  b = pack8(v);
+  unpack_bf16x8(a, x);
+  unpack_bf16x8(b, y);
+  rotate_pairs<kInter>(x, y, c, s);
+  a = pack_bf16x8(x);
+  b = pack_bf16x8(y);
 }
 
 // Thread -> (token, head group, chunk), chunk fastest: neighbouring lanes read neighbouring
@@ -85,60 +52,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   const int g = static_cast<int>(item - tok32 * a.n_groups);
   const int64_t tok = a.tok0 + tok32;
 
-  // the token's batch row and place, its position and (append) its cache slot
-  int64_t b = 0, i = tok, pos;
-  int64_t slot_k = -1;  // element offset of the token's row in the caches; < 0: not stored
-  if (kAppend) {
-    int n;
-    if (a.cu) {
-      // the sequence that owns row tok: the first whose end lies behind it
-      int lo = 0, hi = a.B;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid + 1] <= tok) lo = mid + 1; else hi = mid;
-      }
-      if (lo >= a.B) return;  // rows behind the last sequence stay as they are
-      b = lo;
-      const int first = a.cu[lo];
-      n = a.cu[lo + 1] - first;
-      i = tok - first;
-      if (i < 0) return;
-    } else {
-      b = a.B == 1 ? 0 : div_fl(tok, a.S);
-      i = tok - b * a.S;
-      n = static_cast<int>(a.S);
-    }
-    const int64_t j = static_cast<int64_t>(a.seq_len[b]) - n + i;
-    pos = a.pos ? a.pos[tok] : a.pos0 + j;
-    if (j >= 0) {
-      const int64_t pg = div_fl(j, a.page_size);
-      const int64_t page = pg < a.max_pages ? a.table[b * a.table_stride + pg] : -1;
-      if (page >= 0 && page < a.n_pages)
-        slot_k = page * a.page_stride + (j - pg * a.page_size) * a.slot_stride;
-      else if (c == 0 && g == 0)
-        atomicOr(a.err, kErrBadPage);
-    }
-    if (a.cu) {
-      b = 0;  // packed rows: the inputs are addressed by row alone
-      i = tok;
-    }
-  } else {
-    b = a.B == 1 ? 0 : div_fl(tok, a.S);
-    i = tok - b * a.S;
-    pos = a.pos ? a.pos[tok] : a.pos0 + i;
-  }
+  TokenPlace at;
+  if (!place_token<kAppend>(a, tok, c == 0 && g == 0, &at)) return;
+  const int64_t b = at.b, i = at.i, slot_k = at.slot;
 
   // this chunk's two vectors of a head
-  const int nr = a.rot >> 4;
-  const bool turns = c < nr;
   int o0, o1;
-  if (turns) {
-    o0 = kInter ? 16 * c : 8 * c;
-    o1 = kInter ? 16 * c + 8 : a.rot / 2 + 8 * c;
-  } else {
-    o0 = a.rot + 16 * (c - nr);
-    o1 = o0 + 8;
-  }
+  const bool turns = chunk_features(c, a.rot, kInter, &o0, &o1);
   const bool two = o1 < a.D;
 
   uint4 va[kHeads], vb[kHeads];
@@ -171,22 +91,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     if (two) vb[j] = *reinterpret_cast<const uint4*>(src + o1);
   }
   float cs[8], sn[8];
-  if (turns) {
-    const ulonglong2* ph = reinterpret_cast<const ulonglong2*>(a.phase) + 4 * c;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const ulonglong2 p = ph[q];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint64_t t = static_cast<uint64_t>(pos) * (e ? p.y : p.x);
-        const float half_turns = __ll2float_rn(static_cast<int64_t>(t)) * 0x1p-63f;
-        float s_, c_;
-        sincospif(half_turns, &s_, &c_);
-        cs[2 * q + e] = c_ * a.mscale;
-        sn[2 * q + e] = s_ * a.sin_scale;
-      }
-    }
-  }
+  if (turns) chunk_angles(a.phase, c, at.pos, a.mscale, a.sin_scale, cs, sn);
 #pragma unroll
   for (int j = 0; j < kHeads; ++j) {
     if (!out[j]) continue;

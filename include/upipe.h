@@ -347,6 +347,47 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
                    double mscale, int B, int64_t S, int D, int rot_dim, int interleaved,
                    void* stream);
 
+/* ---- Head norms with the rotation ------------------------------------------------------------
+ *
+ * Norm of each head of q and k by its root mean square and the rotation of its position, in one
+ * pass, before attention. For a head x of D features with weights w:
+ *   r = (mean x^2 + eps)^(-1/2);  y = R (offset + w) r x,  R the rotation above (the identity
+ * without phase). Backward, for dy: g = R^T dy, t = (offset + w) g, dx = r (t - x r^2 mean(t x)),
+ * dw = the sum over tokens and heads of g r x. fp32 arithmetic, one rounding of y and dx; sums of
+ * dw in fp32, in an order fixed by the shape.
+ */
+
+/* Weights of the two norms: device [D], bf16 or (wide = 1) float32, 16-byte aligned, shared by
+ * the heads of their tensor. NULL: all ones (offset is not added). offset: 0, or 1 for weights that
+ * are kept as their distance from one. eps >= 0. */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  double offset, eps;
+  int32_t wide;
+} upipe_norm;
+
+/*
+ * As upipe_rope_fwd, with the norm before the rotation; phase = NULL: nothing is rotated. D up to
+ * 512. The backward takes the outputs' gradients (dq_out, dk_out) and the forward's inputs (q, k) and
+ * writes dq, dk (each its gradient in place, or overlapping no other tensor) and dq_weight, dk_weight
+ * (device float32 [D], overwritten; NULL: not wanted; only for weights that are there).
+ *   workspace: 256-byte aligned, >= upipe_norm_rope_workspace_bytes(...); without dq_weight and
+ *   dk_weight none is needed (NULL). Calls that may run at the same time need their own.
+ * No token: the weights' gradients are zeros and nothing else happens.
+ */
+int upipe_norm_rope_fwd(const upipe_heads* q, const upipe_heads* k, const upipe_heads* q_out,
+                        const upipe_heads* k_out, const upipe_norm* norm, const int64_t* pos,
+                        int64_t pos0, const uint64_t* phase, double mscale, int B, int64_t S,
+                        int D, int rot_dim, int interleaved, void* stream);
+size_t upipe_norm_rope_workspace_bytes(int B, int64_t S, int Hq, int Hkv, int D);
+int upipe_norm_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const upipe_heads* q,
+                        const upipe_heads* k, const upipe_heads* dq, const upipe_heads* dk,
+                        float* dq_weight, float* dk_weight, const upipe_norm* norm,
+                        const int64_t* pos, int64_t pos0, const uint64_t* phase, double mscale,
+                        int B, int64_t S, int D, int rot_dim, int interleaved, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* ---- Paged key/value cache and attention over it ------------------------------------------
  *
  * Serving after a prefill (upipe_attn_fwd with lse = NULL): new keys and values go into a paged
@@ -395,6 +436,14 @@ int upipe_kv_append(const upipe_heads* q, const upipe_heads* q_out, const upipe_
                     const int32_t* cu_rows, const int64_t* pos, int64_t pos0,
                     const uint64_t* phase, double mscale, int B, int64_t S, int rot_dim,
                     int interleaved, void* stream);
+
+/* The same with the norm of each head of q and k before the rotation (D up to 512). */
+int upipe_kv_append_norm(const upipe_heads* q, const upipe_heads* q_out, const upipe_heads* k,
+                         const upipe_heads* v, const upipe_norm* norm, const upipe_pages* cache,
+                         const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                         const int32_t* seq_len, const int32_t* cu_rows, const int64_t* pos,
+                         int64_t pos0, const uint64_t* phase, double mscale, int B, int64_t S,
+                         int rot_dim, int interleaved, void* stream);
 
 /*
  * o = softmax(q k^T / sqrt(D)) v over the keys that each row sees: the first prefix_len tokens of
@@ -448,7 +497,10 @@ enum {
   UPIPE_K_ATTN_PAGED = 13, /* attention over the paged cache: own pages (and short prefixes) */
   UPIPE_K_PAGED_MERGE = 14, /* joins the parts of its rows */
   UPIPE_K_ATTN_PREFIX = 15, /* the shared prefix on 128-row tensor-core tiles */
-  UPIPE_K_COUNT = 16
+  UPIPE_K_NORM_ROPE = 16, /* head norms with the rotation, into the paged cache too */
+  UPIPE_K_EMBED = 17,     /* token embedding, its gradient and the sort of the tokens */
+  UPIPE_K_LOGP = 18,      /* token log probabilities: short calls' logits, selection */
+  UPIPE_K_COUNT = 19
 };
 
 typedef struct {

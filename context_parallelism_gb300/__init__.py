@@ -97,6 +97,9 @@ SIGNATURES = {
     "upipe_mlp_fwd": (_i, [_vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz, _vp]),
     "upipe_mlp_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz,
                            _vp]),
+    "upipe_embed_fwd": (_i, [_vp, _vp, _vp, _i64, _i, _i64, _d, _vp]),
+    "upipe_embed_workspace_bytes": (_sz, [_i64, _i, _i64]),
+    "upipe_embed_bwd": (_i, [_vp, _vp, _vp, _i64, _i, _i64, _d, _i, _vp, _sz, _vp]),
     "upipe_rope_frequencies": (_i, [ctypes.POINTER(_d), ctypes.POINTER(_d), _i, _d, _i, _d, _d,
                                     _d, _d]),
     "upipe_rope_phases": (_i, [ctypes.POINTER(_d), ctypes.POINTER(_u64), _i]),
@@ -338,6 +341,25 @@ def upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspa
                             _ptr(dw_d), S, Dm, F, seq_tile, _ptr(workspace), wb,
                             _stream(stream, x, dx, workspace))
     _check(st, "upipe_mlp_bwd")
+
+
+def upipe_embed_fwd(token, w, h, S, Dm, V, scale=1.0, stream=None):
+    _check(_lib.upipe_embed_fwd(_ptr(token), _ptr(w), _ptr(h), S, Dm, V, scale,
+                                _stream(stream, h, w)), "upipe_embed_fwd")
+
+
+@functools.lru_cache(maxsize=4096)
+def upipe_embed_workspace_bytes(S, Dm, V):
+    return int(_lib.upipe_embed_workspace_bytes(S, Dm, V))
+
+
+def upipe_embed_bwd(token, dh, dw, S, Dm, V, scale, add, workspace, workspace_bytes=None,
+                    stream=None):
+    wb = workspace_bytes
+    if wb is None:
+        wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.upipe_embed_bwd(_ptr(token), _ptr(dh), _ptr(dw), S, Dm, V, scale, int(add),
+                                _ptr(workspace), wb, _stream(stream, dw, dh)), "upipe_embed_bwd")
 
 
 def upipe_rope_frequencies(rot_dim, theta=10000.0, scaling=UPIPE_ROPE_PLAIN, factor=1.0,
@@ -635,6 +657,56 @@ def mlp_backward(x, w_gu, w_d, dy, seq_tile=8192, workspace=None, stream=None,
     upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspace, None,
                   stream)
     return dx, dw_gu, dw_d
+
+
+# ---- token embedding ------------------------------------------------------------------------
+
+def _matrix(t, name, dtype, dims=2):
+    """Checks a dense tensor whose last dimension is a row of features; returns its sizes."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() < dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {dims} dimensions or more, not "
+                         f"{tuple(t.shape)}")
+    return t.shape
+
+
+def embed_forward(tokens, w, scale=1.0, stream=None):
+    """h = scale * w[tokens], bf16 [*tokens.shape, Dm]: tokens int64, w bf16 [V, Dm]. A negative
+    token (padding) gives zeros, one beyond the table NaN."""
+    torch = _torch or _lazy_torch()
+    shape = _matrix(tokens, "tokens", torch.int64, 0)
+    if len(_matrix(w, "w", torch.bfloat16)) != 2:
+        raise ValueError(f"w must be [V, Dm], not {tuple(w.shape)}")
+    V, Dm = w.shape
+    h = _empty(stream, w, (*shape, Dm), w.dtype)
+    st = _lib.upipe_embed_fwd(tokens.data_ptr(), w.data_ptr(), h.data_ptr(), tokens.numel(), Dm, V,
+                              scale, _stream(stream, w))
+    if st:
+        raise UpipeError(st, "upipe_embed_fwd")
+    return h
+
+
+def embed_backward(tokens, dh, V, scale=1.0, dw=None, workspace=None, stream=None):
+    """The gradient of w (float32 [V, Dm]) from dh (bf16 [*tokens.shape, Dm]). dw: added to instead
+    of a new one (tied weights: the readout's), returned."""
+    torch = _torch or _lazy_torch()
+    shape = _matrix(dh, "dh", torch.bfloat16, 1)
+    if _matrix(tokens, "tokens", torch.int64, 0) != shape[:-1]:
+        raise ValueError(f"dh must be {tuple(tokens.shape)} + [Dm], not {tuple(shape)}")
+    S, Dm, add = tokens.numel(), shape[-1], dw is not None
+    if not add:
+        dw = _empty(stream, dh, (V, Dm), torch.float32)
+    elif _matrix(dw, "dw", torch.float32) != (V, Dm):
+        raise ValueError(f"dw must be [{V}, {Dm}], not {tuple(dw.shape)}")
+    if workspace is None:
+        workspace = _empty(stream, dh, (upipe_embed_workspace_bytes(S, Dm, V),), torch.uint8)
+    st = _lib.upipe_embed_bwd(tokens.data_ptr(), dh.data_ptr(), dw.data_ptr(), S, Dm, V, scale,
+                              1 if add else 0, workspace.data_ptr(), workspace.numel(),
+                              _stream(stream, dh))
+    if st:
+        raise UpipeError(st, "upipe_embed_bwd")
+    return dw
 
 
 # ---- rotary positions, paged cache ----------------------------------------------------------

@@ -428,6 +428,39 @@ cudaError_t launch_attn_prefix(const PagedArgs& a, const CUtensorMap& k_map,
                                const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
+// ---- token embedding (embed.cu) --------------------------------------------------------------
+// h [S][Dm] = scale w[token]; Dm % 8 == 0. Zeros for a negative token, NaN for one beyond the table.
+cudaError_t launch_embed(const int64_t* tokens, const void* w, void* h, int64_t S, int Dm,
+                         int64_t V, float scale, cudaStream_t stream);
+
+// Sizes and workspace (byte offsets) of the gradient; S >= 1, V < 2^31, host arithmetic.
+struct EmbedPlan {
+  int passes, bits;         // of the sort
+  int64_t tiles;            // its blocks
+  int threads, slices;      // of the sums: threads a block, blocks a chunk
+  int chunk;                // places a chunk
+  int64_t chunks;
+  size_t keys[2], places[2], hist, present, part, total;
+};
+EmbedPlan plan_embed(int64_t S, int Dm, int64_t V);
+
+struct EmbedArgs {
+  const int64_t* tokens;    // [S]
+  const __nv_bfloat16* dh;  // [S][Dm]
+  float* dw;                // [V][Dm]
+  int64_t S, V;
+  int Dm;
+  float scale;
+  int add;                  // dw is added to (else written whole)
+  // set by launch_embed_bwd
+  uint32_t* hist;
+  uint32_t* present;        // bitmap of the tokens that occur (not with add)
+  float* part;              // [chunks][2][Dm]
+  int64_t chunks;
+  int chunk, slices;
+};
+cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaStream_t stream);
+
 // ---- services of api.cpp to the other entry points -----------------------------------------
 // Per-device state (streams, status word) for `dev`, created on first use; a upipe status.
 int device_status_word(int dev, uint32_t** err);

@@ -19,6 +19,7 @@
 // while tile i computes, and each tile's outputs are copied out on an outbound copy stream
 // while the next tile computes (the block-input offload the talk lists before sequence
 // tiling: activations live on the host and are brought in when needed).
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -69,8 +70,6 @@ int lfail(int status, const char* fmt, ...) {
 constexpr size_t kAl = 256;
 inline size_t al(size_t x) { return (x + kAl - 1) / kAl * kAl; }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // 0 = device memory (*dev set), 1 = pinned host memory, -1 = anything else.
 int placement(const void* p, int* dev) {
   cudaPointerAttributes at;
@@ -85,14 +84,16 @@ int placement(const void* p, int* dev) {
   return at.type == cudaMemoryTypeHost ? 1 : -1;
 }
 
-// Every pointer non-null and 16-byte aligned; those with may_host[i] may be pinned host memory
-// (host[i] set), every other one device memory of one device (*dev).
+// Every pointer non-null and 16-byte aligned (or align[i]); those with may_host[i] may be pinned host
+// memory (host[i] set), every other one device memory of one device (*dev).
 int check_ptrs(const void* const* ptrs, const char* const* names, const bool* may_host, int n,
-               bool* host, int* dev) {
+               bool* host, int* dev, const int* align = nullptr) {
   int d0 = -1;
   for (int i = 0; i < n; ++i) {
     if (!ptrs[i]) return lfail(UPIPE_ERR_INVALID_ARG, "%s is NULL", names[i]);
-    if (!aligned16(ptrs[i])) return lfail(UPIPE_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+    const int bytes = align ? align[i] : 16;
+    if (reinterpret_cast<uintptr_t>(ptrs[i]) % bytes)
+      return lfail(UPIPE_ERR_INVALID_ARG, "%s is not %d-byte aligned", names[i], bytes);
     int d = -1;
     const int kind = placement(ptrs[i], &d);
     host[i] = kind == 1;
@@ -827,6 +828,99 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
     LOSS_CUDA(launch_gemm_tc(kEpiStoreBf16, false, true, t_dgu_k, t_wgu_mn, gx, cap, stream));
     return UPIPE_OK;
   });
+}
+
+}  // extern "C"
+
+// ---- token embedding -----------------------------------------------------------------------
+
+namespace upipe {
+namespace {
+
+int check_embed(int64_t S, int Dm, int64_t V, double scale) {
+  if (S < 0 || Dm < 1 || V < 1)
+    return lfail(UPIPE_ERR_INVALID_ARG, "S=%lld Dm=%d V=%lld", (long long)S, Dm, (long long)V);
+  if (!std::isfinite(scale)) return lfail(UPIPE_ERR_INVALID_ARG, "scale must be finite");
+  if (Dm % 8 || S > (int64_t(1) << 30) || V >= (int64_t(1) << 31))
+    return lfail(UPIPE_ERR_UNSUPPORTED, "need Dm %% 8 == 0, S <= 2^30, V < 2^31");
+  // blocks of one launch: the places' chunks and the rows that are zeroed
+  const EmbedPlan p = plan_embed(S < 1 ? 1 : S, Dm, V);
+  if (p.chunks * p.slices + V / 16 + 1 > 0x7fffffff ||
+      (S + 7) / 8 * ((Dm + 1023) / 1024) > 0x7fffffff)
+    return lfail(UPIPE_ERR_UNSUPPORTED, "S=%lld Dm=%d: too many blocks", (long long)S, Dm);
+  return UPIPE_OK;
+}
+
+}  // namespace
+}  // namespace upipe
+
+extern "C" {
+
+int upipe_embed_fwd(const int64_t* token, const void* w, void* h, int64_t S, int Dm, int64_t V,
+                    double scale, void* stream) {
+  const NvtxRange range("upipe_embed_fwd");
+  set_last_error("");
+  int st = check_embed(S, Dm, V, scale);
+  if (st != UPIPE_OK || S == 0) return st;
+  const void* ptrs[3] = {token, w, h};
+  const char* names[3] = {"token", "w", "h"};
+  const bool may_host[3] = {false, false, false};
+  bool host[3];
+  int dev = -1;
+  const int align[3] = {8, 16, 16};
+  st = check_ptrs(ptrs, names, may_host, 3, host, &dev, align);
+  if (st != UPIPE_OK) return st;
+  const DeviceGuard dguard;
+  LOSS_CUDA(cudaSetDevice(dev));
+  LOSS_CUDA(launch_embed(token, w, h, S, Dm, V, static_cast<float>(scale),
+                         static_cast<cudaStream_t>(stream)));
+  return UPIPE_OK;
+}
+
+size_t upipe_embed_workspace_bytes(int64_t S, int Dm, int64_t V) {
+  if (check_embed(S, Dm, V, 1.0) != UPIPE_OK || S == 0) return 0;
+  return plan_embed(S, Dm, V).total;
+}
+
+int upipe_embed_bwd(const int64_t* token, const void* dh, float* dw, int64_t S, int Dm, int64_t V,
+                    double scale, int add, void* workspace, size_t workspace_bytes,
+                    void* stream_) {
+  const NvtxRange range("upipe_embed_bwd");
+  set_last_error("");
+  int st = check_embed(S, Dm, V, scale);
+  if (st != UPIPE_OK) return st;
+  if (add != 0 && add != 1) return lfail(UPIPE_ERR_INVALID_ARG, "add must be 0 or 1");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (S == 0 && add) return UPIPE_OK;
+  const void* ptrs[4] = {dw, token, dh, workspace};
+  const char* names[4] = {"dw", "token", "dh", "workspace"};
+  const bool may_host[4] = {false, false, false, false};
+  bool host[4];
+  int dev = -1;
+  const int align[4] = {16, 8, 16, 256};
+  const EmbedPlan p = plan_embed(S ? S : 1, Dm, V);
+  if (S && workspace_bytes < p.total)
+    return lfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes,
+                 p.total);
+  st = check_ptrs(ptrs, names, may_host, S == 0 ? 1 : 4, host, &dev, align);
+  if (st != UPIPE_OK) return st;
+  const DeviceGuard dguard;
+  LOSS_CUDA(cudaSetDevice(dev));
+  if (S == 0) {
+    LOSS_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * Dm * 4, stream));
+    return UPIPE_OK;
+  }
+  EmbedArgs a{};
+  a.tokens = token;
+  a.dh = static_cast<const __nv_bfloat16*>(dh);
+  a.dw = dw;
+  a.S = S;
+  a.V = V;
+  a.Dm = Dm;
+  a.scale = static_cast<float>(scale);
+  a.add = add;
+  LOSS_CUDA(launch_embed_bwd(a, p, static_cast<uint8_t*>(workspace), stream));
+  return UPIPE_OK;
 }
 
 }  // extern "C"

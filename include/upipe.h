@@ -290,6 +290,26 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
                   float* dw_gu, float* dw_d, int64_t S, int Dm, int F, int64_t seq_tile,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Token embedding -------------------------------------------------------------------------
+ *
+ * The other end of the readout: h_i = scale w[token_i], and the gradient of the table, in the layout
+ * of the loss's dw, so that a table that both share (tied weights) collects both gradients:
+ *   dw_v = scale sum over {i : token_i = v} of dh_i   (add = 0: the whole table is written, zeros
+ *   where no token is v; add = 1: added to what is there, rows without a token are not touched).
+ * token [S] int64; a negative one (padding) gives a row of zeros and has no gradient; one beyond the
+ * table gives a row of NaN and has none either. w [V][Dm], h, dh [S][Dm] bf16, dw [V][Dm] float32,
+ * dense. One rounding of h; dw is summed in fp32, in an order that the tokens alone decide: results
+ * repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
+ * Supported: Dm a multiple of 8, S up to 2^30, V below 2^31. S = 0 reads nothing (add = 0: dw becomes
+ * zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
+ * may run at the same time need workspaces of their own.
+ */
+int upipe_embed_fwd(const int64_t* token, const void* w, void* h, int64_t S, int Dm, int64_t V,
+                    double scale, void* stream);
+size_t upipe_embed_workspace_bytes(int64_t S, int Dm, int64_t V);
+int upipe_embed_bwd(const int64_t* token, const void* dh, float* dw, int64_t S, int Dm, int64_t V,
+                    double scale, int add, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Rotary positions --------------------------------------------------------------------
  *
  * The positions of q and k, before attention (training and prefill). For pair i < rot/2 of a

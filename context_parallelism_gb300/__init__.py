@@ -97,6 +97,9 @@ SIGNATURES = {
     "upipe_mlp_fwd": (_i, [_vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz, _vp]),
     "upipe_mlp_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i64, _vp, _sz,
                            _vp]),
+    "upipe_logp_workspace_bytes": (_sz, [_i64, _i, _i64, _i, _i64, _i]),
+    "upipe_logp_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i64, _i, _i64, _vp,
+                            _sz, _vp]),
     "upipe_embed_fwd": (_i, [_vp, _vp, _vp, _i64, _i, _i64, _d, _vp]),
     "upipe_embed_workspace_bytes": (_sz, [_i64, _i, _i64]),
     "upipe_embed_bwd": (_i, [_vp, _vp, _vp, _i64, _i, _i64, _d, _i, _vp, _sz, _vp]),
@@ -341,6 +344,20 @@ def upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspa
                             _ptr(dw_d), S, Dm, F, seq_tile, _ptr(workspace), wb,
                             _stream(stream, x, dx, workspace))
     _check(st, "upipe_mlp_bwd")
+
+
+@functools.lru_cache(maxsize=4096)
+def upipe_logp_workspace_bytes(S, Dm, V, top, seq_tile, host_mask=0):
+    return int(_lib.upipe_logp_workspace_bytes(S, Dm, V, top, seq_tile, int(host_mask)))
+
+
+def upipe_logp_fwd(h, w, target, logp, entropy, lse, top_logp, top_index, S, Dm, V, top, seq_tile,
+                   workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(_lib.upipe_logp_fwd(_ptr(h), _ptr(w), _ptr(target), _ptr(logp), _ptr(entropy), _ptr(lse),
+                               _ptr(top_logp), _ptr(top_index), S, Dm, V, top, seq_tile,
+                               _ptr(workspace), wb, _stream(stream, h, w, workspace)),
+           "upipe_logp_fwd")
 
 
 def upipe_embed_fwd(token, w, h, S, Dm, V, scale=1.0, stream=None):
@@ -657,6 +674,44 @@ def mlp_backward(x, w_gu, w_d, dy, seq_tile=8192, workspace=None, stream=None,
     upipe_mlp_bwd(x, w_gu, w_d, dy, dx, dw_gu, dw_d, S, Dm, F, seq_tile, workspace, None,
                   stream)
     return dx, dw_gu, dw_d
+
+
+# ---- token log probabilities ----------------------------------------------------------------
+
+def token_logprobs(h, w, target=None, top=0, seq_tile=4096, workspace=None, stream=None):
+    """logp, entropy, lse (float32 [S]), top_logp (float32 [S, top]), top_index (int64 [S, top]) of the
+    readout h [S, Dm] @ w[V, Dm]^T (bf16): the log probability of target [S] (int64, negative: 0;
+    None: logp is None), the entropy, the log of the sum of the exponentials, and the `top` most
+    likely tokens with theirs (None, None for top = 0), seq_tile tokens at a time. h may be a pinned
+    host tensor (staged tile by tile). The gradient of sum g * logp: ce_loss_backward with
+    dloss = -g and this lse."""
+    torch = _torch or _lazy_torch()
+    f32, i64 = torch.float32, torch.int64
+    if len(_matrix(h, "h", torch.bfloat16)) != 2 or len(_matrix(w, "w", torch.bfloat16)) != 2 or \
+            h.shape[1] != w.shape[1]:
+        raise ValueError(f"h and w must be [S, Dm] and [V, Dm], not {tuple(h.shape)} and "
+                         f"{tuple(w.shape)}")
+    S, Dm = h.shape
+    V = w.shape[0]
+    logp = None
+    if target is not None:
+        _dense(target, i64, (S,), "target")
+        logp = _empty(stream, w, (S,), f32)
+    entropy, lse = _empty(stream, w, (S,), f32), _empty(stream, w, (S,), f32)
+    top_logp = top_index = None
+    if top:
+        top_logp = _empty(stream, w, (S, top), f32)
+        top_index = _empty(stream, w, (S, top), i64)
+    if workspace is None:
+        need = upipe_logp_workspace_bytes(S, Dm, V, top, seq_tile, 0 if h.is_cuda else UPIPE_HOST_ACT)
+        workspace = _empty(stream, w, (need,), torch.uint8)
+    st = _lib.upipe_logp_fwd(h.data_ptr(), w.data_ptr(), _ptr(target), _ptr(logp),
+                             entropy.data_ptr(), lse.data_ptr(), _ptr(top_logp), _ptr(top_index), S,
+                             Dm, V, top, seq_tile, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(stream, w))
+    if st:
+        raise UpipeError(st, "upipe_logp_fwd")
+    return logp, entropy, lse, top_logp, top_index
 
 
 # ---- token embedding ------------------------------------------------------------------------

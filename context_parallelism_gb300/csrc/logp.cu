@@ -1,0 +1,561 @@
+// Token log probabilities out of the readout x = h w^T, with the entropy and the largest alternatives.
+//
+//   lse = M + ln z,  z = sum exp(x_j - M),  M = max x;   logp = (x_t - M) - ln z;
+//   H = ln z - sum exp(x_j - M) (x_j - M) / z.
+//
+// The logits are made in groups of columns (256 in the tensor-core GEMM of longer calls, up to 128 in
+// the kernel for short ones below). Each group leaves, per row, its maximum, how often that occurs,
+// and the sums of e = exp(x - max) and e (x - max) over the other columns. A probability near one
+// leaves its mark in ln z alone, as z - 1; with the maximum's own ones counted apart that difference
+// is a sum of small terms and keeps all its digits (ln z = ln count + ln(1 + rest / count)).
+//
+// Alternatives. The k largest logits lie in the k groups with the largest maxima (equal ones by index:
+// an element outside has k elements before it). So the logits are stored, and a row reads k groups of
+// them. Which of two logits is the larger is decided on sums that do not depend on how a kernel
+// accumulates: the kMargin candidates behind the k-th are kept too, and all are summed again as a float
+// and its error (every product of two bf16 is exact in fp32), then ordered by that, ties by index.
+//
+// Short calls (up to 64 rows) are bound by HBM: every row of w is read once. 128 rows of w are the M of
+// an MMA, the few rows of h its N. Blocks own equal runs of rows of w (multiples of 16: with whole
+// tiles of 128 the last of seven rounds over 152 SMs would be six tenths full). The tensor cores'
+// fp32 sums are truncated, not rounded (4096 products that add up to 20 come out 8e-5 low); an
+// accumulator takes 256 products here, and these sums are added up in registers, rounded to nearest.
+#include <cfloat>
+
+#include "internal.h"
+#include "rope.cuh"
+
+namespace upipe {
+namespace {
+
+constexpr int kClass = 18;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ---- groups' sums -----------------------------------------------------------------------------
+
+// Maximum, sum of e over the others, sum of e (x - max), how often the maximum occurs.
+using Sums = float4;
+
+__device__ __forceinline__ Sums no_sums() { return make_float4(-INFINITY, 0.f, 0.f, 0.f); }
+
+// s brought to the maximum m >= s.x, its own maximum among the others where m is larger.
+__device__ __forceinline__ Sums rebase(const Sums& s, float m) {
+  if (s.x == m) return s;
+  if (s.x == -INFINITY) return make_float4(m, s.y, 0.f, 0.f);  // nothing, or NaN
+  const float d = s.x - m, f = exp2f(d * kLog2e), n = s.y + s.w;
+  return make_float4(m, f * n, f * fmaf(d, n, s.z), 0.f);
+}
+
+// ---- short calls ------------------------------------------------------------------------------
+
+constexpr int kShortThreads = 192;
+constexpr int kChunk = 4;  // stages of 64 products that one accumulator takes
+constexpr int kAccs = 4;
+
+template <int N>
+struct ShortLayout {
+  static constexpr int kA = 128 * 128, kB = N * 128, kStage = kA + kB;
+  static constexpr int kStages = (220 * 1024) / kStage;
+  static constexpr int kBar = kStages * kStage;
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccs + 1;
+  static constexpr int kComb = kBar + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kSlot = kComb + 4 * N * 16;
+  static constexpr int kBytes = kSlot + 16 + 1024;
+};
+
+template <int N>
+__device__ __forceinline__ void add_columns(uint32_t taddr, float (&acc)[N]) {
+  if constexpr (N == 16) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int n = 0; n < 16; ++n) acc[n] += __uint_as_float(r[n]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) {
+      uint32_t r[32];
+      tmem_ld32_sync(taddr + c, r);
+#pragma unroll
+      for (int n = 0; n < 32; ++n) acc[c + n] += __uint_as_float(r[n]);
+    }
+  }
+}
+
+// tm_w: boxes of 128 rows, tm_w16: of 16, tm_h: of N (rows behind the last are zeros).
+template <int N>
+__global__ void __launch_bounds__(kShortThreads, 1)
+    logp_short_kernel(const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_w16,
+                      const __grid_constant__ CUtensorMap tm_h, const LogpArgs a) {
+  using L = ShortLayout<N>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* acc_empty = acc_full + kAccs;
+  uint64_t* drain = acc_empty + kAccs;
+  Sums* comb = reinterpret_cast<Sums*>(smem + L::kComb);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
+  constexpr uint32_t kCols = kAccs * N;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t v_lo = static_cast<int64_t>(blockIdx.x) * a.run;
+  const int rows = static_cast<int>(a.V - v_lo < a.run ? a.V - v_lo : a.run);
+  const int tiles = (rows + 127) / 128;
+  const int nk = (a.Dm + 63) / 64;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  launch_dependents();
+
+  auto wait = [&](uint64_t* br, uint32_t parity) -> bool {
+    if (mbar_try_wait(br, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+      if (mbar_try_wait(br, parity)) return true;
+      if ((n & 31) == 0) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicOr(a.err, kErrWaitTimeout | 0x8000u);
+          return false;
+        }
+      }
+    }
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int64_t fills = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < tiles; ++t) {
+        const int left = rows - 128 * t, y0 = static_cast<int>(v_lo) + 128 * t;
+        // rows behind the run's last keep what the stage held: their results are not used
+        const int boxes = left >= 128 ? 0 : (left + 15) / 16;
+        const uint32_t bytes = (boxes ? boxes * 2048u : 16384u) + L::kB;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wait(empty + s, ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * L::kStage;
+          mbar_arrive_expect_tx(full + s, bytes);
+          tma_load_3d(sa + L::kA, &tm_h, kb * 64, 0, 0, full + s);
+          if (!boxes) {
+            tma_load_3d(sa, &tm_w, kb * 64, y0, 0, full + s);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_3d(sa + i * 2048, &tm_w16, kb * 64, y0 + 16 * i, 0, full + s);
+          }
+          ++fills;
+          if (++s == L::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        // let the loads still in flight land before the block ends
+        const int64_t first = fills > L::kStages ? fills - L::kStages : 0;
+        for (int64_t f = first; f < fills; ++f)
+          mbar_wait(full + (f % L::kStages), static_cast<uint32_t>((f / L::kStages) & 1),
+                    100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, N, false, false);
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t dA0 = kdesc0(s0), dB0 = kdesc0(s0 + L::kA);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 1;
+      bool ok = true;
+      for (int t = 0; ok && t < tiles; ++t) {
+        for (int kb = 0; kb < nk; ++kb) {
+          const bool first = kb % kChunk == 0;
+          if ((first && !wait(acc_empty + buf, acc_ph)) || !wait(full + s, ph)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tD = tmem + static_cast<uint32_t>(buf * N);
+          const uint64_t dA = dA0 + s * (L::kStage >> 4), dB = dB0 + s * (L::kStage >> 4);
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16)
+            umma_f16_ss(tD, dA + kstep(k16), dB + kstep(k16), idesc, !first || k16 > 0 ? 1u : 0u);
+          umma_commit(empty + s);
+          if (++s == L::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (kb % kChunk == kChunk - 1 || kb == nk - 1) {
+            umma_commit(acc_full + buf);
+            if (++buf == kAccs) {
+              buf = 0;
+              acc_ph ^= 1;
+            }
+          }
+        }
+      }
+      if (!ok) {
+        umma_commit(drain);
+        mbar_wait(drain, 0, 100000000ull);
+      }
+    }
+  } else {
+    // ---------------- sums: warps 2..5, a row of w each thread ----------------
+    const int quarter = warp & 3;
+    const int r = 32 * quarter + lane;
+    const int chunks = (nk + kChunk - 1) / kChunk;
+    int buf = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = 0; t < tiles; ++t) {
+      float acc[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[n] = 0.f;
+      for (int c = 0; ok && c < chunks; ++c) {
+        ok = __all_sync(kAll, wait(acc_full + buf, ph));
+        if (!ok) break;
+        tc_fence_after();
+        add_columns<N>(tmem + (static_cast<uint32_t>(32 * quarter) << 16) +
+                           static_cast<uint32_t>(buf * N), acc);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + buf);
+        if (++buf == kAccs) {
+          buf = 0;
+          ph ^= 1;
+        }
+      }
+      const int64_t col = v_lo + 128 * t + r;
+      const bool in = 128 * t + r < rows;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (n >= a.M) break;
+        const float x = in ? acc[n] : -INFINITY;
+        if (in && a.logits) a.logits[n * a.ldl + col] = x;
+        if (in && a.target && a.target[n] == col) a.tlogit[n] = x;
+        float m = x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        const bool top = x == m;
+        const float d = x - m;
+        const float e = top || !in ? 0.f : exp2f(d * kLog2e);  // NaN stays
+        float sum = e, sum1 = e * fmaxf(d, -1000.f);
+        if (!in) sum1 = 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          sum += __shfl_xor_sync(kAll, sum, o);
+          sum1 += __shfl_xor_sync(kAll, sum1, o);
+        }
+        const int count = __popc(__ballot_sync(kAll, top && in));
+        if (lane == 0) comb[quarter * N + n] = make_float4(m, sum, sum1, static_cast<float>(count));
+      }
+      // the four warps' sums as one group (a warp whose wait expired keeps step at these barriers)
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const int n = threadIdx.x - 64;
+      if (n < N && n < a.M) {
+        Sums s[4];
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          s[q] = comb[q * N + n];
+          m = fmaxf(m, s[q].x);
+        }
+        Sums all = make_float4(m, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const Sums u = rebase(s[q], m);
+          all.y += u.y;
+          all.z += u.z;
+          all.w += u.w;
+        }
+        a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] = all;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    // groups that this run does not reach
+    for (int t = tiles; t < a.per_run; ++t)
+      for (int n = threadIdx.x - 64; n < a.M; n += 128)
+        a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] = no_sums();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ---- rows' results ----------------------------------------------------------------------------
+
+constexpr int kPickThreads = 256;
+constexpr int kNone = 0x7fffffff;
+
+__device__ __forceinline__ bool before(float v, int i, float u, int j) {
+  return v > u || (v == u && i < j);
+}
+
+// The `n` best (value, index) so far, one a lane, best first; empty places hold (-inf, kNone).
+struct Best {
+  float v = -INFINITY;
+  int i = kNone;
+  // Offers a lane's own (u, j) of every lane; `ask` says which take part. All lanes call.
+  __device__ __forceinline__ void offer(float u, int j, bool ask, int n) {
+    const int lane = threadIdx.x & 31;
+    float last_v = __shfl_sync(kAll, v, n - 1);
+    int last_i = __shfl_sync(kAll, i, n - 1);
+    uint32_t left = __ballot_sync(kAll, ask && before(u, j, last_v, last_i));
+    while (left) {
+      const int l = __ffs(left) - 1;
+      left &= left - 1;
+      const float cu = __shfl_sync(kAll, u, l);
+      const int cj = __shfl_sync(kAll, j, l);
+      if (!before(cu, cj, last_v, last_i)) continue;
+      const int at = __popc(__ballot_sync(kAll, before(v, i, cu, cj)));
+      const float up_v = __shfl_up_sync(kAll, v, 1);
+      const int up_i = __shfl_up_sync(kAll, i, 1);
+      if (lane > at) {
+        v = up_v;
+        i = up_i;
+      }
+      if (lane == at) {
+        v = cu;
+        i = cj;
+      }
+      last_v = __shfl_sync(kAll, v, n - 1);
+      last_i = __shfl_sync(kAll, i, n - 1);
+    }
+  }
+};
+
+// <h, w> of two rows of Dm bf16 by one warp, with an error near 2^-45 of the terms: each lane keeps its
+// sum and the sum of what each addition lost.
+__device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm) {
+  const int lane = threadIdx.x & 31;
+  float s = 0.f, lost = 0.f;
+  for (int k = lane * 8; k < Dm; k += 256) {
+    float x[8], y[8];
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(h + k), x);
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(w + k)), y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = __fmul_rn(x[i], y[i]);
+      const float t = __fadd_rn(s, p);
+      const float b = __fadd_rn(t, -s);
+      lost = __fadd_rn(lost, __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -b)), __fadd_rn(p, -b)));
+      s = t;
+    }
+  }
+  double d = static_cast<double>(s) + static_cast<double>(lost);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(kAll, d, o);
+  return d;
+}
+
+// One block per row. smem: `keep` groups of `width` logits.
+__global__ void __launch_bounds__(kPickThreads) logp_pick_kernel(const LogpArgs a) {
+  extern __shared__ float picked[];
+  __shared__ float red[kPickThreads / 32][3];
+  __shared__ float row_max, row_ln;
+  __shared__ int grp[32], cand[32];
+  __shared__ float cand_x[32];
+  __shared__ double cand_y[32];
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  const Sums* part = a.part + row * a.groups;
+
+  float m = -INFINITY;
+  for (int g = threadIdx.x; g < a.groups; g += kPickThreads) m = fmaxf(m, part[g].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  if (lane == 0) red[warp][0] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPickThreads / 32; ++k) m = fmaxf(m, red[k][0]);
+  __syncthreads();
+  float rest = 0.f, sum1 = 0.f, count = 0.f;
+  for (int g = threadIdx.x; g < a.groups; g += kPickThreads) {
+    const Sums u = rebase(part[g], m);
+    rest += u.y;
+    sum1 += u.z;
+    count += u.w;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    rest += __shfl_xor_sync(kAll, rest, o);
+    sum1 += __shfl_xor_sync(kAll, sum1, o);
+    count += __shfl_xor_sync(kAll, count, o);
+  }
+  if (lane == 0) {
+    red[warp][0] = rest;
+    red[warp][1] = sum1;
+    red[warp][2] = count;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    rest = sum1 = count = 0.f;
+    for (int k = 0; k < kPickThreads / 32; ++k) {
+      rest += red[k][0];
+      sum1 += red[k][1];
+      count += red[k][2];
+    }
+    // a row with a logit of NaN or +inf, or without a finite one, has no probabilities
+    float ln = logf(count) + log1pf(rest / count);
+    if (!(fabsf(m) <= FLT_MAX)) ln = __int_as_float(0x7fc00000);
+    if (a.lse) a.lse[row] = m + ln;
+    if (a.entropy) a.entropy[row] = ln - sum1 / (count + rest);
+    if (a.logp) {
+      const int64_t t = a.target[row];
+      a.logp[row] = t < 0 ? 0.f : t < a.V ? (a.tlogit[row] - m) - ln : __int_as_float(0x7fc00000);
+    }
+    row_max = m;
+    row_ln = ln;
+  }
+  if (!a.top) return;
+  __syncthreads();
+  m = row_max;
+  const float ln = row_ln;
+  float* out_v = a.top_logp + row * a.top;
+  int64_t* out_i = a.top_index + row * a.top;
+  if (!(fabsf(ln) <= FLT_MAX)) {
+    for (int k = threadIdx.x; k < a.top; k += kPickThreads) {
+      out_v[k] = __int_as_float(0x7fc00000);
+      out_i[k] = -1;
+    }
+    return;
+  }
+
+  const int keep = a.keep;
+  if (warp == 0) {
+    Best b;
+    for (int g0 = 0; g0 < a.groups; g0 += 32) {
+      const int g = g0 + lane;
+      const bool in = g < a.groups;
+      const float x = in ? part[g].x : 0.f;
+      // a group of a run that ends before it has no column
+      b.offer(x, g, in && group_start(a, g) < a.V && group_width(a, g) > 0, keep);
+    }
+    grp[lane] = lane < keep ? b.i : kNone;
+  }
+  __syncthreads();
+  const float* x = a.logits + row * a.ldl;
+  for (int k = warp; k < keep; k += kPickThreads / 32) {
+    const int g = grp[k];
+    if (g == kNone) continue;
+    const int64_t c0 = group_start(a, g);
+    const int n = group_width(a, g);
+    for (int c = lane; c < n; c += 32) picked[k * a.width + c] = x[c0 + c];
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Best b;
+    for (int k = 0; k < keep; ++k) {
+      const int g = grp[k];
+      if (g == kNone) break;
+      const int c0 = static_cast<int>(group_start(a, g)), n = group_width(a, g);
+      for (int c = 0; c < n; c += 32)
+        b.offer(c + lane < n ? picked[k * a.width + c + lane] : 0.f, c0 + c + lane, c + lane < n, keep);
+    }
+    cand[lane] = lane < keep ? b.i : kNone;
+    cand_x[lane] = b.v;
+  }
+  __syncthreads();
+  for (int k = warp; k < keep; k += kPickThreads / 32) {
+    if (cand[k] == kNone) continue;
+    const double y = dot_again(a.h + row * a.Dm, a.w + static_cast<int64_t>(cand[k]) * a.Dm, a.Dm);
+    // where infinities or an overflow leave no sum, the order is that of the logits
+    if (lane == 0) cand_y[k] = fabs(y) <= DBL_MAX ? y : static_cast<double>(cand_x[k]);
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int me = lane < keep ? cand[lane] : kNone;
+  const int found = __popc(__ballot_sync(kAll, me != kNone));
+  if (lane >= found && lane < a.top) {  // fewer columns than asked for
+    out_v[lane] = -INFINITY;
+    out_i[lane] = -1;
+  }
+  if (me == kNone) return;
+  int rank = 0;
+  for (int k = 0; k < found; ++k)
+    if (cand_y[k] > cand_y[lane] || (cand_y[k] == cand_y[lane] && cand[k] < me)) ++rank;
+  if (rank < a.top) {
+    out_v[rank] = (cand_x[lane] - m) - ln;
+    out_i[rank] = me;
+  }
+}
+
+template <int N>
+cudaError_t launch_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
+                         const LogpArgs& a, cudaStream_t stream) {
+  using L = ShortLayout<N>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_short_kernel<N>), L::kBytes);
+  if (e != cudaSuccess) return e;
+  launch_begin(kClass, stream);
+  logp_short_kernel<N><<<static_cast<unsigned>((a.V + a.run - 1) / a.run), kShortThreads, L::kBytes,
+                         stream>>>(tw, tw16, th, a);
+  e = cudaGetLastError();
+  launch_end(kClass, stream);
+  return e;
+}
+
+}  // namespace
+
+int logp_short_box(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
+                              const LogpArgs& a, cudaStream_t stream) {
+  const int n = logp_short_box(a.M);
+  return n == 16 ? launch_short<16>(tw, tw16, th, a, stream)
+       : n == 32 ? launch_short<32>(tw, tw16, th, a, stream)
+                 : launch_short<64>(tw, tw16, th, a, stream);
+}
+
+cudaError_t launch_logp_pick(const LogpArgs& a, cudaStream_t stream) {
+  launch_begin(kClass, stream);
+  const cudaError_t e =
+      launch_after(logp_pick_kernel, dim3(static_cast<unsigned>(a.M)), dim3(kPickThreads),
+                   a.top ? static_cast<size_t>(a.keep) * a.width * 4 : 0, stream, true, a);
+  launch_end(kClass, stream);
+  return e;
+}
+
+}  // namespace upipe

@@ -1,6 +1,6 @@
-// C ABI of the sequence-tiled per-token computations - the readout + cross-entropy loss and the
-// gated (SwiGLU) MLP: validation, workspace plans, host staging and the per-tile launch
-// sequences.
+// C ABI of the per-token computations - the sequence-tiled readout + cross-entropy loss, gated
+// (SwiGLU) MLP and token log probabilities, and the token embedding: validation, workspace plans,
+// host staging and the per-tile launch sequences.
 //
 // Sequence tiling chunks the per-token computations along the sequence so that no buffer has
 // the whole sequence along one dimension ("Road to 5 million sequence length" talk notes,
@@ -10,6 +10,8 @@
 //                  256-column vocabulary tile, the target's logit), then one merge launch;
 //   loss backward: logits GEMM again with the CE_BWD epilogue -> dlogits (bf16, seq_tile x V,
 //                  the only large buffer), dh_tile = dlogits w, dw += dlogits^T h_tile;
+//   log probabilities: logits GEMM with the LOGP epilogue (short tiles: logp.cu's own kernel), then
+//                  one launch that joins a row's groups and picks its alternatives;
 //   MLP forward:   gate/up GEMM with the SWIGLU epilogue -> a (bf16, seq_tile x F), y = a Wd^T;
 //   MLP backward:  the gate/up GEMM again (a, and g | u), da = dy Wd with the DSWIGLU epilogue
 //                  -> dg | du, dWd += dy^T a, dWgu += (dg | du)^T x, dx = (dg | du) [Wg; Wu].
@@ -921,6 +923,178 @@ int upipe_embed_bwd(const int64_t* token, const void* dh, float* dw, int64_t S, 
   a.add = add;
   LOSS_CUDA(launch_embed_bwd(a, p, static_cast<uint8_t*>(workspace), stream));
   return UPIPE_OK;
+}
+
+}  // extern "C"
+
+// ---- token log probabilities -----------------------------------------------------------------
+
+namespace upipe {
+namespace {
+
+struct LogpPlan {
+  int64_t T = 0;             // tokens per tile
+  int64_t ldl = 0;           // row pitch of the stored logits
+  int keep = 0;              // candidates of a row
+  int run = 0, per_run = 0, short_groups = 0;  // of tiles of up to kLogpShortRows rows
+  int groups = 0;            // of longer ones: 256-column tiles
+  size_t part = 0, tl = 0, logits = 0, h[2] = {0, 0}, total = 0;
+};
+
+int check_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile) {
+  if (S < 0 || Dm < 1 || V < 1 || top < 0 || seq_tile < 1)
+    return lfail(UPIPE_ERR_INVALID_ARG, "S=%lld Dm=%d V=%lld top=%d seq_tile=%lld", (long long)S,
+                 Dm, (long long)V, top, (long long)seq_tile);
+  if (Dm % 8 || Dm > (1 << 24) || V > (int64_t(1) << 30) || seq_tile % 128 ||
+      seq_tile > (int64_t(1) << 24) || top > kLogpMaxTop)
+    return lfail(UPIPE_ERR_UNSUPPORTED,
+                 "need Dm %% 8 == 0, Dm <= 2^24, V <= 2^30, seq_tile %% 128 == 0, seq_tile <= 2^24, "
+                 "top <= %d",
+                 kLogpMaxTop);
+  return UPIPE_OK;
+}
+
+LogpPlan plan_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile, bool host_act) {
+  LogpPlan p;
+  p.T = seq_tile < S ? seq_tile : S;
+  p.ldl = (V + 31) / 32 * 32;
+  p.keep = top + kLogpMargin;
+  const int64_t run = (V + kLogpShortBlocks - 1) / kLogpShortBlocks;
+  p.run = static_cast<int>((run + 15) / 16 * 16);
+  p.per_run = (p.run + 127) / 128;
+  p.short_groups = static_cast<int>((V + p.run - 1) / p.run) * p.per_run;
+  p.groups = static_cast<int>((V + 255) / 256);
+  const int64_t few = p.T < kLogpShortRows ? p.T : kLogpShortRows;
+  const size_t parts = static_cast<size_t>(p.T) * p.groups,
+               few_parts = static_cast<size_t>(few) * p.short_groups;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += al(bytes);
+    return at;
+  };
+  p.part = take((parts > few_parts ? parts : few_parts) * 16);
+  p.tl = take(static_cast<size_t>(p.T) * 4);
+  if (top) p.logits = take(static_cast<size_t>(p.T) * p.ldl * 4);
+  if (host_act) plan_slots(&off, p.T, int64_t(Dm) * 2, p.h);
+  p.total = off;
+  return p;
+}
+
+}  // namespace
+}  // namespace upipe
+
+extern "C" {
+
+size_t upipe_logp_workspace_bytes(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile,
+                                  int host_mask) {
+  if (check_logp(S, Dm, V, top, seq_tile) != UPIPE_OK || S == 0) return 0;
+  if (host_mask & ~UPIPE_HOST_ACT) return 0;
+  return plan_logp(S, Dm, V, top, seq_tile, (host_mask & UPIPE_HOST_ACT) != 0).total;
+}
+
+int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* logp,
+                   float* entropy, float* lse, float* top_logp, int64_t* top_index, int64_t S,
+                   int Dm, int64_t V, int top, int64_t seq_tile, void* workspace,
+                   size_t workspace_bytes, void* stream_) {
+  const NvtxRange range("upipe_logp_fwd");
+  set_last_error("");
+  int st = check_logp(S, Dm, V, top, seq_tile);
+  if (st != UPIPE_OK || S == 0) return st;
+  if ((target == nullptr) != (logp == nullptr))
+    return lfail(UPIPE_ERR_INVALID_ARG, "target and logp go together");
+  if ((top_logp != nullptr) != (top > 0) || (top_index != nullptr) != (top > 0))
+    return lfail(UPIPE_ERR_INVALID_ARG, "top_logp and top_index go with top > 0");
+  // h, w and workspace first; then those that are there
+  const void* ptrs[9] = {h, w, workspace};
+  const char* names[9] = {"h", "w", "workspace"};
+  int align[9] = {16, 16, 256};
+  bool may_host[9] = {true};
+  int n = 3;
+  auto add = [&](const void* p, const char* name, int bytes) {
+    if (!p) return;
+    ptrs[n] = p;
+    names[n] = name;
+    align[n++] = bytes;
+  };
+  add(target, "target", 8);
+  add(logp, "logp", 4);
+  add(entropy, "entropy", 4);
+  add(lse, "lse", 4);
+  add(top_logp, "top_logp", 4);
+  add(top_index, "top_index", 8);
+  bool host[9];
+  int dev = -1;
+  st = check_ptrs(ptrs, names, may_host, n, host, &dev, align);
+  if (st != UPIPE_OK) return st;
+  const LogpPlan p = plan_logp(S, Dm, V, top, seq_tile, host[0]);
+  if (workspace_bytes < p.total)
+    return lfail(UPIPE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes,
+                 p.total);
+  const DeviceGuard dguard;
+  LOSS_CUDA(cudaSetDevice(dev));
+  uint32_t* err = nullptr;
+  st = device_status_word(dev, &err);
+  if (st != UPIPE_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int cap = sm_count(dev);
+  const Act in[1] = {make_act(h, int64_t(Dm) * 2, host[0], ws, p.h)};
+  return run_tiles(S, p.T, in, 1, nullptr, 0, dev, stream,
+                   [&](int64_t r0, int64_t Mc, int s) -> int {
+    LogpArgs a{};
+    a.h = reinterpret_cast<const __nv_bfloat16*>(in[0].rows(s, r0));
+    a.w = static_cast<const __nv_bfloat16*>(w);
+    a.target = target ? target + r0 : nullptr;
+    a.tlogit = reinterpret_cast<float*>(ws + p.tl);
+    a.part = reinterpret_cast<float4*>(ws + p.part);
+    a.logits = top ? reinterpret_cast<float*>(ws + p.logits) : nullptr;
+    a.ldl = p.ldl;
+    a.logp = logp ? logp + r0 : nullptr;
+    a.entropy = entropy ? entropy + r0 : nullptr;
+    a.lse = lse ? lse + r0 : nullptr;
+    a.top_logp = top ? top_logp + r0 * top : nullptr;
+    a.top_index = top ? top_index + r0 * top : nullptr;
+    a.M = static_cast<int>(Mc);
+    a.Dm = Dm;
+    a.top = top;
+    a.keep = p.keep;
+    a.V = V;
+    a.err = err;
+    CUtensorMap th, tw, tw16;
+    if (Mc <= kLogpShortRows) {
+      a.run = p.run;
+      a.per_run = p.per_run;
+      a.width = 128;
+      a.groups = p.short_groups;
+      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, logp_short_box(a.M)));
+      LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 128));
+      LOSS_CUDA(make_tmap_bf16(&tw16, w, Dm, V, 1, 16));
+      LOSS_CUDA(launch_logp_short(tw, tw16, th, a, stream));
+    } else {
+      a.run = a.width = 256;
+      a.per_run = 1;
+      a.groups = p.groups;
+      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, 128));
+      LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 256));
+      GemmArgs g{};
+      g.M = a.M;
+      g.N = static_cast<int>(V);
+      g.K = Dm;
+      g.m_fastest = 1;
+      g.group_m = UPIPE_CE_GROUP_M;
+      g.c = a.logits;
+      g.ldc = p.ldl;
+      g.target = a.target;
+      g.part = reinterpret_cast<float*>(a.part);
+      g.part_stride = a.groups;
+      g.tlogit = a.tlogit;
+      g.err = err;
+      LOSS_CUDA(launch_gemm_tc(kEpiLogp, false, false, th, tw, g, cap, stream));
+    }
+    LOSS_CUDA(launch_logp_pick(a, stream));
+    return UPIPE_OK;
+  });
 }
 
 }  // extern "C"

@@ -258,6 +258,38 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
                      float* loss, float* lse, void* dh, float* dw, int64_t S, int Dm, int64_t V,
                      int64_t seq_tile, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Sequence tiling: token log probabilities -----------------------------------------------
+ *
+ * Scoring and sampling out of the same readout, without the logits: for tokens i < S
+ *   x_ij = <h_i, w_j>;  lse_i = ln sum_j exp(x_ij);  logp_i = x_i,target[i] - lse_i (= -loss above;
+ *   0 for a negative target, NaN for one beyond the vocabulary);  entropy_i = -sum_j p_ij ln p_ij,
+ *   p = exp(x - lse);  top_index_i: the `top` largest x_ij, the largest first, equal ones by index;
+ *   top_logp_i: their x - lse.
+ * The gradient of sum g_i logp_i is upipe_ce_bwd's for dloss = -g and this lse.
+ * Which of two logits is the larger is decided on sums of the exact products with an error near
+ * 2^-45 of their magnitudes, whatever the tile; top + 8 candidates are looked at so, those with the
+ * largest tensor-core sums. The values are the tensor cores' (fp32; in calls of up to 64 tokens in
+ * pieces of 256 products, rounded to nearest between them). A row with a logit of NaN or +inf, or
+ * without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
+ * and -1.
+ * Layouts (dense): h [S][Dm], w [V][Dm] bf16; target, top_index [S], [S][top] int64; logp, entropy,
+ * lse [S], top_logp [S][top] float32. target and logp may both be NULL, entropy and lse each;
+ * top_logp and top_index are NULL when top = 0. h and w 16-byte, workspace 256-byte aligned, the
+ * others to their elements. Device memory of one device; h may be PINNED host memory, staged as for
+ * the loss (host_mask = UPIPE_HOST_ACT).
+ * Supported: Dm a multiple of 8, any V up to 2^30, top up to 24, seq_tile a multiple of 128. S = 0
+ * does nothing. Workspace: upipe_logp_workspace_bytes: for T = min(seq_tile, S) tokens 16 bytes for
+ * each token and 256 columns (or, up to 64 tokens, each of the runs' groups of 128), 4 T, and with
+ * top > 0 the tile's logits, 4 T V; each rounded up to 256, plus two slots with UPIPE_HOST_ACT.
+ * Results repeat bitwise for the same sizes.
+ */
+size_t upipe_logp_workspace_bytes(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile,
+                                  int host_mask);
+int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* logp,
+                   float* entropy, float* lse, float* top_logp, int64_t* top_index, int64_t S,
+                   int Dm, int64_t V, int top, int64_t seq_tile, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
 /* ---- Sequence tiling: gated (SwiGLU) MLP ------------------------------------------------
  *
  * The MLP is the other per-token computation the same passages chunk along the sequence.

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include <cstdio>
+#include <type_traits>
 #include <utility>
 
 #include <cuda.h>
@@ -352,13 +353,13 @@ struct NormArgs {
   int64_t tokens;           // backward
   float* part;              // backward: [blocks][2][D] partial sums of dw, or NULL
   // set by the launchers
-  int lanes, log_lanes, groups[3];
+  int lanes, log_lanes, per, groups[3];  // per: heads of a group at most
   float inv_d;
 };
 cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t tokens,
                              cudaStream_t stream);
 // Blocks of the backward (host arithmetic); part holds 2 D floats for each.
-constexpr int kNormBwdBlocks = 608;
+constexpr int kNormBwdBlocks = 608;  // four on each of 152 SMs
 int norm_bwd_blocks(int64_t tokens, int D, int heads_q, int heads_k);
 // dq_w, dk_w: float32 [D], written; either may be NULL.
 cudaError_t launch_norm_rope_bwd(NormArgs a, bool interleaved, float* dq_w, float* dk_w,

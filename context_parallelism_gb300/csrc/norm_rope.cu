@@ -8,9 +8,19 @@
 // Everything between the bf16 input and the one rounding of the output is fp32. r is recomputed in
 // the backward, from an x that it reads anyway: nothing is kept from the forward.
 //
-// Bound: HBM. A thread owns the 16 features of a chunk (two 16-byte vectors, eight pairs) of a few
-// heads of one token, and the 2, 4, 8, 16 or 32 lanes that share a head add up its sums by shuffles.
-// Heads of one tensor form a thread's group, so the weights of its chunk are read once.
+// A thread owns the 16 features of a chunk (two 16-byte vectors, eight pairs) of a few heads of one
+// token, and the 2, 4, 8, 16 or 32 lanes that share a head add up its sums by shuffles. Heads of one
+// tensor form a thread's group; they share the angles and the weights. Whatever the layout, a chunk
+// is held as the first features X of its eight pairs and the second ones Y, two to a register pair
+// for the paired multiply-adds: in the half layout these are its two vectors, in the interleaved one
+// the even and the odd elements of both.
+//
+// Bound: HBM, once enough bytes are in flight: the loads go to the thread's own places in shared
+// memory as asynchronous copies, which hold no registers (131072 tokens of 32 + 8 heads of 128: 568 us
+// with loads to registers, 385 so, 105 % of a copy's rate), and the angles are shared by eight heads.
+// Copies past L1 want whole sectors to a request: with the 32 bytes of four interleaved pairs in one
+// lane, two requests of half sectors, the backward of 8194 tokens took 123 us, now 85. The backward
+// of 32768 tokens takes 170 us, 89 % of a copy's rate; its 330 instructions a lane and head are next.
 #include "internal.h"
 #include "rope.cuh"
 
@@ -18,34 +28,175 @@ namespace upipe {
 namespace {
 
 constexpr int kFwdThreads = 64;
-constexpr int kFwdHeads = 4;  // heads of one token per thread
-constexpr int kBwdThreads = 256;
-constexpr int kBwdHeads = 2;
+constexpr int kFwdShort = 2, kFwdLong = 8;  // heads of one token per thread
+constexpr int kBwdThreads = 128;
+constexpr int kBwdShort = 2, kBwdLong = 8;
+constexpr int kBwdAhead = 2;  // heads whose loads a thread has in flight
 
-// A chunk's effective weights: offset + w, or ones.
-__device__ __forceinline__ void load_weights(const NormArgs& a, int t, int o, float (&w)[8]) {
-  if (!a.w[t]) {
+// Waits until all but the thread's last n groups of asynchronous copies have landed.
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Eight floats as four pairs.
+struct F8 {
+  uint64_t p[4];
+};
+
+// A chunk's vectors as the firsts X and seconds Y of its pairs, and back.
+template <bool kInter>
+__device__ __forceinline__ void unpack_chunk(const uint4& a, const uint4& b, F8& x, F8& y) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    return;
+  for (int i = 0; i < 4; ++i) {
+    if (kInter) {
+      x.p[i] = f2_pack_u(w[2 * i] << 16, w[2 * i + 1] << 16);
+      y.p[i] = f2_pack_u(w[2 * i] & 0xffff0000u, w[2 * i + 1] & 0xffff0000u);
+    } else {
+      x.p[i] = f2_pack_u(w[i] << 16, w[i] & 0xffff0000u);
+      y.p[i] = f2_pack_u(w[4 + i] << 16, w[4 + i] & 0xffff0000u);
+    }
   }
-  if (a.wide) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.w[t]) + o);
-    const float4 u = p[0], v = p[1];
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
-  } else {
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w[t]) + o), w);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] += a.offset;
 }
 
-__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
-  float s = 0.f;
+template <bool kInter>
+__device__ __forceinline__ void pack_chunk(const F8& x, const F8& y, uint4& a, uint4& b) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
-  return s;
+  for (int i = 0; i < 4; ++i) {
+    float x0, x1, y0, y1;
+    f2_unpack(x.p[i], x0, x1);
+    f2_unpack(y.p[i], y0, y1);
+    if (kInter) {
+      w[2 * i] = pack_bf16(x0, y0);
+      w[2 * i + 1] = pack_bf16(x1, y1);
+    } else {
+      w[i] = pack_bf16(x0, x1);
+      w[4 + i] = pack_bf16(y0, y1);
+    }
+  }
+  a = make_uint4(w[0], w[1], w[2], w[3]);
+  b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The two vectors of a head that chunk c holds (D: none). Neighbouring lanes hold neighbouring vectors,
+// whole sectors of a head to a request, in both layouts: 8 c and rot / 2 + 8 c of the rotated part,
+// the first and the second half of the vectors behind it likewise.
+__device__ __forceinline__ bool chunk_vectors(int c, int rot, int D, int* o0, int* o1) {
+  const int nr = rot >> 4, nt = (D - rot + 15) >> 4, k = c - nr;
+  if (k < 0) {
+    *o0 = 8 * c;
+    *o1 = rot / 2 + 8 * c;
+    return true;
+  }
+  *o0 = k < nt ? rot + 8 * k : D;
+  *o1 = k < nt ? rot + 8 * (nt + k) : D;
+  return false;
+}
+
+// Feature of the head that X's (second = 0) or Y's i-th element is.
+template <bool kInter>
+__device__ __forceinline__ int feature(int i, int second, int o0, int o1) {
+  if (kInter) return (i < 4 ? o0 + 2 * i : o1 + 2 * (i - 4)) + second;
+  return (second ? o1 : o0) + i;
+}
+
+// Eight effective weights, offset + w or ones, from feature o on; zeros behind the head.
+__device__ __forceinline__ void load_weights8(const NormArgs& a, int t, int o, float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (o >= a.r.D) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  } else if (a.w[t]) {
+    if (a.wide) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.w[t]) + o);
+      const float4 u = p[0], v = p[1];
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    } else {
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w[t]) + o), w);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] += a.offset;
+  }
+}
+
+// Those of a chunk's X and Y.
+template <bool kInter>
+__device__ __forceinline__ void load_weights(const NormArgs& a, int t, int o0, int o1, F8& x, F8& y) {
+  float u[8], v[8];
+  load_weights8(a, t, o0, u);
+  load_weights8(a, t, o1, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kInter) {
+      const float* w = i < 2 ? u : v;
+      const int k = 4 * (i & 1);
+      x.p[i] = f2_pack(w[k], w[k + 2]);
+      y.p[i] = f2_pack(w[k + 1], w[k + 3]);
+    } else {
+      x.p[i] = f2_pack(u[2 * i], u[2 * i + 1]);
+      y.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t both(float v) { return f2_pack(v, v); }
+
+// Cosines and sines, times their factors, of chunk c's eight pairs at position pos. The fraction of a turn,
+// p * phase modulo 2^64 (see rope.cu), is kept to 32 bits (2^-32 of a turn); its upper bits name the
+// nearest quarter turn, and for the rest, x within pi / 4, the Taylor series up to x^9 and x^10 are
+// off by less than 2^-28. About 20 instructions an angle, well under a general sine and cosine.
+template <bool kInter>
+__device__ __forceinline__ void chunk_turns(const RopeArgs& a, int c, int64_t pos, F8& cs, F8& sn) {
+  const ulonglong2* ph = reinterpret_cast<const ulonglong2*>(a.phase) + (kInter ? 2 : 4) * c;
+  const float m = a.mscale, ms = a.sin_scale;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const ulonglong2 f = ph[kInter && i >= 2 ? a.rot / 8 + i - 2 : i];
+    const uint32_t t0 = static_cast<uint32_t>((static_cast<uint64_t>(pos) * f.x) >> 32);
+    const uint32_t t1 = static_cast<uint32_t>((static_cast<uint64_t>(pos) * f.y) >> 32);
+    const uint32_t q0 = (t0 + 0x20000000u) >> 30, q1 = (t1 + 0x20000000u) >> 30;
+    const float r0 = static_cast<float>(static_cast<int32_t>(t0 - (q0 << 30)));
+    const float r1 = static_cast<float>(static_cast<int32_t>(t1 - (q1 << 30)));
+    const uint64_t x = fmul2(f2_pack(r0, r1), both(6.283185307179586f * 0x1p-32f));
+    const uint64_t z = fmul2(x, x);
+    uint64_t s = ffma2(z, both(1.f / 362880), both(-1.f / 5040));
+    s = ffma2(z, s, both(1.f / 120));
+    s = ffma2(z, s, both(-1.f / 6));
+    s = ffma2(fmul2(z, x), s, x);
+    uint64_t d = ffma2(z, both(-1.f / 3628800), both(1.f / 40320));
+    d = ffma2(z, d, both(-1.f / 720));
+    d = ffma2(z, d, both(1.f / 24));
+    d = ffma2(z, d, both(-0.5f));
+    d = ffma2(z, d, both(1.f));
+    float s0, s1, d0, d1;
+    f2_unpack(s, s0, s1);
+    f2_unpack(d, d0, d1);
+    // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+    const float a0 = q0 & 1 ? s0 : d0, b0 = q0 & 1 ? d0 : s0;
+    const float a1 = q1 & 1 ? s1 : d1, b1 = q1 & 1 ? d1 : s1;
+    const uint32_t n0 = ((q0 + 1) << 30) & 0x80000000u, n1 = ((q1 + 1) << 30) & 0x80000000u;
+    const uint32_t k0 = (q0 << 30) & 0x80000000u, k1 = (q1 << 30) & 0x80000000u;
+    cs.p[i] = fmul2(f2_pack_u(__float_as_uint(a0) ^ n0, __float_as_uint(a1) ^ n1), both(m));
+    sn.p[i] = fmul2(f2_pack_u(__float_as_uint(b0) ^ k0, __float_as_uint(b1) ^ k1), both(ms));
+  }
+}
+
+// <x, u> + <y, v>
+__device__ __forceinline__ float dot_pairs(const F8& x, const F8& u, const F8& y, const F8& v) {
+  uint64_t s = fmul2(x.p[0], u.p[0]), t = fmul2(y.p[0], v.p[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    s = ffma2(x.p[i], u.p[i], s);
+    t = ffma2(y.p[i], v.p[i], t);
+  }
+  float lo, hi;
+  f2_unpack(fadd2(s, t), lo, hi);
+  return lo + hi;
 }
 
 // Sum over the lanes that share a head.
@@ -56,26 +207,37 @@ __device__ __forceinline__ float head_sum(float s, int lanes) {
 
 // (ss / D + eps)^(-1/2) of a head whose squares sum to ss; heads whose squares leave fp32's range
 // (elements of 2^59 and more) are summed again, scaled down by 2^96. All lanes of a warp call.
-__device__ __forceinline__ float inverse_rms(const NormArgs& a, float ss, const float (&x)[8],
-                                             const float (&y)[8]) {
+__device__ __forceinline__ float inverse_rms(const NormArgs& a, float ss, const F8& x, const F8& y) {
   float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
   const bool out = !(ss <= 0x1p127f);
   if (__any_sync(0xffffffffu, out)) {
-    float s = 0.f;
+    F8 u, v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = x[i] * 0x1p-96f, v = y[i] * 0x1p-96f;
-      s += u * u + v * v;
+    for (int i = 0; i < 4; ++i) {
+      u.p[i] = fmul2(x.p[i], both(0x1p-96f));
+      v.p[i] = fmul2(y.p[i], both(0x1p-96f));
     }
-    s = head_sum(s, a.lanes);
+    const float s = head_sum(dot_pairs(u, u, v, v), a.lanes);
     if (out) r = 0x1p-96f * rsqrtf(s * a.inv_d);
   }
   return r;
 }
 
-// Thread -> (token, head group, lane of a head), lane fastest; groups number q's, k's, v's heads.
-template <bool kInter, bool kAppend>
-__global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const NormArgs a) {
+// f(0), .. f(n - 1) with the number a constant.
+template <int n, int j = 0, typename F>
+__device__ __forceinline__ void unrolled(F& f) {
+  if constexpr (j < n) {
+    f(std::integral_constant<int, j>());
+    unrolled<n, j + 1>(f);
+  }
+}
+
+// Thread -> (token, head group, lane of a head), lane fastest; groups number q's, k's, v's heads. A
+// group's kPer heads share the angles and the weights, folded into one map of the chunk; all their
+// loads are started before anything else.
+template <bool kInter, bool kAppend, int kPer>
+__global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_kernel(const NormArgs a) {
+  __shared__ uint4 stage[2 * kPer][kFwdThreads];
   const RopeArgs& ra = a.r;
   const uint32_t idx = blockIdx.x * static_cast<uint32_t>(kFwdThreads) + threadIdx.x;
   const uint32_t item = idx >> a.log_lanes;
@@ -90,63 +252,90 @@ __global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const NormArgs a
   int t = 0;
   while (t < 2 && g >= a.groups[t]) g -= a.groups[t++];
   int o0, o1;
-  const bool turns = chunk_features(c, ra.rot, kInter, &o0, &o1);
-  const bool in0 = o0 < ra.D, two = o1 < ra.D;
+  const bool turns = chunk_vectors(c, ra.rot, ra.D, &o0, &o1);
+  const bool two = o1 < ra.D;
+  const bool cached = kAppend && t > 0, normed = t < 2;
+  live = live && o0 < ra.D && !(cached && at.slot < 0);
+  const int step = a.groups[t];
+  const int mine = live ? (ra.heads[t] - g + step - 1) / step : 0;  // heads of this thread
 
-  uint4 va[kFwdHeads], vb[kFwdHeads];
-  __nv_bfloat16* out[kFwdHeads];
+  {
+    const uint32_t to = smem_u32(&stage[0][threadIdx.x]);
+    constexpr uint32_t kRow = kFwdThreads * 16;
+    const __nv_bfloat16* src = ra.src[t] + at.b * ra.src_b[t] + at.i * ra.src_s[t] + g * ra.src_h[t];
+    const int64_t src_step = step * ra.src_h[t];
 #pragma unroll
-  for (int j = 0; j < kFwdHeads; ++j) {
-    const int h = g + j * a.groups[t];
-    out[j] = nullptr;
-    va[j] = vb[j] = make_uint4(0, 0, 0, 0);
-    if (!live || !in0 || h >= ra.heads[t]) continue;
-    if (kAppend && t > 0) {
-      if (at.slot < 0) continue;
-      out[j] = ra.dst[t] + at.slot + h * ra.head_stride;
-    } else {
-      out[j] = ra.dst[t] + at.b * ra.dst_b[t] + at.i * ra.dst_s[t] + h * ra.dst_h[t];
-    }
-    const __nv_bfloat16* src = ra.src[t] + at.b * ra.src_b[t] + at.i * ra.src_s[t] + h * ra.src_h[t];
-    va[j] = *reinterpret_cast<const uint4*>(src + o0);
-    if (two) vb[j] = *reinterpret_cast<const uint4*>(src + o1);
-  }
-  float cs[8], sn[8], wa[8], wb[8];
-  const bool normed = t < 2;
-  if (live && in0 && normed) {
-    if (turns) chunk_angles(ra.phase, c, at.pos, ra.mscale, ra.sin_scale, cs, sn);
-    load_weights(a, t, o0, wa);
-    if (two) load_weights(a, t, o1, wb);
-  }
-#pragma unroll
-  for (int j = 0; j < kFwdHeads; ++j) {
-    float x[8], y[8];
-    unpack_bf16x8(va[j], x);
-    unpack_bf16x8(vb[j], y);
-    const float ss = head_sum(dot8(x, x) + dot8(y, y), a.lanes);
-    const float r = inverse_rms(a, normed ? ss : 0.f, x, y);
-    if (!out[j]) continue;
-    if (normed) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = x[i] * r * wa[i];
-        y[i] = y[i] * r * wb[i];
+    for (int j = 0; j < kPer; ++j, src += src_step) {
+      if (j < mine) {
+        cp_async16(to + 2 * j * kRow, src + o0);
+        if (two) cp_async16(to + (2 * j + 1) * kRow, src + o1);
       }
-      if (turns) rotate_pairs<kInter>(x, y, cs, sn);
-      va[j] = pack_bf16x8(x);
-      vb[j] = pack_bf16x8(y);
+      cp_async_commit();
     }
-    *reinterpret_cast<uint4*>(out[j] + o0) = va[j];
-    if (two) *reinterpret_cast<uint4*>(out[j] + o1) = vb[j];
   }
+  // X' = X ax + Y bx, Y' = Y ay + X by
+  F8 ax{}, ay{}, bx{}, by{};
+  if (live && normed) {
+    load_weights<kInter>(a, t, o0, o1, ax, ay);
+    if (turns) {
+      F8 cs, sn;
+      chunk_turns<kInter>(ra, c, at.pos, cs, sn);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bx.p[i] = fmul2(fmul2(sn.p[i], ay.p[i]), both(-1.f));
+        by.p[i] = fmul2(sn.p[i], ax.p[i]);
+        ax.p[i] = fmul2(cs.p[i], ax.p[i]);
+        ay.p[i] = fmul2(cs.p[i], ay.p[i]);
+      }
+    }
+  }
+  const int64_t dst_h = cached ? ra.head_stride : ra.dst_h[t];
+  __nv_bfloat16* dst = ra.dst[t] + (cached ? at.slot : at.b * ra.dst_b[t] + at.i * ra.dst_s[t]) +
+                       g * dst_h;
+  auto head = [&](auto J) {
+    constexpr int j = decltype(J)::value;
+    cp_async_wait<kPer - 1 - j>();
+    const bool here = j < mine;
+    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
+    if (here) {
+      va = stage[2 * j][threadIdx.x];
+      if (two) vb = stage[2 * j + 1][threadIdx.x];
+    }
+    F8 x, y;
+    unpack_chunk<kInter>(va, vb, x, y);
+    const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
+    const float r = inverse_rms(a, normed ? ss : 0.f, x, y);
+    if (here) {
+      if (normed) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // r first: a head's features may leave fp32's range times the weights, its normed ones not
+          const uint64_t u = fmul2(x.p[i], both(r)), v = fmul2(y.p[i], both(r));
+          x.p[i] = fmul2(u, ax.p[i]);
+          y.p[i] = fmul2(v, ay.p[i]);
+          if (turns) {
+            x.p[i] = ffma2(v, bx.p[i], x.p[i]);
+            y.p[i] = ffma2(u, by.p[i], y.p[i]);
+          }
+        }
+        pack_chunk<kInter>(x, y, va, vb);
+      }
+      *reinterpret_cast<uint4*>(dst + o0) = va;
+      if (two) *reinterpret_cast<uint4*>(dst + o1) = vb;
+    }
+    dst += step * dst_h;
+  };
+  unrolled<kPer>(head);
 }
 
 // A set of `lanes` lanes keeps one head group and walks the tokens, so that its 16 sums of dw and its
 // weights stay in registers; a block adds its sets' sums in order and leaves 2 D partial sums.
-template <bool kInter>
-__global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const NormArgs a) {
+template <bool kInter, int kPer>
+__global__ void __launch_bounds__(kBwdThreads, 4) norm_rope_bwd_kernel(const NormArgs a) {
+  static_assert(kPer % kBwdAhead == 0, "a head's slot is a constant");
   const RopeArgs& ra = a.r;
-  __shared__ float part[kBwdThreads * 16];
+  // [slot][x: two vectors, dy: two][thread]; at the end the partial sums
+  __shared__ uint4 ring[kBwdAhead * 4][kBwdThreads];
   const int sets = kBwdThreads >> a.log_lanes;
   const int set_in = static_cast<int>(threadIdx.x) >> a.log_lanes;
   const int c = static_cast<int>(threadIdx.x) & (a.lanes - 1);
@@ -160,80 +349,126 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
     t = 1;
   }
   int o0, o1;
-  const bool turns = chunk_features(c, ra.rot, kInter, &o0, &o1);
+  const bool turns = chunk_vectors(c, ra.rot, ra.D, &o0, &o1);
   const bool in0 = o0 < ra.D, two = o1 < ra.D;
-  float wa[8], wb[8], da[8], db[8];
+  const int step = a.groups[t];
+  const int own = walker < walkers && in0 ? (ra.heads[t] - g + step - 1) / step : 0;
+  F8 wx, wy, dwx{}, dwy{};
+  load_weights<kInter>(a, t, o0, o1, wx, wy);
+
+  const uint32_t to = smem_u32(&ring[0][threadIdx.x]);
+  constexpr uint32_t kRow = kBwdThreads * 16;
+  // the token that loads are started for, one ahead of the other in time
+  struct Token {
+    __nv_bfloat16* dx;
+    int64_t pos;
+    int heads;
+  };
+  const __nv_bfloat16 *px = nullptr, *pg = nullptr;
+  auto enter = [&](int64_t token) {
+    Token w{nullptr, 0, 0};
+    if (own && token < a.tokens) {
+      const int64_t b = ra.B == 1 ? 0 : div_fl(token, ra.S), i = token - b * ra.S;
+      px = a.x[t] + b * a.x_b[t] + i * a.x_s[t] + g * a.x_h[t];
+      pg = ra.src[t] + b * ra.src_b[t] + i * ra.src_s[t] + g * ra.src_h[t];
+      w.dx = ra.dst[t] + b * ra.dst_b[t] + i * ra.dst_s[t] + g * ra.dst_h[t];
+      w.pos = ra.pos ? ra.pos[token] : ra.pos0 + i;
+      w.heads = own;
+    }
+    return w;
+  };
+  auto start = [&](bool is, int slot) {
+    if (is) {
+      cp_async16(to + slot * 4 * kRow, px + o0);
+      cp_async16(to + (slot * 4 + 2) * kRow, pg + o0);
+      if (two) {
+        cp_async16(to + (slot * 4 + 1) * kRow, px + o1);
+        cp_async16(to + (slot * 4 + 3) * kRow, pg + o1);
+      }
+    }
+    cp_async_commit();
+    px += step * a.x_h[t];
+    pg += step * ra.src_h[t];
+  };
+
+  Token w = enter(walker);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) wa[i] = wb[i] = da[i] = db[i] = 0.f;
-  if (in0) load_weights(a, t, o0, wa);
-  if (two) load_weights(a, t, o1, wb);
+  for (int j = 0; j < kBwdAhead; ++j) start(j < w.heads, j);
 
   // every lane of a warp takes the same number of steps: the shuffles want them all
-  const int64_t steps = (a.tokens + walkers - 1) / walkers;
-  for (int64_t n = 0; n < steps; ++n) {
-    const int64_t tok = n * walkers + walker;
-    const bool live = walker < walkers && tok < a.tokens && in0;
-    TokenPlace at{};
-    if (live) place_token<false>(ra, tok, false, &at);
-    uint4 xa[kBwdHeads], xb[kBwdHeads], ga[kBwdHeads], gb[kBwdHeads];
-#pragma unroll
-    for (int j = 0; j < kBwdHeads; ++j) {
-      const int h = g + j * a.groups[t];
-      xa[j] = xb[j] = ga[j] = gb[j] = make_uint4(0, 0, 0, 0);
-      if (!live || h >= ra.heads[t]) continue;
-      const __nv_bfloat16* x = a.x[t] + at.b * a.x_b[t] + at.i * a.x_s[t] + h * a.x_h[t];
-      const __nv_bfloat16* dy = ra.src[t] + at.b * ra.src_b[t] + at.i * ra.src_s[t] + h * ra.src_h[t];
-      xa[j] = *reinterpret_cast<const uint4*>(x + o0);
-      ga[j] = *reinterpret_cast<const uint4*>(dy + o0);
-      if (two) {
-        xb[j] = *reinterpret_cast<const uint4*>(x + o1);
-        gb[j] = *reinterpret_cast<const uint4*>(dy + o1);
+  const int64_t tokens = (a.tokens + walkers - 1) / walkers;
+  for (int64_t n = 0; n < tokens; ++n) {
+    F8 cs{}, sn{};
+    if (w.heads && turns) chunk_turns<kInter>(ra, c, w.pos, cs, sn);
+    Token next{nullptr, 0, 0};
+    auto head = [&](auto J) {
+      constexpr int j = decltype(J)::value, slot = j % kBwdAhead, then = j + kBwdAhead;
+      const bool here = j < w.heads;
+      cp_async_wait<kBwdAhead - 1>();
+      uint4 xa = make_uint4(0, 0, 0, 0), xb = xa, ga = xa, gb = xa;
+      if (here) {
+        xa = ring[slot * 4][threadIdx.x];
+        ga = ring[slot * 4 + 2][threadIdx.x];
+        if (two) {
+          xb = ring[slot * 4 + 1][threadIdx.x];
+          gb = ring[slot * 4 + 3][threadIdx.x];
+        }
       }
-    }
-    float cs[8], sn[8];
-    if (live && turns) chunk_angles(ra.phase, c, at.pos, ra.mscale, ra.sin_scale, cs, sn);
-#pragma unroll
-    for (int j = 0; j < kBwdHeads; ++j) {
-      const int h = g + j * a.groups[t];
-      float x[8], y[8], u[8], v[8];
-      unpack_bf16x8(xa[j], x);
-      unpack_bf16x8(xb[j], y);
-      unpack_bf16x8(ga[j], u);
-      unpack_bf16x8(gb[j], v);
-      if (live && turns) rotate_pairs<kInter>(u, v, cs, sn);
-      const float ss = head_sum(dot8(x, x) + dot8(y, y), a.lanes);
+      F8 x, y, u, v;
+      unpack_chunk<kInter>(xa, xb, x, y);
+      unpack_chunk<kInter>(ga, gb, u, v);
+      if (then == kPer) next = enter((n + 1) * walkers + walker);
+      start(then < kPer ? then < w.heads : then - kPer < next.heads, slot);
+      const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
       const float r = inverse_rms(a, ss, x, y);
-      float tx = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= r;
-        y[i] *= r;
-        da[i] = fmaf(u[i], x[i], da[i]);
-        db[i] = fmaf(v[i], y[i], db[i]);
-        u[i] *= wa[i];
-        v[i] *= wb[i];
-        tx = fmaf(u[i], x[i], fmaf(v[i], y[i], tx));
+      for (int i = 0; i < 4; ++i) {
+        if (turns) {
+          const uint64_t p = u.p[i], q = v.p[i];
+          u.p[i] = ffma2(p, cs.p[i], fmul2(fmul2(q, both(-1.f)), sn.p[i]));
+          v.p[i] = ffma2(q, cs.p[i], fmul2(p, sn.p[i]));
+        }
+        x.p[i] = fmul2(x.p[i], both(r));
+        y.p[i] = fmul2(y.p[i], both(r));
+        dwx.p[i] = ffma2(u.p[i], x.p[i], dwx.p[i]);
+        dwy.p[i] = ffma2(v.p[i], y.p[i], dwy.p[i]);
+        u.p[i] = fmul2(u.p[i], wx.p[i]);
+        v.p[i] = fmul2(v.p[i], wy.p[i]);
       }
-      tx = head_sum(tx, a.lanes) * a.inv_d;
-      if (!live || h >= ra.heads[t]) continue;
-      __nv_bfloat16* dx = ra.dst[t] + at.b * ra.dst_b[t] + at.i * ra.dst_s[t] + h * ra.dst_h[t];
+      const float tx = head_sum(dot_pairs(u, x, v, y), a.lanes) * -a.inv_d;
+      if (here) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        u[i] = r * fmaf(-x[i], tx, u[i]);
-        v[i] = r * fmaf(-y[i], tx, v[i]);
+        for (int i = 0; i < 4; ++i) {
+          u.p[i] = fmul2(both(r), ffma2(x.p[i], both(tx), u.p[i]));
+          v.p[i] = fmul2(both(r), ffma2(y.p[i], both(tx), v.p[i]));
+        }
+        pack_chunk<kInter>(u, v, ga, gb);
+        __nv_bfloat16* dx = w.dx + j * step * ra.dst_h[t];
+        *reinterpret_cast<uint4*>(dx + o0) = ga;
+        if (two) *reinterpret_cast<uint4*>(dx + o1) = gb;
       }
-      *reinterpret_cast<uint4*>(dx + o0) = pack_bf16x8(u);
-      if (two) *reinterpret_cast<uint4*>(dx + o1) = pack_bf16x8(v);
-    }
+    };
+    unrolled<kPer>(head);
+    w = next;
   }
+  cp_async_wait<0>();
 
   if (!a.part) return;
   // part[set][feature of the head]; a set's tensor follows from its group
+  float* part = reinterpret_cast<float*>(&ring[0][0]);
+  static_assert(sizeof(ring) >= kBwdThreads * 16 * 4, "the partial sums fit the ring");
   const int row = a.lanes * 16;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (in0) part[set_in * row + o0 + i] = da[i];
-    if (two) part[set_in * row + o1 + i] = db[i];
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float lo, hi;
+      f2_unpack(k ? dwy.p[i] : dwx.p[i], lo, hi);
+      const int f = feature<kInter>(2 * i, k, o0, o1), h = feature<kInter>(2 * i + 1, k, o0, o1);
+      if (f < ra.D) part[set_in * row + f] = lo;
+      if (h < ra.D) part[set_in * row + h] = hi;
+    }
   }
   __syncthreads();
   for (int f = threadIdx.x; f < 2 * ra.D; f += kBwdThreads) {
@@ -247,25 +482,33 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
   }
 }
 
-// dw[f] = the blocks' partial sums of feature f, in order within eight interleaved runs.
-__global__ void __launch_bounds__(256) norm_weights_kernel(const float* part, int blocks, int D,
-                                                           float* dq_w, float* dk_w) {
-  __shared__ float run[8][32];
-  const int f = blockIdx.x * 32 + (threadIdx.x & 31), k0 = threadIdx.x >> 5;
+// dw[f] = the blocks' partial sums of feature f, in order within 32 interleaved runs.
+constexpr int kRuns = 32;
+__global__ void __launch_bounds__(32 * kRuns) norm_weights_kernel(const float* part, int blocks,
+                                                                  int D, float* dq_w, float* dk_w) {
+  __shared__ float run[kRuns][33];
+  const int lane = threadIdx.x & 31, k0 = threadIdx.x >> 5, f = blockIdx.x * 32 + lane;
   grid_dependency_wait();
   float s = 0.f;
-  if (f < 2 * D)
-    for (int k = k0; k < blocks; k += 8) s += part[static_cast<int64_t>(k) * 2 * D + f];
-  run[k0][threadIdx.x & 31] = s;
+  if (f < 2 * D) {
+#pragma unroll 8
+    for (int k = k0; k < blocks; k += kRuns) s += part[static_cast<int64_t>(k) * 2 * D + f];
+  }
+  run[k0][lane] = s;
   __syncthreads();
-  if (k0 || f >= 2 * D) return;
-  for (int k = 1; k < 8; ++k) s += run[k][threadIdx.x];
-  float* out = f < D ? dq_w : dk_w;
-  if (out) out[f < D ? f : f - D] = s;
+  // a warp adds a feature's runs
+  s = run[lane][k0];
+#pragma unroll
+  for (int m = kRuns / 2; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  const int g = blockIdx.x * 32 + k0;
+  if (lane || g >= 2 * D) return;
+  float* out = g < D ? dq_w : dk_w;
+  if (out) out[g < D ? g : g - D] = s;
 }
 
-// Lanes per head, groups of heads.
+// Lanes per head, groups of up to `heads` heads.
 void plan_groups(NormArgs* a, int heads) {
+  a->per = heads;
   const int chunks = (a->r.D + 15) / 16;
   a->lanes = 1;
   a->log_lanes = 0;
@@ -281,11 +524,28 @@ void plan_groups(NormArgs* a, int heads) {
   }
 }
 
+// Heads of a group in the backward: two in short calls (240 tokens of 32 + 8 heads of 128: 8.3 us, 10.8
+// with eight), else eight (512 tokens: 12.1, 12.9 with two).
+int bwd_heads(int64_t tokens, int heads, int D) {
+  return tokens * heads * ((D + 15) / 16) < 152 * 1024 ? kBwdShort : kBwdLong;
+}
+
+template <bool kInter, bool kAppend>
+void launch_fwd(const NormArgs& a, unsigned grid, cudaStream_t stream) {
+  if (a.per == kFwdLong)
+    norm_rope_kernel<kInter, kAppend, kFwdLong><<<grid, kFwdThreads, 0, stream>>>(a);
+  else
+    norm_rope_kernel<kInter, kAppend, kFwdShort><<<grid, kFwdThreads, 0, stream>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t tokens,
                              cudaStream_t stream) {
-  plan_groups(&a, kFwdHeads);
+  const int64_t H = a.r.heads[0] + a.r.heads[1] + a.r.heads[2];
+  // two heads a thread while that leaves the SMs room (512 tokens of 32 + 8 heads of 128: 4.8 us, 5.5 with
+  // eight), eight beyond (1024 tokens: 6.4, 7.4 with two)
+  plan_groups(&a, tokens * H * ((a.r.D + 15) / 16) < 152 * 1536 ? kFwdShort : kFwdLong);
   const int64_t per_tok = static_cast<int64_t>(a.lanes) * a.r.n_groups;
   // thread indices fit 32 bits; a longer call goes in several launches
   const int64_t most = ((int64_t(1) << 31) - 1) / per_tok;
@@ -296,11 +556,11 @@ cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t 
     const unsigned grid = static_cast<unsigned>((n * per_tok + kFwdThreads - 1) / kFwdThreads);
     launch_begin(16, stream);
     if (append) {
-      if (interleaved) norm_rope_kernel<true, true><<<grid, kFwdThreads, 0, stream>>>(a);
-      else norm_rope_kernel<false, true><<<grid, kFwdThreads, 0, stream>>>(a);
+      if (interleaved) launch_fwd<true, true>(a, grid, stream);
+      else launch_fwd<false, true>(a, grid, stream);
     } else {
-      if (interleaved) norm_rope_kernel<true, false><<<grid, kFwdThreads, 0, stream>>>(a);
-      else norm_rope_kernel<false, false><<<grid, kFwdThreads, 0, stream>>>(a);
+      if (interleaved) launch_fwd<true, false>(a, grid, stream);
+      else launch_fwd<false, false>(a, grid, stream);
     }
     const cudaError_t e = cudaGetLastError();
     launch_end(16, stream);
@@ -314,8 +574,8 @@ int norm_bwd_blocks(int64_t tokens, int D, int heads_q, int heads_k) {
   a.r.D = D;
   a.r.heads[0] = heads_q;
   a.r.heads[1] = heads_k;
-  plan_groups(&a, kBwdHeads);
-  // a block for every 256 threads of work, at most kNormBwdBlocks; at least a walker for each group
+  plan_groups(&a, bwd_heads(tokens, heads_q + heads_k, D));
+  // a block for every block's worth of work, at most kNormBwdBlocks; at least a walker for each group
   const int sets = kBwdThreads / a.lanes;
   const int64_t least = (static_cast<int64_t>(a.r.n_groups) + sets - 1) / sets;
   const int64_t work = tokens > (int64_t(1) << 32) ? int64_t(1) << 40 : tokens * a.r.n_groups;
@@ -326,16 +586,18 @@ int norm_bwd_blocks(int64_t tokens, int D, int heads_q, int heads_k) {
 
 cudaError_t launch_norm_rope_bwd(NormArgs a, bool interleaved, float* dq_w, float* dk_w,
                                  cudaStream_t stream) {
-  plan_groups(&a, kBwdHeads);
+  plan_groups(&a, bwd_heads(a.tokens, a.r.heads[0] + a.r.heads[1], a.r.D));
   const int blocks = norm_bwd_blocks(a.tokens, a.r.D, a.r.heads[0], a.r.heads[1]);
+  auto* kernel = a.per == kBwdLong
+                     ? interleaved ? norm_rope_bwd_kernel<true, kBwdLong> : norm_rope_bwd_kernel<false, kBwdLong>
+                     : interleaved ? norm_rope_bwd_kernel<true, kBwdShort> : norm_rope_bwd_kernel<false, kBwdShort>;
   launch_begin(16, stream);
-  if (interleaved) norm_rope_bwd_kernel<true><<<blocks, kBwdThreads, 0, stream>>>(a);
-  else norm_rope_bwd_kernel<false><<<blocks, kBwdThreads, 0, stream>>>(a);
+  kernel<<<blocks, kBwdThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   launch_end(16, stream);
   if (e != cudaSuccess || !a.part) return e;
   launch_begin(16, stream);
-  e = launch_after(norm_weights_kernel, dim3((2 * a.r.D + 31) / 32), dim3(256), 0, stream, true,
+  e = launch_after(norm_weights_kernel, dim3((2 * a.r.D + 31) / 32), dim3(32 * kRuns), 0, stream, true,
                    static_cast<const float*>(a.part), blocks, a.r.D, dq_w, dk_w);
   launch_end(16, stream);
   return e;

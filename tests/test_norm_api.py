@@ -86,7 +86,8 @@ def test_workspace():
     ws = up.upipe_norm_rope_workspace_bytes
     assert ws(1, 1 << 30, 32, 8, 128) == 608 * 2 * 128 * 4
     assert 0 < ws(1, 1, 1, 0, 64) <= 608 * 2 * 64 * 4
-    assert ws(1, 1, 65536, 0, 512) == 65536 // 2 // 8 * 2 * 512 * 4  # 8 head groups a block
+    # a block for each four groups of eight heads at least
+    assert ws(1, 1, 65536, 0, 512) == 65536 // 8 // 4 * 2 * 512 * 4
     for bad in ((0, 1, 4, 1, 64), (1, 0, 4, 1, 64), (1, 1, 0, 0, 64), (1, 1, 65536, 1, 64),
                 (1, 1, 4, 1, 60), (1, 1, 4, 1, 520), (2, 1 << 40, 4, 1, 64), (1, 1, -1, 3, 64)):
         assert ws(*bad) == 0

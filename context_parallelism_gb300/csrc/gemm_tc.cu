@@ -140,21 +140,42 @@ struct Epi<kEpiCeFwd> {
 
 // Two walks over the accumulator: the row's maximum over the tile, then the sums against it. The
 // maximum's own ones are counted, not added to the others' sum (see logp.cu).
+// Logits are wanted for the row's `slots` largest alone. Each slot holds the largest logit of every
+// slots-th tile so far, so all slots' smallest is a bound below which no logit can be among them: a
+// slice of 32 columns below it is not stored. (4096 x 128256 logits: 3.0 ms with all of them
+// stored.) The bound only grows; an older one stores more, never less.
 template <>
 struct Epi<kEpiLogp> {
-  float mx = -INFINITY, rest = 0.f, sum1 = 0.f, count = 0.f;
+  float mx = -INFINITY, rest = 0.f, sum1 = 0.f;
+  int count = 0;
+  uint32_t bound = 0, stored = 0;
+  bool keep = false;  // logits are wanted of this row
   int64_t tg = -1;
   __device__ void begin(const GemmArgs& a, int64_t row, bool row_ok) {
     mx = -INFINITY;
-    rest = sum1 = count = 0.f;
+    rest = sum1 = 0.f;
+    count = 0;
+    stored = 0;
+    bound = 0xffffffffu;
+    keep = a.c && row_ok;
+    if (keep)
+      for (int k = 0; k < a.slots; ++k)
+        bound = min(bound, *static_cast<const volatile uint32_t*>(a.best + static_cast<int64_t>(k) * a.M + row));
     tg = row_ok && a.target ? a.target[row] : -1;
   }
   __device__ void look(const float* x) {
 #pragma unroll
     for (int j = 0; j < 32; j += 2) mx = fmax3(mx, x[j], x[j + 1]);
   }
-  __device__ void slice(const GemmArgs& a, int64_t row, bool row_ok, int col0, const float* x) {
-    if (a.c && row_ok) {
+  __device__ void looked(const GemmArgs& a, int64_t row, int nt) {
+    if (keep) atomicMax(a.best + static_cast<int64_t>(nt % a.slots) * a.M + row, order_key(mx));
+  }
+  __device__ void slice(const GemmArgs& a, int64_t row, int c, int col0, const float* x) {
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < 31; j += 2) top = fmax3(top, x[j], x[j + 1]);
+    if (keep && order_key(fmaxf(top, x[31])) >= bound) {
+      stored |= 1u << (c >> 5);
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.c) + row * a.ldc + col0);
 #pragma unroll
       for (int v = 0; v < 8; ++v)
@@ -164,9 +185,9 @@ struct Epi<kEpiLogp> {
     for (int j = 0; j < 32; ++j) {
       const float d = x[j] - mx;
       const float e = ex2_approx(d * kLog2e);
-      const bool top = x[j] == mx;
-      rest += top ? 0.f : e;
-      count += top ? 1.f : 0.f;
+      const bool max = x[j] == mx;
+      rest += max ? 0.f : e;
+      count += max ? 1 : 0;
       sum1 = fmaf(e, fmaxf(d, -1000.f), sum1);  // d = 0 for the maximum; no 0 * inf for -inf
     }
     const int64_t off = tg - col0;
@@ -179,8 +200,9 @@ struct Epi<kEpiLogp> {
     }
   }
   __device__ void end(const GemmArgs& a, int64_t row, bool row_ok, int nt, int) {
-    if (!row_ok) return;
-    reinterpret_cast<float4*>(a.part)[row * a.part_stride + nt] = make_float4(mx, rest, sum1, count);
+    if (row_ok)
+      reinterpret_cast<float4*>(a.part)[row * a.part_stride + nt] =
+          make_float4(mx, rest, sum1, logp_mark(count, stored));
   }
 };
 
@@ -518,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if constexpr (EPI == kEpiLogp) {
 #pragma unroll 1
-        for (int walk = 0; walk < 2; ++walk)
+        for (int walk = 0; walk < 2; ++walk) {
+          if (walk == 1) e.looked(a, row, nt);
 #pragma unroll 1
           for (int c = 0; c < kBN; c += 32) {
             if (n0 + c >= a.N) break;
@@ -533,8 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n0 + c + j >= a.N) x[j] = -INFINITY;
             }
             if (walk == 0) e.look(x);
-            else e.slice(a, row, row_ok, n0 + c, x);
+            else e.slice(a, row, c, n0 + c, x);
           }
+        }
       } else {
         for (int c = 0; c < kBN; c += 32) {
           if (n0 + c >= a.N) break;  // N % 64 == 0: a slice is wholly inside or outside

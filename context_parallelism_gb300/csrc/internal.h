@@ -282,6 +282,8 @@ struct GemmArgs {
   float* part;            // CE_FWD: float2 [ceil(N/256)][part_stride] (max in log2 units, sum)
   int64_t part_stride;    // LOGP: float4 [M][part_stride], one for each N tile
   float* tlogit;          // CE_FWD, LOGP: [M] logit at the target
+  uint32_t* best;         // LOGP with c: [slots][M] order_keys, zeros before the call; slot n % slots
+  int slots;              // gets the largest of the N tiles n, and what is below all slots is not stored
   void* c2;               // SWIGLU: optional bf16 g | u store [M][ldc2] (u at column split + j)
   int64_t ldc2;
   const void* aux;        // DSWIGLU: bf16 g | u [M][ld_aux]
@@ -476,7 +478,7 @@ struct LogpArgs {
   const __nv_bfloat16 *h, *w;  // [M][Dm], [V][Dm]
   const int64_t* target;       // [M], or NULL
   float* tlogit;               // [M] logit at the target
-  float4* part;                // [M][groups]: see logp.cu
+  float4* part;                // [M][groups]: see logp.cu (the last word: logp_mark)
   float* logits;               // [M][ldl], or NULL (no alternatives)
   int64_t ldl;
   float *logp, *entropy, *lse; // [M]; each may be NULL
@@ -487,6 +489,18 @@ struct LogpArgs {
   int groups, per_run, run, width;
   uint32_t* err;
 };
+#ifdef __CUDACC__
+// Last word of a group's sums: how often its maximum occurs, and which of its slices of 32 columns are
+// stored (bit k: columns 32 k and on).
+__device__ __forceinline__ float logp_mark(int count, uint32_t stored) {
+  return __uint_as_float(static_cast<uint32_t>(count) | stored << 16);
+}
+// Unsigned numbers in the order of the floats (-0 as +0); 0 is below all of them.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+#endif
 __host__ __device__ inline int64_t group_start(const LogpArgs& a, int g) {
   const int r = g / a.per_run;
   return static_cast<int64_t>(r) * a.run + static_cast<int64_t>(g - r * a.per_run) * a.width;

@@ -39,6 +39,11 @@ using Sums = float4;
 
 __device__ __forceinline__ Sums no_sums() { return make_float4(-INFINITY, 0.f, 0.f, 0.f); }
 
+// In memory the last one is logp_mark's word.
+__device__ __forceinline__ Sums read_sums(const float4& s) {
+  return make_float4(s.x, s.y, s.z, static_cast<float>(__float_as_uint(s.w) & 0xffffu));
+}
+
 // s brought to the maximum m >= s.x, its own maximum among the others where m is larger.
 __device__ __forceinline__ Sums rebase(const Sums& s, float m) {
   if (s.x == m) return s;
@@ -56,12 +61,14 @@ constexpr int kAccs = 4;
 template <int N>
 struct ShortLayout {
   static constexpr int kA = 128 * 128, kB = N * 128, kStage = kA + kB;
-  static constexpr int kStages = (220 * 1024) / kStage;
-  static constexpr int kBar = kStages * kStage;
+  static constexpr int kTile = N * 128 * 4;  // the logits of a tile, [token][column]
+  static constexpr int kStages = (224 * 1024 - kTile) / kStage;
+  static constexpr int kX = kStages * kStage;
+  static constexpr int kBar = kX + kTile;
   static constexpr int kNumBars = 2 * kStages + 2 * kAccs + 1;
-  static constexpr int kComb = kBar + (kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kSlot = kComb + 4 * N * 16;
+  static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kBytes = kSlot + 16 + 1024;
+  static_assert(kBytes <= 227 * 1024, "a block's shared memory");
 };
 
 template <int N>
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   uint64_t* acc_full = empty + L::kStages;
   uint64_t* acc_empty = acc_full + kAccs;
   uint64_t* drain = acc_empty + kAccs;
-  Sums* comb = reinterpret_cast<Sums*>(smem + L::kComb);
+  float* tile = reinterpret_cast<float*>(smem + L::kX);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
   constexpr uint32_t kCols = kAccs * N;
@@ -263,52 +270,55 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           ph ^= 1;
         }
       }
-      const int64_t col = v_lo + 128 * t + r;
-      const bool in = 128 * t + r < rows;
+      // logits to [token][column], so that a warp takes a token's 128 at a time: sums over the
+      // lanes once a token, not once a token and warp, and whole lines to memory
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the tile before is done with
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         if (n >= a.M) break;
-        const float x = in ? acc[n] : -INFINITY;
-        if (in && a.logits) a.logits[n * a.ldl + col] = x;
-        if (in && a.target && a.target[n] == col) a.tlogit[n] = x;
-        float m = x;
+        tile[n * 128 + r] = acc[n];
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const int left = rows - 128 * t;  // columns of this tile, and more
+      const int64_t col = v_lo + 128 * t + 4 * lane;
+#pragma unroll 2
+      for (int n = quarter; n < a.M; n += 4) {
+        float4 v = reinterpret_cast<const float4*>(tile + n * 128)[lane];
+        if (4 * lane + 0 >= left) v.x = -INFINITY;
+        if (4 * lane + 1 >= left) v.y = -INFINITY;
+        if (4 * lane + 2 >= left) v.z = -INFINITY;
+        if (4 * lane + 3 >= left) v.w = -INFINITY;
+        // (a run's columns are a multiple of 16, or end the padded row)
+        if (a.logits && 4 * lane < left) *reinterpret_cast<float4*>(a.logits + n * a.ldl + col) = v;
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        if (a.target) {
+          const int64_t k = a.target[n] - col;
+          if (k >= 0 && k < 4 && 4 * lane + k < left)
+            a.tlogit[n] = k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
+        }
+        float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-        const bool top = x == m;
-        const float d = x - m;
-        const float e = top || !in ? 0.f : exp2f(d * kLog2e);  // NaN stays
-        float sum = e, sum1 = e * fmaxf(d, -1000.f);
-        if (!in) sum1 = 0.f;
+        float sum = 0.f, sum1 = 0.f;
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = 4 * lane + k < left, top = x[k] == m;
+          const float d = x[k] - m;
+          const float e = top || !in ? 0.f : exp2f(d * kLog2e);  // NaN stays
+          sum += e;
+          if (in) sum1 = fmaf(e, fmaxf(d, -1000.f), sum1);
+          count += __popc(__ballot_sync(kAll, top && in));
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           sum += __shfl_xor_sync(kAll, sum, o);
           sum1 += __shfl_xor_sync(kAll, sum1, o);
         }
-        const int count = __popc(__ballot_sync(kAll, top && in));
-        if (lane == 0) comb[quarter * N + n] = make_float4(m, sum, sum1, static_cast<float>(count));
+        if (lane == 0)
+          a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] =
+              make_float4(m, sum, sum1, logp_mark(count, 15u));
       }
-      // the four warps' sums as one group (a warp whose wait expired keeps step at these barriers)
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      const int n = threadIdx.x - 64;
-      if (n < N && n < a.M) {
-        Sums s[4];
-        float m = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          s[q] = comb[q * N + n];
-          m = fmaxf(m, s[q].x);
-        }
-        Sums all = make_float4(m, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const Sums u = rebase(s[q], m);
-          all.y += u.y;
-          all.z += u.z;
-          all.w += u.w;
-        }
-        a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] = all;
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
     }
     // groups that this run does not reach
     for (int t = tiles; t < a.per_run; ++t)
@@ -326,99 +336,178 @@ __global__ void __launch_bounds__(kShortThreads, 1)
 
 // ---- rows' results ----------------------------------------------------------------------------
 
-constexpr int kPickThreads = 256;
-constexpr int kNone = 0x7fffffff;
+constexpr int kOwn = 4;  // groups that a thread keeps in registers
 
-__device__ __forceinline__ bool before(float v, int i, float u, int j) {
-  return v > u || (v == u && i < j);
+// The `want` (at most 32) items of [0, n) with the largest keys, equal ones by number, in any order, to
+// list; returns how many there are. Items with a key below `least` (1 or more) do not count. A radix
+// selection: the digits of the last one's key from the top, by counting, until the items with the
+// digits so far are all wanted. The whole block calls.
+template <int kThreads, typename Key>
+__device__ int block_select(Key key, int n, int want, uint32_t least, int* list, uint32_t* counts) {
+  __shared__ uint32_t prefix_s, need_s, exact_s, found_s;
+  const int lane = threadIdx.x & 31;
+  uint32_t prefix = 0, mask = 0, need = want;
+  bool exact = false;
+  for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
+    __syncthreads();
+    if (threadIdx.x < 256) counts[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const uint32_t k = key(i);
+      if (k >= least && (k & mask) == prefix) atomicAdd(&counts[(k >> shift) & 255], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // eight digits a lane, the largest first
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += c[j] = counts[255 - 8 * lane - j];
+      uint32_t up = sum;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t o = __shfl_up_sync(kAll, up, m);
+        if (lane >= m) up += o;
+      }
+      uint32_t above = up - sum;
+      const uint32_t all = __shfl_sync(kAll, up, 31);
+      if (all <= need) {  // (first digit) no more than are wanted
+        if (lane == 0) {
+          prefix_s = 0;
+          need_s = all;
+          exact_s = 1;
+        }
+      } else if (above < need && need <= up) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (above < need && need <= above + c[j]) {
+            prefix_s = prefix | static_cast<uint32_t>(255 - 8 * lane - j) << shift;
+            need_s = need - above;
+            exact_s = need - above == c[j];
+          }
+          above += c[j];
+        }
+      }
+      if (lane == 0) found_s = 0;
+    }
+    __syncthreads();
+    prefix = prefix_s;
+    need = need_s;
+    exact = exact_s != 0;
+    mask |= 255u << shift;
+  }
+  // exact: every key from the prefix on; else those above the prefix, which is a whole key now, and
+  // the first `need` of its own
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t k = key(i);
+    if (k >= least && (exact ? k >= prefix : k > prefix)) list[atomicAdd(&found_s, 1u)] = i;
+  }
+  __syncthreads();
+  int found = static_cast<int>(found_s);
+  if (!exact) {
+    if (threadIdx.x < 32) {
+      uint32_t taken = 0;
+      for (int i0 = 0; taken < need; i0 += 32) {
+        const bool is = i0 + lane < n && key(i0 + lane) == prefix;
+        const uint32_t all = __ballot_sync(kAll, is);
+        const uint32_t at = taken + __popc(all & ((1u << lane) - 1));
+        if (is && at < need) list[found + at] = i0 + lane;
+        taken += __popc(all);
+      }
+    }
+    found += static_cast<int>(need);
+    __syncthreads();
+  }
+  return found;
 }
 
-// The `n` best (value, index) so far, one a lane, best first; empty places hold (-inf, kNone).
-struct Best {
-  float v = -INFINITY;
-  int i = kNone;
-  // Offers a lane's own (u, j) of every lane; `ask` says which take part. All lanes call.
-  __device__ __forceinline__ void offer(float u, int j, bool ask, int n) {
-    const int lane = threadIdx.x & 31;
-    float last_v = __shfl_sync(kAll, v, n - 1);
-    int last_i = __shfl_sync(kAll, i, n - 1);
-    uint32_t left = __ballot_sync(kAll, ask && before(u, j, last_v, last_i));
-    while (left) {
-      const int l = __ffs(left) - 1;
-      left &= left - 1;
-      const float cu = __shfl_sync(kAll, u, l);
-      const int cj = __shfl_sync(kAll, j, l);
-      if (!before(cu, cj, last_v, last_i)) continue;
-      const int at = __popc(__ballot_sync(kAll, before(v, i, cu, cj)));
-      const float up_v = __shfl_up_sync(kAll, v, 1);
-      const int up_i = __shfl_up_sync(kAll, i, 1);
-      if (lane > at) {
-        v = up_v;
-        i = up_i;
-      }
-      if (lane == at) {
-        v = cu;
-        i = cj;
-      }
-      last_v = __shfl_sync(kAll, v, n - 1);
-      last_i = __shfl_sync(kAll, i, n - 1);
-    }
-  }
-};
-
-// <h, w> of two rows of Dm bf16 by one warp, with an error near 2^-45 of the terms: each lane keeps its
-// sum and the sum of what each addition lost.
-__device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm) {
+// The part of <h, w>, two rows of Dm bf16, that falls to one warp of two (which: 0 or 1; turns of 2048
+// features), with an error near 2^-45 of the terms: each lane keeps its sums and the sums of what each
+// addition lost.
+__device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
+                                            int which) {
+  constexpr int kAhead = 8;  // the rows come from anywhere in w: their vectors are asked for together
   const int lane = threadIdx.x & 31;
-  float s = 0.f, lost = 0.f;
-  for (int k = lane * 8; k < Dm; k += 256) {
-    float x[8], y[8];
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(h + k), x);
-    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(w + k)), y);
+  float s[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
+  for (int k0 = which * 256 * kAhead + lane * 8; k0 < Dm; k0 += 2 * 256 * kAhead) {
+    uint4 a[kAhead], b[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = __fmul_rn(x[i], y[i]);
-      const float t = __fadd_rn(s, p);
-      const float b = __fadd_rn(t, -s);
-      lost = __fadd_rn(lost, __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -b)), __fadd_rn(p, -b)));
-      s = t;
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + 256 * j;
+      a[j] = b[j] = make_uint4(0, 0, 0, 0);
+      if (k < Dm) {
+        b[j] = __ldg(reinterpret_cast<const uint4*>(w + k));
+        a[j] = *reinterpret_cast<const uint4*>(h + k);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      float x[8], y[8];
+      unpack_bf16x8(a[j], x);
+      unpack_bf16x8(b[j], y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float& u = s[i & 1];
+        const float p = __fmul_rn(x[i], y[i]);
+        const float t = __fadd_rn(u, p);
+        const float z = __fadd_rn(t, -u);
+        lost[i & 1] = __fadd_rn(lost[i & 1],
+                                __fadd_rn(__fadd_rn(u, -__fadd_rn(t, -z)), __fadd_rn(p, -z)));
+        u = t;
+      }
     }
   }
-  double d = static_cast<double>(s) + static_cast<double>(lost);
+  double d = (static_cast<double>(s[0]) + static_cast<double>(s[1])) +
+             (static_cast<double>(lost[0]) + static_cast<double>(lost[1]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(kAll, d, o);
   return d;
 }
 
 // One block per row. smem: `keep` groups of `width` logits.
-__global__ void __launch_bounds__(kPickThreads) logp_pick_kernel(const LogpArgs a) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ float picked[];
-  __shared__ float red[kPickThreads / 32][3];
+  __shared__ float red[kWarps][3];
   __shared__ float row_max, row_ln;
-  __shared__ int grp[32], cand[32];
+  __shared__ uint32_t counts[256];
+  __shared__ int list[32], grp[32], cand[32];
+  __shared__ uint32_t grp_least;
   __shared__ float cand_x[32];
-  __shared__ double cand_y[32];
+  __shared__ double cand_y[32][2];
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
-  const Sums* part = a.part + row * a.groups;
+  const float4* part = a.part + row * a.groups;
 
+  Sums own[kOwn];
   float m = -INFINITY;
-  for (int g = threadIdx.x; g < a.groups; g += kPickThreads) m = fmaxf(m, part[g].x);
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int g = threadIdx.x + k * kThreads;
+    own[k] = g < a.groups ? read_sums(part[g]) : no_sums();
+  }
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) m = fmaxf(m, own[k].x);
+  for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads)
+    m = fmaxf(m, part[g].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   if (lane == 0) red[warp][0] = m;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kPickThreads / 32; ++k) m = fmaxf(m, red[k][0]);
+  for (int k = 0; k < kWarps; ++k) m = fmaxf(m, red[k][0]);
   __syncthreads();
   float rest = 0.f, sum1 = 0.f, count = 0.f;
-  for (int g = threadIdx.x; g < a.groups; g += kPickThreads) {
-    const Sums u = rebase(part[g], m);
+  auto add = [&](const Sums& s) {
+    const Sums u = rebase(s, m);
     rest += u.y;
     sum1 += u.z;
     count += u.w;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) add(own[k]);
+  for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads) add(read_sums(part[g]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     rest += __shfl_xor_sync(kAll, rest, o);
@@ -433,7 +522,7 @@ __global__ void __launch_bounds__(kPickThreads) logp_pick_kernel(const LogpArgs 
   __syncthreads();
   if (threadIdx.x == 0) {
     rest = sum1 = count = 0.f;
-    for (int k = 0; k < kPickThreads / 32; ++k) {
+    for (int k = 0; k < kWarps; ++k) {
       rest += red[k][0];
       sum1 += red[k][1];
       count += red[k][2];
@@ -457,66 +546,79 @@ __global__ void __launch_bounds__(kPickThreads) logp_pick_kernel(const LogpArgs 
   float* out_v = a.top_logp + row * a.top;
   int64_t* out_i = a.top_index + row * a.top;
   if (!(fabsf(ln) <= FLT_MAX)) {
-    for (int k = threadIdx.x; k < a.top; k += kPickThreads) {
+    for (int k = threadIdx.x; k < a.top; k += kThreads) {
       out_v[k] = __int_as_float(0x7fc00000);
       out_i[k] = -1;
     }
     return;
   }
 
-  const int keep = a.keep;
-  if (warp == 0) {
-    Best b;
-    for (int g0 = 0; g0 < a.groups; g0 += 32) {
-      const int g = g0 + lane;
-      const bool in = g < a.groups;
-      const float x = in ? part[g].x : 0.f;
-      // a group of a run that ends before it has no column
-      b.offer(x, g, in && group_start(a, g) < a.V && group_width(a, g) > 0, keep);
+  // the groups with the largest maxima (one of a run that ends before it has no column), by number
+  auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
+  uint32_t* keys = reinterpret_cast<uint32_t*>(picked);  // not used yet
+  const bool fits = a.groups <= a.keep * a.width;
+  if (fits)
+    for (int g = threadIdx.x; g < a.groups; g += kThreads) keys[g] = group_key(g);
+  const int groups = block_select<kThreads>([&](int g) { return fits ? keys[g] : group_key(g); }, a.groups,
+                                  a.keep, 1u, list, counts);
+  if (threadIdx.x < 32) {
+    const int mine = lane < groups ? list[lane] : 0x7fffffff;
+    int rank = 0;
+    for (int k = 0; k < groups; ++k) rank += list[k] < mine;
+    uint32_t least = 0xffffffffu;
+    if (lane < groups) {
+      grp[rank] = mine;
+      least = order_key(part[mine].x);
     }
-    grp[lane] = lane < keep ? b.i : kNone;
+    least = __reduce_min_sync(kAll, least);
+    // with as many groups as are kept, their maxima are as many logits: none below counts
+    if (lane == 0) grp_least = groups == a.keep ? least : 1u;
   }
   __syncthreads();
   const float* x = a.logits + row * a.ldl;
-  for (int k = warp; k < keep; k += kPickThreads / 32) {
-    const int g = grp[k];
-    if (g == kNone) continue;
-    const int64_t c0 = group_start(a, g);
-    const int n = group_width(a, g);
-    for (int c = lane; c < n; c += 32) picked[k * a.width + c] = x[c0 + c];
+  for (int k = warp; k < groups; k += kWarps) {
+    const int64_t c0 = group_start(a, grp[k]);
+    const int n = group_width(a, grp[k]);
+    // columns that were not stored are below as many others
+    const uint32_t stored = __float_as_uint(part[grp[k]].w) >> 16;
+    for (int c = lane; c < a.width; c += 32)
+      picked[k * a.width + c] = c < n && (stored >> (c >> 5) & 1) ? x[c0 + c] : NAN;
   }
   __syncthreads();
-  if (warp == 0) {
-    Best b;
-    for (int k = 0; k < keep; ++k) {
-      const int g = grp[k];
-      if (g == kNone) break;
-      const int c0 = static_cast<int>(group_start(a, g)), n = group_width(a, g);
-      for (int c = 0; c < n; c += 32)
-        b.offer(c + lane < n ? picked[k * a.width + c + lane] : 0.f, c0 + c + lane, c + lane < n, keep);
-    }
-    cand[lane] = lane < keep ? b.i : kNone;
-    cand_x[lane] = b.v;
+  const int found = block_select<kThreads>(
+      [&](int i) {
+        const float v = picked[i];
+        return v == v ? order_key(v) : 0u;
+      },
+      groups * a.width, a.keep, grp_least, list, counts);
+  if (threadIdx.x < found) {
+    const int i = list[threadIdx.x], k = i / a.width;
+    cand[threadIdx.x] = static_cast<int>(group_start(a, grp[k])) + i - k * a.width;
+    cand_x[threadIdx.x] = picked[i];
   }
   __syncthreads();
-  for (int k = warp; k < keep; k += kPickThreads / 32) {
-    if (cand[k] == kNone) continue;
-    const double y = dot_again(a.h + row * a.Dm, a.w + static_cast<int64_t>(cand[k]) * a.Dm, a.Dm);
-    // where infinities or an overflow leave no sum, the order is that of the logits
-    if (lane == 0) cand_y[k] = fabs(y) <= DBL_MAX ? y : static_cast<double>(cand_x[k]);
+  for (int k = warp; k < 2 * found; k += kWarps) {
+    const double y = dot_again(a.h + row * a.Dm,
+                               a.w + static_cast<int64_t>(cand[k >> 1]) * a.Dm, a.Dm, k & 1);
+    if (lane == 0) cand_y[k >> 1][k & 1] = y;
   }
   __syncthreads();
   if (threadIdx.x >= 32) return;
-  const int me = lane < keep ? cand[lane] : kNone;
-  const int found = __popc(__ballot_sync(kAll, me != kNone));
   if (lane >= found && lane < a.top) {  // fewer columns than asked for
     out_v[lane] = -INFINITY;
     out_i[lane] = -1;
   }
-  if (me == kNone) return;
+  // where infinities or an overflow leave no sum, the order is that of the logits
+  double y = lane < found ? cand_y[lane][0] + cand_y[lane][1] : 0.0;
+  if (!(fabs(y) <= DBL_MAX)) y = static_cast<double>(cand_x[lane]);
+  const int me = lane < found ? cand[lane] : 0;
   int rank = 0;
-  for (int k = 0; k < found; ++k)
-    if (cand_y[k] > cand_y[lane] || (cand_y[k] == cand_y[lane] && cand[k] < me)) ++rank;
+  for (int k = 0; k < found; ++k) {
+    const double z = __shfl_sync(kAll, y, k);
+    const int other = __shfl_sync(kAll, me, k);
+    if (z > y || (z == y && other < me)) ++rank;
+  }
+  if (lane >= found) return;
   if (rank < a.top) {
     out_v[rank] = (cand_x[lane] - m) - ln;
     out_i[rank] = me;
@@ -550,10 +652,14 @@ cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, co
 }
 
 cudaError_t launch_logp_pick(const LogpArgs& a, cudaStream_t stream) {
+  const size_t smem = a.top ? static_cast<size_t>(a.keep) * a.width * 4 : 0;
+  const dim3 grid(static_cast<unsigned>(a.M));
   launch_begin(kClass, stream);
+  // Few rows: a whole SM's warps each, for the latency of a row. More: what hides it is other rows.
+  // Only a single block may start early: several would all go to the first SM that is free.
   const cudaError_t e =
-      launch_after(logp_pick_kernel, dim3(static_cast<unsigned>(a.M)), dim3(kPickThreads),
-                   a.top ? static_cast<size_t>(a.keep) * a.width * 4 : 0, stream, true, a);
+      a.M <= 152 ? launch_after(logp_pick_kernel<1024>, grid, dim3(1024), smem, stream, a.M == 1, a)
+                 : launch_after(logp_pick_kernel<256>, grid, dim3(256), smem, stream, false, a);
   launch_end(kClass, stream);
   return e;
 }

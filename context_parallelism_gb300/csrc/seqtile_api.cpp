@@ -938,7 +938,7 @@ struct LogpPlan {
   int keep = 0;              // candidates of a row
   int run = 0, per_run = 0, short_groups = 0;  // of tiles of up to kLogpShortRows rows
   int groups = 0;            // of longer ones: 256-column tiles
-  size_t part = 0, tl = 0, logits = 0, h[2] = {0, 0}, total = 0;
+  size_t part = 0, tl = 0, logits = 0, best = 0, h[2] = {0, 0}, total = 0;
 };
 
 int check_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile) {
@@ -975,7 +975,10 @@ LogpPlan plan_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile, bool
   };
   p.part = take((parts > few_parts ? parts : few_parts) * 16);
   p.tl = take(static_cast<size_t>(p.T) * 4);
-  if (top) p.logits = take(static_cast<size_t>(p.T) * p.ldl * 4);
+  if (top) {
+    p.logits = take(static_cast<size_t>(p.T) * p.ldl * 4);
+    p.best = take(static_cast<size_t>(p.T) * p.keep * 4);
+  }
   if (host_act) plan_slots(&off, p.T, int64_t(Dm) * 2, p.h);
   p.total = off;
   return p;
@@ -1090,6 +1093,11 @@ int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* l
       g.part_stride = a.groups;
       g.tlogit = a.tlogit;
       g.err = err;
+      if (top) {
+        g.best = reinterpret_cast<uint32_t*>(ws + p.best);
+        g.slots = p.keep;
+        LOSS_CUDA(cudaMemsetAsync(g.best, 0, static_cast<size_t>(Mc) * p.keep * 4, stream));
+      }
       LOSS_CUDA(launch_gemm_tc(kEpiLogp, false, false, th, tw, g, cap, stream));
     }
     LOSS_CUDA(launch_logp_pick(a, stream));

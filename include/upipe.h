@@ -280,7 +280,8 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * Supported: Dm a multiple of 8, any V up to 2^30, top up to 24, seq_tile a multiple of 128. S = 0
  * does nothing. Workspace: upipe_logp_workspace_bytes: for T = min(seq_tile, S) tokens 16 bytes for
  * each token and 256 columns (or, up to 64 tokens, each of the runs' groups of 128), 4 T, and with
- * top > 0 the tile's logits, 4 T V; each rounded up to 256, plus two slots with UPIPE_HOST_ACT.
+ * top > 0 the tile's logits, 4 T V (V rounded up to 32; few of them are written), and 4 T (top + 8);
+ * each rounded up to 256, plus two slots with UPIPE_HOST_ACT.
  * Results repeat bitwise for the same sizes.
  */
 size_t upipe_logp_workspace_bytes(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile,

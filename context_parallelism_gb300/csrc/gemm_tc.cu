@@ -24,8 +24,6 @@
 //   CE_BWD    logits -> dlogits = g_row * (exp(logit - lse_row) - [col == target]) as bf16
 //   STORE     C -> bf16
 //   ACC_F32   C -> fp32, added to what is there when accumulating, else stored
-//   LOGP      logits -> per (row, 256-column tile) the sums that the token log probabilities take
-//             (logp.cu), the target's logit, optionally the logits; any number of columns
 // and those of the sequence-tiled gated MLP (same passages: "all the MLPs" are chunked):
 //   SWIGLU    gate and up projections in one tile: the B stage holds 128 rows of the gate
 //             block and the matching 128 rows of the up block (two TMA boxes), so one
@@ -135,74 +133,6 @@ struct Epi<kEpiCeFwd> {
     reinterpret_cast<float2*>(a.part)[static_cast<int64_t>(nt) * a.part_stride + row] =
         make_float2(mx, sm);
     if (tg >= n0 && tg < n0 + kBN && tg < a.N) a.tlogit[row] = tl;
-  }
-};
-
-// Two walks over the accumulator: the row's maximum over the tile, then the sums against it. The
-// maximum's own ones are counted, not added to the others' sum (see logp.cu).
-// Logits are wanted for the row's `slots` largest alone. Each slot holds the largest logit of every
-// slots-th tile so far, so all slots' smallest is a bound below which no logit can be among them: a
-// slice of 32 columns below it is not stored. (4096 x 128256 logits: 3.0 ms with all of them
-// stored.) The bound only grows; an older one stores more, never less.
-template <>
-struct Epi<kEpiLogp> {
-  float mx = -INFINITY, rest = 0.f, sum1 = 0.f;
-  int count = 0;
-  uint32_t bound = 0, stored = 0;
-  bool keep = false;  // logits are wanted of this row
-  int64_t tg = -1;
-  __device__ void begin(const GemmArgs& a, int64_t row, bool row_ok) {
-    mx = -INFINITY;
-    rest = sum1 = 0.f;
-    count = 0;
-    stored = 0;
-    bound = 0xffffffffu;
-    keep = a.c && row_ok;
-    if (keep)
-      for (int k = 0; k < a.slots; ++k)
-        bound = min(bound, *static_cast<const volatile uint32_t*>(a.best + static_cast<int64_t>(k) * a.M + row));
-    tg = row_ok && a.target ? a.target[row] : -1;
-  }
-  __device__ void look(const float* x) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) mx = fmax3(mx, x[j], x[j + 1]);
-  }
-  __device__ void looked(const GemmArgs& a, int64_t row, int nt) {
-    if (keep) atomicMax(a.best + static_cast<int64_t>(nt % a.slots) * a.M + row, order_key(mx));
-  }
-  __device__ void slice(const GemmArgs& a, int64_t row, int c, int col0, const float* x) {
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < 31; j += 2) top = fmax3(top, x[j], x[j + 1]);
-    if (keep && order_key(fmaxf(top, x[31])) >= bound) {
-      stored |= 1u << (c >> 5);
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.c) + row * a.ldc + col0);
-#pragma unroll
-      for (int v = 0; v < 8; ++v)
-        dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-    }
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float d = x[j] - mx;
-      const float e = ex2_approx(d * kLog2e);
-      const bool max = x[j] == mx;
-      rest += max ? 0.f : e;
-      count += max ? 1 : 0;
-      sum1 = fmaf(e, fmaxf(d, -1000.f), sum1);  // d = 0 for the maximum; no 0 * inf for -inf
-    }
-    const int64_t off = tg - col0;
-    if (off >= 0 && off < 32) {
-      const int o = static_cast<int>(off);
-      float v = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v = j == o ? x[j] : v;
-      if (col0 + o < a.N) a.tlogit[row] = v;
-    }
-  }
-  __device__ void end(const GemmArgs& a, int64_t row, bool row_ok, int nt, int) {
-    if (row_ok)
-      reinterpret_cast<float4*>(a.part)[row * a.part_stride + nt] =
-          make_float4(mx, rest, sum1, logp_mark(count, stored));
   }
 };
 
@@ -538,27 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           e.slice2(a, row, row_ok, n0 + c, xg, xu);
         }
-      } else if constexpr (EPI == kEpiLogp) {
-#pragma unroll 1
-        for (int walk = 0; walk < 2; ++walk) {
-          if (walk == 1) e.looked(a, row, nt);
-#pragma unroll 1
-          for (int c = 0; c < kBN; c += 32) {
-            if (n0 + c >= a.N) break;
-            uint32_t r[32];
-            tmem_ld32_sync(tD + static_cast<uint32_t>(c), r);
-            float x[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
-            if (n0 + c + 32 > a.N) {  // the last columns of a ragged N
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n0 + c + j >= a.N) x[j] = -INFINITY;
-            }
-            if (walk == 0) e.look(x);
-            else e.slice(a, row, c, n0 + c, x);
-          }
-        }
       } else {
         for (int c = 0; c < kBN; c += 32) {
           if (n0 + c >= a.N) break;  // N % 64 == 0: a slice is wholly inside or outside
@@ -660,7 +569,6 @@ cudaError_t launch_gemm_tc(int epi, bool a_mn, bool b_mn, const CUtensorMap& ta,
                            cudaStream_t stream) {
   if (epi == kEpiCeFwd && !a_mn && !b_mn) return launch_one<kEpiCeFwd, false, false>(ta, tb, a, grid_cap, stream);
   if (epi == kEpiCeBwd && !a_mn && !b_mn) return launch_one<kEpiCeBwd, false, false>(ta, tb, a, grid_cap, stream);
-  if (epi == kEpiLogp && !a_mn && !b_mn) return launch_one<kEpiLogp, false, false>(ta, tb, a, grid_cap, stream);
   if (epi == kEpiStoreBf16 && !a_mn && b_mn) return launch_one<kEpiStoreBf16, false, true>(ta, tb, a, grid_cap, stream);
   if (epi == kEpiAccF32 && a_mn && b_mn) return launch_one<kEpiAccF32, true, true>(ta, tb, a, grid_cap, stream);
   if (epi == kEpiStoreBf16 && !a_mn && !b_mn) return launch_one<kEpiStoreBf16, false, false>(ta, tb, a, grid_cap, stream);

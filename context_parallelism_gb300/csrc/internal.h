@@ -264,7 +264,6 @@ enum : int {
   kEpiAccF32 = 3,
   kEpiSwiglu = 4,   // N = F outputs per row; B = w_gu [2F][K] with the up block at row `split`
   kEpiDSwiglu = 5,  // c = dgu [M][2F]: dg at column j, du at split + j; aux = gu likewise
-  kEpiLogp = 6,     // per row and tile the sums of logp.cu; N need not be a multiple of 64
 };
 
 struct GemmArgs {
@@ -272,18 +271,15 @@ struct GemmArgs {
   int m_fastest;          // tile order: 1 walks M tiles first (shares a B strip), 0 N tiles first
   int group_m;            // tiles of the fast dimension per group (<= 0: all), see tile_coords
   void* c;                // STORE: bf16 [M][ldc]; ACC_F32: fp32 [M][ldc]; CE_BWD: bf16 dlogits;
-                          // CE_FWD, LOGP: optional fp32 logits [M][ldc] (NULL: not stored)
+                          // CE_FWD: optional fp32 logits [M][ldc] (NULL: not stored)
   int64_t ldc;
   int accumulate;         // ACC_F32: add into c instead of overwriting
-  const int64_t* target;  // CE, LOGP: [M] vocabulary index of each row's target, < 0 = ignored
-                          // (LOGP: may be NULL)
+  const int64_t* target;  // CE: [M] vocabulary index of each row's target, < 0 = ignored
   const float* lse;       // CE_BWD: [M] natural-log log-sum-exp of each row's logits
   const float* g;         // CE_BWD: [M] upstream gradient of each row's loss
   float* part;            // CE_FWD: float2 [ceil(N/256)][part_stride] (max in log2 units, sum)
-  int64_t part_stride;    // LOGP: float4 [M][part_stride], one for each N tile
-  float* tlogit;          // CE_FWD, LOGP: [M] logit at the target
-  uint32_t* best;         // LOGP with c: [slots][M] order_keys, zeros before the call; slot n % slots
-  int slots;              // gets the largest of the N tiles n, and what is below all slots is not stored
+  int64_t part_stride;
+  float* tlogit;          // CE_FWD: [M] logit at the target
   void* c2;               // SWIGLU: optional bf16 g | u store [M][ldc2] (u at column split + j)
   int64_t ldc2;
   const void* aux;        // DSWIGLU: bf16 g | u [M][ld_aux]
@@ -292,7 +288,7 @@ struct GemmArgs {
   uint32_t* err;
 };
 
-// Supported (epi, A MN-major, B MN-major): (CE_FWD, 0, 0), (CE_BWD, 0, 0), (LOGP, 0, 0), (STORE, 0, 1),
+// Supported (epi, A MN-major, B MN-major): (CE_FWD, 0, 0), (CE_BWD, 0, 0), (STORE, 0, 1),
 // (STORE, 0, 0), (ACC_F32, 1, 1), (SWIGLU, 0, 0), (DSWIGLU, 0, 1). K-major maps have 128-row
 // (A) / 256-row (B; 128-row for SWIGLU, loaded twice) boxes; MN-major maps 64-row boxes; all
 // 64 columns wide with 128-byte swizzle. The grid is min(tiles, grid_cap) CTAs.
@@ -468,10 +464,10 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
 
 // ---- token log probabilities (logp.cu) --------------------------------------------------------
 // Rows [0, M) of one tile of a call. The logits' columns come in `groups` groups: `per_run` in each run
-// of `run` columns, `width` columns in a group (fewer at a run's end).
-constexpr int kLogpShortRows = 64;    // rows of a tile that the kernel for short calls takes at most
+// of `run` columns, kLogpWidth columns in a group (fewer at a run's end).
+constexpr int kLogpShortRows = 16;    // rows of a tile that the kernel for short calls takes at most
 constexpr int kLogpShortBlocks = 152;
-constexpr int kLogpMargin = 8;        // candidates kept behind the last alternative
+constexpr int kLogpMargin = 4;        // candidates kept behind the last alternative
 constexpr int kLogpMaxTop = 24;
 
 struct LogpArgs {
@@ -486,39 +482,30 @@ struct LogpArgs {
   int64_t* top_index;
   int M, Dm, top, keep;
   int64_t V;
-  int groups, per_run, run, width;
+  int groups, per_run, run;
+  uint32_t* best;              // longer tiles with logits: [keep][M], see logp.cu
   uint32_t* err;
 };
-#ifdef __CUDACC__
-// Last word of a group's sums: how often its maximum occurs, and which of its slices of 32 columns are
-// stored (bit k: columns 32 k and on).
-__device__ __forceinline__ float logp_mark(int count, uint32_t stored) {
-  return __uint_as_float(static_cast<uint32_t>(count) | stored << 16);
-}
-// Unsigned numbers in the order of the floats (-0 as +0); 0 is below all of them.
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-#endif
+constexpr int kLogpWidth = 128;  // columns of a group
 __host__ __device__ inline int64_t group_start(const LogpArgs& a, int g) {
   const int r = g / a.per_run;
-  return static_cast<int64_t>(r) * a.run + static_cast<int64_t>(g - r * a.per_run) * a.width;
+  return static_cast<int64_t>(r) * a.run + static_cast<int64_t>(g - r * a.per_run) * kLogpWidth;
 }
 // Columns of a group (0 or less: none).
 __host__ __device__ inline int group_width(const LogpArgs& a, int g) {
   const int64_t c = group_start(a, g);
-  const int64_t in_run = a.run - static_cast<int64_t>(g % a.per_run) * a.width;
-  int64_t n = in_run < a.width ? in_run : a.width;
+  const int64_t in_run = a.run - static_cast<int64_t>(g % a.per_run) * kLogpWidth;
+  int64_t n = in_run < kLogpWidth ? in_run : kLogpWidth;
   if (a.V - c < n) n = a.V - c;
   return static_cast<int>(n);
 }
-// Rows of the box of h's map for `rows` rows.
-int logp_short_box(int rows);
 // Logits and groups of up to kLogpShortRows rows. Maps of w with boxes of 128 and of 16 rows, of h with
-// one of logp_short_box rows.
+// one of kLogpShortRows.
 cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
                               const LogpArgs& a, cudaStream_t stream);
+// The same of more rows, one run of all columns. Maps of h with boxes of 128 rows, of w with 256.
+cudaError_t launch_logp_long(const CUtensorMap& th, const CUtensorMap& tw, const LogpArgs& a, int sms,
+                             cudaStream_t stream);
 cudaError_t launch_logp_pick(const LogpArgs& a, cudaStream_t stream);
 
 // ---- services of api.cpp to the other entry points -----------------------------------------

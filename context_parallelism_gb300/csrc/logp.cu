@@ -3,23 +3,33 @@
 //   lse = M + ln z,  z = sum exp(x_j - M),  M = max x;   logp = (x_t - M) - ln z;
 //   H = ln z - sum exp(x_j - M) (x_j - M) / z.
 //
-// The logits are made in groups of columns (256 in the tensor-core GEMM of longer calls, up to 128 in
-// the kernel for short ones below). Each group leaves, per row, its maximum, how often that occurs,
-// and the sums of e = exp(x - max) and e (x - max) over the other columns. A probability near one
-// leaves its mark in ln z alone, as z - 1; with the maximum's own ones counted apart that difference
-// is a sum of small terms and keeps all its digits (ln z = ln count + ln(1 + rest / count)).
+// The logits are made in groups of up to 128 columns, and never kept as a whole. Each group leaves, per
+// row, its maximum, how often that occurs, and the sums of e = exp(x - max) and e (x - max) over the
+// other columns. A probability near one leaves its mark in ln z alone, as z - 1; with the maximum's
+// own ones counted apart that difference is a sum of small terms and keeps all its digits
+// (ln z = ln count + ln(1 + rest / count)).
+//
+// The tensor cores' fp32 sums are truncated, not rounded: 4096 products that add up to 20 come out
+// 8e-5 low. So an accumulator takes 512 products (short calls: 128), and these sums are added up in
+// registers, rounded to nearest, while the next ones run. Entropies of 512 rows, 4096 products a
+// logit, against 64 bits: 1.7e-6 off with one accumulator for all, 1.8e-7 with 512 products, 0.9e-7
+// with 256, which takes 4 % longer where the tensor cores set the time.
 //
 // Alternatives. The k largest logits lie in the k groups with the largest maxima (equal ones by index:
-// an element outside has k elements before it). So the logits are stored, and a row reads k groups of
-// them. Which of two logits is the larger is decided on sums that do not depend on how a kernel
-// accumulates: the kMargin candidates behind the k-th are kept too, and all are summed again as a float
-// and its error (every product of two bf16 is exact in fp32), then ordered by that, ties by index.
+// an element outside has k elements before it). So logits are stored, and a row reads k groups of
+// them: those not below the k-th largest maximum, which are few. Which of two logits is the larger is
+// decided on sums that do not depend on how a kernel accumulates: kLogpMargin candidates behind the
+// last one asked for are kept too, all are summed again in fp32 beside their length, which bounds the
+// sum's error, and those that are nearer to each other than their bounds a third time, as a float
+// and what it lost (every product of two bf16 is exact in fp32). Equal ones go by index.
 //
-// Short calls (up to 64 rows) are bound by HBM: every row of w is read once. 128 rows of w are the M of
-// an MMA, the few rows of h its N. Blocks own equal runs of rows of w (multiples of 16: with whole
-// tiles of 128 the last of seven rounds over 152 SMs would be six tenths full). The tensor cores'
-// fp32 sums are truncated, not rounded (4096 products that add up to 20 come out 8e-5 low); an
-// accumulator takes 256 products here, and these sums are added up in registers, rounded to nearest.
+// Up to 16 rows are bound by HBM: every row of w is read once. 128 rows of w are the M of an MMA, the
+// few rows of h its N. Blocks own equal runs of rows of w (multiples of 16: with whole tiles of 128 the
+// last of seven rounds over 152 SMs would be six tenths full).
+//
+// More rows are bound by HBM up to about 250 and by the tensor cores beyond: 128 x 256 tiles of h and
+// w, persistent blocks. Eight warps hold a tile's sums, 128 columns of a row each; the work on a
+// finished tile runs beside the next one's first 512 products.
 #include <cfloat>
 
 #include "internal.h"
@@ -39,9 +49,18 @@ using Sums = float4;
 
 __device__ __forceinline__ Sums no_sums() { return make_float4(-INFINITY, 0.f, 0.f, 0.f); }
 
-// In memory the last one is logp_mark's word.
+// In memory the last word says how often the maximum occurs and which slices of 32 columns are stored.
+__device__ __forceinline__ float mark(int count, uint32_t stored) {
+  return __uint_as_float(static_cast<uint32_t>(count) | stored << 16);
+}
 __device__ __forceinline__ Sums read_sums(const float4& s) {
   return make_float4(s.x, s.y, s.z, static_cast<float>(__float_as_uint(s.w) & 0xffffu));
+}
+
+// Unsigned numbers in the order of the floats (-0 as +0); 0 is below all of them.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
 // s brought to the maximum m >= s.x, its own maximum among the others where m is larger.
@@ -54,11 +73,12 @@ __device__ __forceinline__ Sums rebase(const Sums& s, float m) {
 
 // ---- short calls ------------------------------------------------------------------------------
 
+constexpr int kChunk = 2;  // stages of 64 products that one accumulator takes
 constexpr int kShortThreads = 192;
-constexpr int kChunk = 4;  // stages of 64 products that one accumulator takes
-constexpr int kAccs = 4;
+constexpr int N = kLogpShortRows;
+static_assert(N == 16, "an MMA's N, and the columns that add_columns loads");
+constexpr int kAccs = 8;
 
-template <int N>
 struct ShortLayout {
   static constexpr int kA = 128 * 128, kB = N * 128, kStage = kA + kB;
   static constexpr int kTile = N * 128 * 4;  // the logits of a tile, [token][column]
@@ -71,39 +91,28 @@ struct ShortLayout {
   static_assert(kBytes <= 227 * 1024, "a block's shared memory");
 };
 
-template <int N>
-__device__ __forceinline__ void add_columns(uint32_t taddr, float (&acc)[N]) {
-  if constexpr (N == 16) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+// x[0 .. 15] += 16 columns of this thread's row of an accumulator
+__device__ __forceinline__ void add_columns(uint32_t taddr, float* x) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-    for (int n = 0; n < 16; ++n) acc[n] += __uint_as_float(r[n]);
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; c += 32) {
-      uint32_t r[32];
-      tmem_ld32_sync(taddr + c, r);
-#pragma unroll
-      for (int n = 0; n < 32; ++n) acc[c + n] += __uint_as_float(r[n]);
-    }
-  }
+  for (int n = 0; n < 16; ++n) x[n] += __uint_as_float(r[n]);
 }
 
 // tm_w: boxes of 128 rows, tm_w16: of 16, tm_h: of N (rows behind the last are zeros).
-template <int N>
 __global__ void __launch_bounds__(kShortThreads, 1)
     logp_short_kernel(const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_w16,
                       const __grid_constant__ CUtensorMap tm_h, const LogpArgs a) {
-  using L = ShortLayout<N>;
+  using L = ShortLayout;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         ok = __all_sync(kAll, wait(acc_full + buf, ph));
         if (!ok) break;
         tc_fence_after();
-        add_columns<N>(tmem + (static_cast<uint32_t>(32 * quarter) << 16) +
+        add_columns(tmem + (static_cast<uint32_t>(32 * quarter) << 16) +
                            static_cast<uint32_t>(buf * N), acc);
         tc_fence_before();
         __syncwarp();
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         }
         if (lane == 0)
           a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] =
-              make_float4(m, sum, sum1, logp_mark(count, 15u));
+              make_float4(m, sum, sum1, mark(count, 15u));
       }
     }
     // groups that this run does not reach
@@ -331,6 +340,272 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ---- longer calls -----------------------------------------------------------------------------
+
+constexpr int kLongThreads = 320;
+constexpr int kLongChunk = 8;  // stages of 64 products that one accumulator takes
+constexpr int kLongGroup = 32;  // M tiles that are walked together: their rows of h stay in L2
+
+struct LongLayout {
+  static constexpr int kA = 128 * 128, kB = 256 * 128, kStage = kA + kB, kStages = 4;
+  static constexpr int kBar = kStages * kStage;
+  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kBytes = kSlot + 16 + 1024;
+};
+
+// Tile t: groups of kLongGroup M tiles, M first.
+__device__ __forceinline__ void long_tile(int64_t t, int m_tiles, int n_tiles, int* mt, int* nt) {
+  const int64_t per = static_cast<int64_t>(kLongGroup) * n_tiles;
+  const int grp = static_cast<int>(div_fl(t, per));
+  const int64_t rem = t - grp * per;
+  const int wide = min(kLongGroup, m_tiles - grp * kLongGroup);
+  *nt = static_cast<int>(div_fl(rem, wide));
+  *mt = grp * kLongGroup + static_cast<int>(rem - static_cast<int64_t>(*nt) * wide);
+}
+
+// Sums, target and wanted logits of 128 columns from col0 on of one row, x.
+// Logits are wanted for the row's `keep` largest alone. Slot g % keep of `best` holds the largest
+// logit of every keep-th group so far, so the smallest of the slots is a bound below which no logit
+// can be among them: a slice of 32 columns below it is not stored (of 4096 x 128256 logits 6 % are, with
+// nine to keep; with all of them stored the call took 0.5 ms more). The bound only grows; an older
+// one stores more, never less.
+__device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int64_t col0,
+                                           uint32_t bound, float (&x)[128]) {
+  if (col0 + 128 > a.V) {
+#pragma unroll
+    for (int j = 0; j < 128; ++j)
+      if (col0 + j >= a.V) x[j] = -INFINITY;
+  }
+  float top[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    top[s] = fmaxf(x[32 * s], x[32 * s + 1]);
+#pragma unroll
+    for (int j = 2; j < 32; j += 2) top[s] = fmax3(top[s], x[32 * s + j], x[32 * s + j + 1]);
+  }
+  const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const int g = static_cast<int>(col0 / kLogpWidth);
+  uint32_t stored = 0;
+  if (a.logits) {
+    atomicMax(a.best + static_cast<int64_t>(g % a.keep) * a.M + row, order_key(mx));
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (col0 + 32 * s >= a.V || order_key(top[s]) < bound) continue;
+      stored |= 1u << s;
+      float4* dst = reinterpret_cast<float4*>(a.logits + row * a.ldl + col0 + 32 * s);
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        dst[v] = make_float4(x[32 * s + 4 * v], x[32 * s + 4 * v + 1], x[32 * s + 4 * v + 2],
+                             x[32 * s + 4 * v + 3]);
+    }
+  }
+  float rest = 0.f, sum1 = 0.f;
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < 128; ++j) {
+    const float d = x[j] - mx;
+    const float e = ex2_approx(d * kLog2e);
+    const bool max = x[j] == mx;
+    rest += max ? 0.f : e;
+    count += max ? 1 : 0;
+    sum1 = fmaf(e, fmaxf(d, -1000.f), sum1);  // d = 0 for the maximum; no 0 * inf for -inf
+  }
+  a.part[row * a.groups + g] = make_float4(mx, rest, sum1, mark(count, stored));
+  if (a.target) {
+    const int64_t k = a.target[row] - col0;
+    if (k >= 0 && k < 128 && col0 + k < a.V) {
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < 128; ++j)  // (written as x[k], or as ?:, it would put x into local memory)
+        asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\tselp.f32 %0, %1, %0, p;\n\t}"
+            : "+f"(v)
+            : "f"(x[j]), "r"(static_cast<int>(k)), "r"(j));
+      a.tlogit[row] = v;
+    }
+  }
+}
+
+// Warp 0 loads, warp 1 multiplies, warps 2 .. 9 add up: warp w holds rows 32 (w % 4) .. + 31 of the tile
+// and its first (w < 6) or second 128 columns. The two accumulators alternate between pieces of
+// kLongChunk stages.
+__global__ void __launch_bounds__(kLongThreads, 1)
+    logp_long_kernel(const __grid_constant__ CUtensorMap tm_h,
+                     const __grid_constant__ CUtensorMap tm_w, const LogpArgs a) {
+  using L = LongLayout;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m_tiles = (a.M + 127) / 128, n_tiles = static_cast<int>((a.V + 255) / 256);
+  const int64_t tiles = static_cast<int64_t>(m_tiles) * n_tiles;
+  const int nk = (a.Dm + 63) / 64;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](uint64_t* br, uint32_t parity) -> bool {
+    if (mbar_try_wait(br, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+      if (mbar_try_wait(br, parity)) return true;
+      if ((n & 31) == 0) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicOr(a.err, kErrWaitTimeout | 0x8000u);
+          return false;
+        }
+      }
+    }
+  };
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_h);
+      tma_prefetch_desc(&tm_w);
+      int s = 0;
+      uint32_t ph = 0;
+      int64_t fills = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        int mt, nt;
+        long_tile(t, m_tiles, n_tiles, &mt, &nt);
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wait(empty + s, ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * L::kStage;
+          mbar_arrive_expect_tx(full + s, L::kStage);
+          tma_load_3d(sa, &tm_h, kb * 64, mt * 128, 0, full + s);
+          tma_load_3d(sa + L::kA, &tm_w, kb * 64, nt * 256, 0, full + s);
+          ++fills;
+          if (++s == L::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        // let the loads still in flight land before the block ends
+        const int64_t first = fills > L::kStages ? fills - L::kStages : 0;
+        for (int64_t f = first; f < fills; ++f)
+          mbar_wait(full + (f % L::kStages), static_cast<uint32_t>((f / L::kStages) & 1),
+                    100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: the whole warp, converged; one lane's products go out ----------------
+    const uint32_t idesc = idesc_bf16(128, 256, false, false);
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t dA0 = kdesc0(s0), dB0 = kdesc0(s0 + L::kA);
+    int s = 0, buf = 0;
+    uint32_t ph = 0, acc_ph = 1;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (int kb = 0; kb < nk; ++kb) {
+        const bool first = kb % kLongChunk == 0;
+        ok = (!first || wait(acc_empty + buf, acc_ph)) && wait(full + s, ph);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tD = tmem + static_cast<uint32_t>(buf * 256);
+        const uint64_t dA = dA0 + s * (L::kStage >> 4), dB = dB0 + s * (L::kStage >> 4);
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16)
+          umma_f16_ss_warp(tD, dA + kstep(k16), dB + kstep(k16), idesc,
+                           !first || k16 > 0 ? 1u : 0u);
+        umma_commit_warp(empty + s);
+        if (++s == L::kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+        if (kb % kLongChunk == kLongChunk - 1 || kb == nk - 1) {
+          umma_commit_warp(acc_full + buf);
+          buf ^= 1;
+          acc_ph ^= buf == 0;
+        }
+      }
+    }
+    if (!ok) {
+      umma_commit_warp(drain);
+      mbar_wait(drain, 0, 100000000ull);
+    }
+  } else {
+    // ---------------- sums ----------------
+    const int quarter = warp & 3, half = warp >= 6;
+    const int chunks = (nk + kLongChunk - 1) / kLongChunk;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128u * half;
+    int buf = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      int mt, nt;
+      long_tile(t, m_tiles, n_tiles, &mt, &nt);
+      const int64_t row = static_cast<int64_t>(mt) * 128 + 32 * quarter + lane;
+      const int64_t col0 = static_cast<int64_t>(nt) * 256 + 128 * half;
+      uint32_t bound = 0xffffffffu;
+      if (a.logits && row < a.M)
+        for (int k = 0; k < a.keep; ++k)
+          bound = min(bound, *static_cast<const volatile uint32_t*>(
+                                 a.best + static_cast<int64_t>(k) * a.M + row));
+      float x[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) x[j] = 0.f;
+      for (int c = 0; c < chunks; ++c) {
+        ok = __all_sync(kAll, wait(acc_full + buf, ph));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          add_columns(mine + static_cast<uint32_t>(buf * 256 + 16 * q), x + 16 * q);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + buf);
+        buf ^= 1;
+        ph ^= buf == 0;
+      }
+      if (ok && row < a.M && col0 < a.V) finish_row(a, row, col0, bound, x);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -350,7 +625,7 @@ __device__ int block_select(Key key, int n, int want, uint32_t least, int* list,
   bool exact = false;
   for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
     __syncthreads();
-    if (threadIdx.x < 256) counts[threadIdx.x] = 0;
+    for (int d = threadIdx.x; d < 256; d += kThreads) counts[d] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint32_t k = key(i);
@@ -420,16 +695,11 @@ __device__ int block_select(Key key, int n, int want, uint32_t least, int* list,
   return found;
 }
 
-// The part of <h, w>, two rows of Dm bf16, that falls to one warp of two (which: 0 or 1; turns of 2048
-// features), with an error near 2^-45 of the terms: each lane keeps its sums and the sums of what each
-// addition lost.
-__device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
-                                            int which) {
-  constexpr int kAhead = 8;  // the rows come from anywhere in w: their vectors are asked for together
-  const int lane = threadIdx.x & 31;
-  float s[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
-  for (int k0 = which * 256 * kAhead + lane * 8; k0 < Dm; k0 += 2 * 256 * kAhead) {
-    uint4 a[kAhead], b[kAhead];
+// Vectors k0, k0 + 256, .. of two rows of Dm bf16, asked for together: the rows come from anywhere in w.
+constexpr int kAhead = 8;
+struct Vectors {
+  uint4 a[kAhead], b[kAhead];
+  __device__ __forceinline__ void load(const __nv_bfloat16* h, const __nv_bfloat16* w, int k0, int Dm) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = k0 + 256 * j;
@@ -439,11 +709,60 @@ __device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_b
         a[j] = *reinterpret_cast<const uint4*>(h + k);
       }
     }
+  }
+};
+
+// <h, w>, <h, h> and <w, w> in fp32, the part that falls to one warp of two (which: 0 or 1; turns of
+// 2048 features).
+__device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
+                                           int which) {
+  uint64_t hw = 0, hh = 0, ww = 0;
+  for (int k0 = which * 256 * kAhead + (threadIdx.x & 31) * 8; k0 < Dm; k0 += 2 * 256 * kAhead) {
+    Vectors v;
+    v.load(h, w, k0, Dm);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const uint32_t x[4] = {v.a[j].x, v.a[j].y, v.a[j].z, v.a[j].w};
+      const uint32_t y[4] = {v.b[j].x, v.b[j].y, v.b[j].z, v.b[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t p = f2_pack_u(x[i] << 16, x[i] & 0xffff0000u);
+        const uint64_t q = f2_pack_u(y[i] << 16, y[i] & 0xffff0000u);
+        hw = ffma2(p, q, hw);
+        hh = ffma2(p, p, hh);
+        ww = ffma2(q, q, ww);
+      }
+    }
+  }
+  float3 r;
+  float lo, hi;
+  f2_unpack(hw, lo, hi);
+  r.x = lo + hi;
+  f2_unpack(hh, lo, hi);
+  r.y = lo + hi;
+  f2_unpack(ww, lo, hi);
+  r.z = lo + hi;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    r.x += __shfl_xor_sync(kAll, r.x, o);
+    r.y += __shfl_xor_sync(kAll, r.y, o);
+    r.z += __shfl_xor_sync(kAll, r.z, o);
+  }
+  return r;
+}
+
+// <h, w> by one warp with an error near 2^-45 of the terms: each lane keeps its sums and the sums of what
+// each addition lost.
+__device__ __forceinline__ double dot_exact(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm) {
+  float s[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
+  for (int k0 = (threadIdx.x & 31) * 8; k0 < Dm; k0 += 256 * kAhead) {
+    Vectors v;
+    v.load(h, w, k0, Dm);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       float x[8], y[8];
-      unpack_bf16x8(a[j], x);
-      unpack_bf16x8(b[j], y);
+      unpack_bf16x8(v.a[j], x);
+      unpack_bf16x8(v.b[j], y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float& u = s[i & 1];
@@ -463,6 +782,8 @@ __device__ __forceinline__ double dot_again(const __nv_bfloat16* h, const __nv_b
   return d;
 }
 
+constexpr int kFew = 128;  // logits of a row that are ranked one against the other
+
 // One block per row. smem: `keep` groups of `width` logits.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
@@ -474,7 +795,11 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   __shared__ int list[32], grp[32], cand[32];
   __shared__ uint32_t grp_least;
   __shared__ float cand_x[32];
-  __shared__ double cand_y[32][2];
+  __shared__ float3 cand_n[32][2];
+  __shared__ double cand_y[32];
+  __shared__ uint32_t near_mask;
+  __shared__ uint32_t few_key[kFew];
+  __shared__ int few_col[kFew], few_n;
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
@@ -556,7 +881,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   // the groups with the largest maxima (one of a run that ends before it has no column), by number
   auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
   uint32_t* keys = reinterpret_cast<uint32_t*>(picked);  // not used yet
-  const bool fits = a.groups <= a.keep * a.width;
+  const bool fits = a.groups <= a.keep * kLogpWidth;
   if (fits)
     for (int g = threadIdx.x; g < a.groups; g += kThreads) keys[g] = group_key(g);
   const int groups = block_select<kThreads>([&](int g) { return fits ? keys[g] : group_key(g); }, a.groups,
@@ -572,87 +897,142 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     }
     least = __reduce_min_sync(kAll, least);
     // with as many groups as are kept, their maxima are as many logits: none below counts
-    if (lane == 0) grp_least = groups == a.keep ? least : 1u;
+    if (lane == 0) {
+      grp_least = groups == a.keep ? least : 1u;
+      few_n = 0;
+    }
   }
   __syncthreads();
+  // their logits from the smallest of these maxima on; columns that were not stored are below it
   const float* x = a.logits + row * a.ldl;
+  const uint32_t least = grp_least;
   for (int k = warp; k < groups; k += kWarps) {
     const int64_t c0 = group_start(a, grp[k]);
     const int n = group_width(a, grp[k]);
-    // columns that were not stored are below as many others
     const uint32_t stored = __float_as_uint(part[grp[k]].w) >> 16;
-    for (int c = lane; c < a.width; c += 32)
-      picked[k * a.width + c] = c < n && (stored >> (c >> 5) & 1) ? x[c0 + c] : NAN;
+    for (int c = lane; c < kLogpWidth; c += 32) {
+      const float v = c < n && (stored >> (c >> 5) & 1) ? x[c0 + c] : NAN;
+      picked[k * kLogpWidth + c] = v;
+      const uint32_t key = order_key(v);
+      if (v == v && key >= least) {
+        const int at = atomicAdd(&few_n, 1);
+        if (at < kFew) {
+          few_key[at] = key;
+          few_col[at] = k * kLogpWidth + c;  // in the order of the columns
+        }
+      }
+    }
   }
   __syncthreads();
-  const int found = block_select<kThreads>(
-      [&](int i) {
-        const float v = picked[i];
-        return v == v ? order_key(v) : 0u;
-      },
-      groups * a.width, a.keep, grp_least, list, counts);
-  if (threadIdx.x < found) {
-    const int i = list[threadIdx.x], k = i / a.width;
-    cand[threadIdx.x] = static_cast<int>(group_start(a, grp[k])) + i - k * a.width;
+  int found = few_n;
+  if (found <= kFew) {
+    for (int i = threadIdx.x; i < few_n; i += kThreads) {
+      const uint32_t key = few_key[i];
+      const int at = few_col[i];
+      int rank = 0;
+      for (int k = 0; k < few_n; ++k) rank += few_key[k] > key || (few_key[k] == key && few_col[k] < at);
+      if (rank < a.keep) list[rank] = at;
+    }
+    found = min(found, a.keep);
+    __syncthreads();
+  } else {
+    found = block_select<kThreads>(
+        [&](int i) {
+          const float v = picked[i];
+          return v == v ? order_key(v) : 0u;
+        },
+        groups * kLogpWidth, a.keep, least, list, counts);
+  }
+  if (threadIdx.x < 32 && static_cast<int>(threadIdx.x) < found) {
+    const int i = list[threadIdx.x], k = i / kLogpWidth;
+    cand[threadIdx.x] = static_cast<int>(group_start(a, grp[k])) + i - k * kLogpWidth;
     cand_x[threadIdx.x] = picked[i];
   }
   __syncthreads();
+  const __nv_bfloat16* h = a.h + row * a.Dm;
   for (int k = warp; k < 2 * found; k += kWarps) {
-    const double y = dot_again(a.h + row * a.Dm,
-                               a.w + static_cast<int64_t>(cand[k >> 1]) * a.Dm, a.Dm, k & 1);
-    if (lane == 0) cand_y[k >> 1][k & 1] = y;
+    const float3 n = dot_near(h, a.w + static_cast<int64_t>(cand[k >> 1]) * a.Dm, a.Dm, k & 1);
+    if (lane == 0) cand_n[k >> 1][k & 1] = n;
   }
   __syncthreads();
+  if (warp == 0) {
+    float v = 0.f, bound = 0.f;
+    if (lane < found) {
+      const float3 n = cand_n[lane][0], o = cand_n[lane][1];
+      v = n.x + o.x;
+      // each of fewer than Dm / 32 + 16 roundings loses at most 2^-24 of the terms' magnitudes, whose sum
+      // is at most the product of the lengths
+      bound = (a.Dm / 32 + 16) * 0x1p-24f * 1.01f * sqrtf(n.y + o.y) * sqrtf(n.z + o.z);
+    }
+    bool near = false;
+    for (int k = 0; k < found; ++k) {
+      const float u = __shfl_sync(kAll, v, k), e = __shfl_sync(kAll, bound, k);
+      // (what is not finite is near everything)
+      if (k != lane && !(fabsf(u - v) > e + bound)) near = true;
+    }
+    const uint32_t all = __ballot_sync(kAll, near && lane < found);
+    if (lane == 0) near_mask = all;
+    cand_y[lane] = v;
+  }
+  __syncthreads();
+  const uint32_t again = near_mask;
+  if (again) {
+    for (int k = warp; k < found; k += kWarps) {
+      if (!(again >> k & 1)) continue;
+      const double y = dot_exact(h, a.w + static_cast<int64_t>(cand[k]) * a.Dm, a.Dm);
+      // where infinities or an overflow leave no sum, the order is that of the logits
+      if (lane == 0) cand_y[k] = fabs(y) <= DBL_MAX ? y : static_cast<double>(cand_x[k]);
+    }
+    __syncthreads();
+  }
   if (threadIdx.x >= 32) return;
   if (lane >= found && lane < a.top) {  // fewer columns than asked for
     out_v[lane] = -INFINITY;
     out_i[lane] = -1;
   }
-  // where infinities or an overflow leave no sum, the order is that of the logits
-  double y = lane < found ? cand_y[lane][0] + cand_y[lane][1] : 0.0;
-  if (!(fabs(y) <= DBL_MAX)) y = static_cast<double>(cand_x[lane]);
-  const int me = lane < found ? cand[lane] : 0;
-  int rank = 0;
-  for (int k = 0; k < found; ++k) {
-    const double z = __shfl_sync(kAll, y, k);
-    const int other = __shfl_sync(kAll, me, k);
-    if (z > y || (z == y && other < me)) ++rank;
-  }
   if (lane >= found) return;
+  const double y = cand_y[lane];
+  const int me = cand[lane];
+  int rank = 0;
+  for (int k = 0; k < found; ++k)
+    if (cand_y[k] > y || (cand_y[k] == y && cand[k] < me)) ++rank;
   if (rank < a.top) {
     out_v[rank] = (cand_x[lane] - m) - ln;
     out_i[rank] = me;
   }
 }
 
-template <int N>
-cudaError_t launch_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
-                         const LogpArgs& a, cudaStream_t stream) {
-  using L = ShortLayout<N>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_short_kernel<N>), L::kBytes);
+}  // namespace
+
+cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
+                              const LogpArgs& a, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_short_kernel),
+                                   ShortLayout::kBytes);
   if (e != cudaSuccess) return e;
   launch_begin(kClass, stream);
-  logp_short_kernel<N><<<static_cast<unsigned>((a.V + a.run - 1) / a.run), kShortThreads, L::kBytes,
-                         stream>>>(tw, tw16, th, a);
+  logp_short_kernel<<<static_cast<unsigned>((a.V + a.run - 1) / a.run), kShortThreads,
+                      ShortLayout::kBytes, stream>>>(tw, tw16, th, a);
   e = cudaGetLastError();
   launch_end(kClass, stream);
   return e;
 }
 
-}  // namespace
-
-int logp_short_box(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
-cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
-                              const LogpArgs& a, cudaStream_t stream) {
-  const int n = logp_short_box(a.M);
-  return n == 16 ? launch_short<16>(tw, tw16, th, a, stream)
-       : n == 32 ? launch_short<32>(tw, tw16, th, a, stream)
-                 : launch_short<64>(tw, tw16, th, a, stream);
+cudaError_t launch_logp_long(const CUtensorMap& th, const CUtensorMap& tw, const LogpArgs& a, int sms,
+                             cudaStream_t stream) {
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_long_kernel),
+                                   LongLayout::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((a.M + 127) / 128) * ((a.V + 255) / 256);
+  launch_begin(kClass, stream);
+  logp_long_kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kLongThreads,
+                     LongLayout::kBytes, stream>>>(th, tw, a);
+  e = cudaGetLastError();
+  launch_end(kClass, stream);
+  return e;
 }
 
 cudaError_t launch_logp_pick(const LogpArgs& a, cudaStream_t stream) {
-  const size_t smem = a.top ? static_cast<size_t>(a.keep) * a.width * 4 : 0;
+  const size_t smem = a.top ? static_cast<size_t>(a.keep) * kLogpWidth * 4 : 0;
   const dim3 grid(static_cast<unsigned>(a.M));
   launch_begin(kClass, stream);
   // Few rows: a whole SM's warps each, for the latency of a row. More: what hides it is other rows.

@@ -10,8 +10,8 @@
 //                  256-column vocabulary tile, the target's logit), then one merge launch;
 //   loss backward: logits GEMM again with the CE_BWD epilogue -> dlogits (bf16, seq_tile x V,
 //                  the only large buffer), dh_tile = dlogits w, dw += dlogits^T h_tile;
-//   log probabilities: logits GEMM with the LOGP epilogue (short tiles: logp.cu's own kernel), then
-//                  one launch that joins a row's groups and picks its alternatives;
+//   log probabilities: logits with each group's sums (logp.cu), then one launch that joins a row's
+//                  groups and picks its alternatives;
 //   MLP forward:   gate/up GEMM with the SWIGLU epilogue -> a (bf16, seq_tile x F), y = a Wd^T;
 //   MLP backward:  the gate/up GEMM again (a, and g | u), da = dy Wd with the DSWIGLU epilogue
 //                  -> dg | du, dWd += dy^T a, dWgu += (dg | du)^T x, dx = (dg | du) [Wg; Wu].
@@ -937,7 +937,7 @@ struct LogpPlan {
   int64_t ldl = 0;           // row pitch of the stored logits
   int keep = 0;              // candidates of a row
   int run = 0, per_run = 0, short_groups = 0;  // of tiles of up to kLogpShortRows rows
-  int groups = 0;            // of longer ones: 256-column tiles
+  int groups = 0;            // of longer ones
   size_t part = 0, tl = 0, logits = 0, best = 0, h[2] = {0, 0}, total = 0;
 };
 
@@ -961,9 +961,9 @@ LogpPlan plan_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile, bool
   p.keep = top + kLogpMargin;
   const int64_t run = (V + kLogpShortBlocks - 1) / kLogpShortBlocks;
   p.run = static_cast<int>((run + 15) / 16 * 16);
-  p.per_run = (p.run + 127) / 128;
+  p.per_run = (p.run + kLogpWidth - 1) / kLogpWidth;
   p.short_groups = static_cast<int>((V + p.run - 1) / p.run) * p.per_run;
-  p.groups = static_cast<int>((V + 255) / 256);
+  p.groups = static_cast<int>((V + kLogpWidth - 1) / kLogpWidth);
   const int64_t few = p.T < kLogpShortRows ? p.T : kLogpShortRows;
   const size_t parts = static_cast<size_t>(p.T) * p.groups,
                few_parts = static_cast<size_t>(few) * p.short_groups;
@@ -1068,37 +1068,21 @@ int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* l
     if (Mc <= kLogpShortRows) {
       a.run = p.run;
       a.per_run = p.per_run;
-      a.width = 128;
       a.groups = p.short_groups;
-      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, logp_short_box(a.M)));
+      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, kLogpShortRows));
       LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 128));
       LOSS_CUDA(make_tmap_bf16(&tw16, w, Dm, V, 1, 16));
       LOSS_CUDA(launch_logp_short(tw, tw16, th, a, stream));
     } else {
-      a.run = a.width = 256;
-      a.per_run = 1;
-      a.groups = p.groups;
+      a.groups = a.per_run = p.groups;
+      a.run = p.groups * kLogpWidth;
       LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, 128));
       LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 256));
-      GemmArgs g{};
-      g.M = a.M;
-      g.N = static_cast<int>(V);
-      g.K = Dm;
-      g.m_fastest = 1;
-      g.group_m = UPIPE_CE_GROUP_M;
-      g.c = a.logits;
-      g.ldc = p.ldl;
-      g.target = a.target;
-      g.part = reinterpret_cast<float*>(a.part);
-      g.part_stride = a.groups;
-      g.tlogit = a.tlogit;
-      g.err = err;
       if (top) {
-        g.best = reinterpret_cast<uint32_t*>(ws + p.best);
-        g.slots = p.keep;
-        LOSS_CUDA(cudaMemsetAsync(g.best, 0, static_cast<size_t>(Mc) * p.keep * 4, stream));
+        a.best = reinterpret_cast<uint32_t*>(ws + p.best);
+        LOSS_CUDA(cudaMemsetAsync(a.best, 0, static_cast<size_t>(Mc) * p.keep * 4, stream));
       }
-      LOSS_CUDA(launch_gemm_tc(kEpiLogp, false, false, th, tw, g, cap, stream));
+      LOSS_CUDA(launch_logp_long(th, tw, a, cap, stream));
     }
     LOSS_CUDA(launch_logp_pick(a, stream));
     return UPIPE_OK;

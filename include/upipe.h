@@ -267,9 +267,9 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  *   top_logp_i: their x - lse.
  * The gradient of sum g_i logp_i is upipe_ce_bwd's for dloss = -g and this lse.
  * Which of two logits is the larger is decided on sums of the exact products with an error near
- * 2^-45 of their magnitudes, whatever the tile; top + 8 candidates are looked at so, those with the
- * largest tensor-core sums. The values are the tensor cores' (fp32; in calls of up to 64 tokens in
- * pieces of 256 products, rounded to nearest between them). A row with a logit of NaN or +inf, or
+ * 2^-45 of their magnitudes, whatever the tile; top + 4 candidates are looked at so, those with the
+ * largest tensor-core sums. The values are the tensor cores' fp32 sums of 128 or 512 products each, added up
+ * rounded to nearest. A row with a logit of NaN or +inf, or
  * without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
  * and -1.
  * Layouts (dense): h [S][Dm], w [V][Dm] bf16; target, top_index [S], [S][top] int64; logp, entropy,
@@ -279,8 +279,8 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * the loss (host_mask = UPIPE_HOST_ACT).
  * Supported: Dm a multiple of 8, any V up to 2^30, top up to 24, seq_tile a multiple of 128. S = 0
  * does nothing. Workspace: upipe_logp_workspace_bytes: for T = min(seq_tile, S) tokens 16 bytes for
- * each token and 256 columns (or, up to 64 tokens, each of the runs' groups of 128), 4 T, and with
- * top > 0 the tile's logits, 4 T V (V rounded up to 32; few of them are written), and 4 T (top + 8);
+ * each token and 128 columns (tiles of up to 16 tokens: each of 152 runs' groups of 128), 4 T, and with
+ * top > 0 the tile's logits, 4 T V (V rounded up to 32; few of them are written), and 4 T (top + 4);
  * each rounded up to 256, plus two slots with UPIPE_HOST_ACT.
  * Results repeat bitwise for the same sizes.
  */

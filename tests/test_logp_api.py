@@ -42,9 +42,9 @@ def test_workspace():
         T = min(S, tile)
         run = -(-(-(-V // 152)) // 16) * 16
         short = -(-V // run) * -(-run // 128)
-        part = max(T * -(-V // 256), min(T, 64) * short) * 16
+        part = max(T * -(-V // 128), min(T, 16) * short) * 16
         want = al(part) + al(4 * T)
-        want += al(4 * T * (-(-V // 32) * 32)) + al(4 * T * (top + 8)) if top else 0
+        want += al(4 * T * (-(-V // 32) * 32)) + al(4 * T * (top + 4)) if top else 0
         want += 2 * al(2 * T * Dm) if host else 0
         assert up.upipe_logp_workspace_bytes(S, Dm, V, top, tile, host) == want
     for bad in ((0, 64, 100, 1, 128), (5, 60, 100, 1, 128), (5, 64, 0, 1, 128), (5, 64, 100, 25, 128),

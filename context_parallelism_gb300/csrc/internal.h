@@ -437,7 +437,7 @@ cudaError_t launch_embed(const int64_t* tokens, const void* w, void* h, int64_t 
 // Sizes and workspace (byte offsets) of the gradient; S >= 1, V < 2^31, host arithmetic.
 struct EmbedPlan {
   int passes, bits;         // of the sort
-  int64_t tiles;            // its blocks
+  int64_t tiles;            // its blocks (0: one block in shared memory)
   int threads, slices;      // of the sums: threads a block, blocks a chunk
   int chunk;                // places a chunk
   int64_t chunks;
@@ -455,7 +455,7 @@ struct EmbedArgs {
   int add;                  // dw is added to (else written whole)
   // set by launch_embed_bwd
   uint32_t* hist;
-  uint32_t* present;        // bitmap of the tokens that occur (not with add)
+  uint32_t* present;        // bitmap of the tokens that occur; NULL: no rows to zero beside the sums
   float* part;              // [chunks][2][Dm]
   int64_t chunks;
   int chunk, slices;

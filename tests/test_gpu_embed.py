@@ -48,7 +48,7 @@ def _check_dw(dw, t, dh, V, scale, before=None):
 
 CASES = [  # places, Dm, V
     (1, 8, 1), (3, 8, 1), (7, 64, 5), (33, 1000, 300), (65, 2056, 17), (129, 8, 70000),
-    (4096, 64, 511), (4097, 32, 512), (5000, 24, 513), (300, 4096, 128256), (9000, 16, 300000),
+    (2048, 64, 511), (4097, 32, 512), (8192, 24, 513), (300, 4096, 128256), (9000, 16, 300000),
     (20000, 8, 1 << 20),
 ]
 
@@ -126,9 +126,11 @@ def test_no_tokens():
     assert (up.embed_backward(none, _bf(9, 8), 5) == 0).all()
 
 
-def test_long_sequence():
-    """More than one run of the scan, runs over many chunks; against index_add in 64 bits."""
-    n, Dm, V = 300001, 16, 40000
+@pytest.mark.parametrize("n,V", [(8192, 3000), (8193, 3000), (300001, 40000), (1100000, 70000)])
+def test_long_sequence(n, V):
+    """Both sides of the border between the sorts, more tiles than a scatter adds up itself, runs over many
+    chunks; against index_add in 64 bits."""
+    Dm = 16
     t, dh = _tokens(n, V, 5, "text").to(DEV), _bf(n, Dm, seed=6)
     dw = up.embed_backward(t, dh, V)
     live = (t >= 0) & (t < V)

@@ -304,3 +304,15 @@ def test_gradient_is_the_losss():
     rh, rw = torch.autograd.grad((p * g * (t >= 0)).sum(), (h64, w64))
     assert (dh.double() - rh).norm() <= 1e-2 * rh.norm()
     assert (dw.double() - rw).norm() <= 1e-2 * rw.norm()
+
+
+def test_short_and_long_calls_agree():
+    """The last tokens of a long call alone: the same logits to the rounding of the pieces' sums, the same
+    alternatives."""
+    h, w, t = _inputs(300, 1024, 3000)
+    a = up.token_logprobs(h, w, t, top=10)
+    b = up.token_logprobs(h[290:].clone(), w, t[290:].clone(), top=10)
+    assert torch.equal(a[4][290:], b[4])
+    ex = torch.from_numpy(_logit_error(h, w)).to(DEV)[290:] * 2 + 2.0 ** -15
+    for i in (0, 2):
+        assert ((a[i][290:] - b[i]).abs().double() <= 2 * ex).all()

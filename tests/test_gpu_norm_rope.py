@@ -352,3 +352,43 @@ def test_raw_entries():
     with pytest.raises(up.UpipeError) as e:
         up.upipe_norm_rope_bwd(*args, workspace_bytes=n - 1)
     assert e.value.status == up.UPIPE_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("B,S,Hq,Hkv,D", [(1, 1, 1, 1, 8), (2, 300, 28, 4, 128), (1, 5000, 5, 1, 80)])
+def test_workspace_bounds(B, S, Hq, Hkv, D):
+    """Exactly the declared bytes, between bands that stay as they are; what they held before does not
+    matter; outputs stay within theirs."""
+    q, k, dy, dz = (_bf(B, S, h, D, seed=i) for i, h in enumerate((Hq, Hkv, Hq, Hkv)))
+    qw, kw = _weights(D, True, 5), _weights(D, True, 6)
+    want = up.norm_rope_backward(dy, dz, q, k, qw, kw)
+    size, band = up.upipe_norm_rope_workspace_bytes(B, S, Hq, Hkv, D), 1 << 16
+    for fill in (0, 255):
+        big = torch.full((size + 2 * band,), fill, dtype=torch.uint8, device=DEV)
+        got = up.norm_rope_backward(dy, dz, q, k, qw, kw, workspace=big[band:band + size])
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert (big[:band] == fill).all() and (big[band + size:] == fill).all()
+    # rows beside the outputs: every second token of a larger tensor
+    x = torch.full((B, 2 * S, Hq, D), 7.0, dtype=BF, device=DEV)
+    x[:, ::2] = q
+    y, _ = up.norm_rope_forward(x[:, ::2], None, qw, None, inplace=True)
+    assert torch.equal(y, up.norm_rope_forward(q, None, qw, None)[0])
+    assert (x[:, 1::2] == 7).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Strides that put a head more than 2^31 elements from the first."""
+    far = (1 << 31) + 8
+    try:
+        x = torch.empty(far + 128, dtype=BF, device=DEV)
+    except torch.OutOfMemoryError:
+        pytest.skip("no room")
+    q = x.as_strided((1, 2, 2, 64), (0, 64, far, 1))
+    q.copy_(_bf(1, 2, 2, 64, seed=1))
+    w, (ph, _) = _weights(64, False, 2), up.rope_phases(64)
+    want = up.norm_rope_forward(q.contiguous(), None, w, None, ph)[0]
+    dy = _bf(1, 2, 2, 64, seed=3)
+    d_want = up.norm_rope_backward(dy, None, q.contiguous(), None, w, None, ph)
+    d = up.norm_rope_backward(dy, None, q, None, w, None, ph)
+    assert torch.equal(d[0], d_want[0]) and torch.equal(d[2], d_want[2])
+    up.norm_rope_forward(q, None, w, None, ph, inplace=True)
+    assert torch.equal(q, want)

@@ -577,10 +577,21 @@ __global__ void __launch_bounds__(kLongThreads, 1)
       const int64_t row = static_cast<int64_t>(mt) * 128 + 32 * quarter + lane;
       const int64_t col0 = static_cast<int64_t>(nt) * 256 + 128 * half;
       uint32_t bound = 0xffffffffu;
-      if (a.logits && row < a.M)
-        for (int k = 0; k < a.keep; ++k)
-          bound = min(bound, *static_cast<const volatile uint32_t*>(
-                                 a.best + static_cast<int64_t>(k) * a.M + row));
+      if (a.logits && row < a.M) {
+        // eight loads at a time: one after the other they would take longer than a piece of the tile
+        for (int k0 = 0; k0 < a.keep; k0 += 8) {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int slot = k0 + k < a.keep ? k0 + k : k0;
+            asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];"
+                         : "=r"(v[k])
+                         : "l"(a.best + static_cast<int64_t>(slot) * a.M + row));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) bound = min(bound, v[k]);
+        }
+      }
       float x[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) x[j] = 0.f;
@@ -713,7 +724,8 @@ struct Vectors {
 };
 
 // <h, w>, <h, h> and <w, w> in fp32, the part that falls to one warp of two (which: 0 or 1; turns of
-// 2048 features).
+// 2048 features). A term of the first is rounded 4 times in its vector, once for each of the lane's
+// vectors (8 a turn) and 6 times across the lanes.
 __device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
                                            int which) {
   uint64_t hw = 0, hh = 0, ww = 0;
@@ -724,14 +736,16 @@ __device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bf
     for (int j = 0; j < kAhead; ++j) {
       const uint32_t x[4] = {v.a[j].x, v.a[j].y, v.a[j].z, v.a[j].w};
       const uint32_t y[4] = {v.b[j].x, v.b[j].y, v.b[j].z, v.b[j].w};
+      uint64_t sum = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t p = f2_pack_u(x[i] << 16, x[i] & 0xffff0000u);
         const uint64_t q = f2_pack_u(y[i] << 16, y[i] & 0xffff0000u);
-        hw = ffma2(p, q, hw);
+        sum = ffma2(p, q, sum);
         hh = ffma2(p, p, hh);
         ww = ffma2(q, q, ww);
       }
+      hw = fadd2(hw, sum);
     }
   }
   float3 r;
@@ -793,36 +807,50 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   __shared__ float row_max, row_ln;
   __shared__ uint32_t counts[256];
   __shared__ int list[32], grp[32], cand[32];
-  __shared__ uint32_t grp_least;
+  __shared__ uint32_t grp_least, last_key, grp_mark[32];
+  __shared__ uint32_t segment[32];
   __shared__ float cand_x[32];
   __shared__ float3 cand_n[32][2];
   __shared__ double cand_y[32];
   __shared__ uint32_t near_mask;
   __shared__ uint32_t few_key[kFew];
-  __shared__ int few_col[kFew], few_n;
+  __shared__ uint32_t few_mark[kFew];
+  __shared__ int few_col[kFew], few_rank[kFew], few_n;
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   const float4* part = a.part + row * a.groups;
 
-  Sums own[kOwn];
-  float m = -INFINITY;
+  // a thread's groups, and the largest of each 32nd group
+  float4 own[kOwn];
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) {
     const int g = threadIdx.x + k * kThreads;
-    own[k] = g < a.groups ? read_sums(part[g]) : no_sums();
+    own[k] = g < a.groups ? part[g] : no_sums();
   }
+  if (threadIdx.x < 32) segment[threadIdx.x] = 0;
+  if (threadIdx.x == 0) few_n = 0;
+  float m = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) m = fmaxf(m, own[k].x);
-  for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads)
-    m = fmaxf(m, part[g].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-  if (lane == 0) red[warp][0] = m;
+  for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads) m = fmaxf(m, part[g].x);
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) m = fmaxf(m, red[k][0]);
+  if (threadIdx.x < a.groups) atomicMax(&segment[lane], order_key(m));
   __syncthreads();
+  uint32_t top_key = segment[lane];
+  if (warp == 0) {
+    // as many groups as are kept have a maximum from the keep-th largest of these on
+    int rank = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const uint32_t u = __shfl_sync(kAll, top_key, k);
+      rank += u > top_key || (u == top_key && k < lane);
+    }
+    static_assert(kLogpMaxTop + kLogpMargin <= 32, "the kept ones, a lane each");
+    if (rank == a.keep - 1) grp_least = max(top_key, 1u);
+  }
+  top_key = __reduce_max_sync(kAll, top_key);
+  m = __uint_as_float(top_key & 0x80000000u ? top_key ^ 0x80000000u : ~top_key);
   float rest = 0.f, sum1 = 0.f, count = 0.f;
   auto add = [&](const Sums& s) {
     const Sums u = rebase(s, m);
@@ -831,7 +859,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     count += u.w;
   };
 #pragma unroll
-  for (int k = 0; k < kOwn; ++k) add(own[k]);
+  for (int k = 0; k < kOwn; ++k) add(read_sums(own[k]));
   for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads) add(read_sums(part[g]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -879,37 +907,67 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   }
 
   // the groups with the largest maxima (one of a run that ends before it has no column), by number
-  auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
-  uint32_t* keys = reinterpret_cast<uint32_t*>(picked);  // not used yet
-  const bool fits = a.groups <= a.keep * kLogpWidth;
-  if (fits)
-    for (int g = threadIdx.x; g < a.groups; g += kThreads) keys[g] = group_key(g);
-  const int groups = block_select<kThreads>([&](int g) { return fits ? keys[g] : group_key(g); }, a.groups,
-                                  a.keep, 1u, list, counts);
-  if (threadIdx.x < 32) {
-    const int mine = lane < groups ? list[lane] : 0x7fffffff;
-    int rank = 0;
-    for (int k = 0; k < groups; ++k) rank += list[k] < mine;
-    uint32_t least = 0xffffffffu;
-    if (lane < groups) {
-      grp[rank] = mine;
-      least = order_key(part[mine].x);
+  auto offer = [&](int g, const float4& p) {
+    const uint32_t key = order_key(p.x);
+    if (g >= a.groups || key < grp_least || group_width(a, g) <= 0) return;
+    const int at = atomicAdd(&few_n, 1);
+    if (at >= kFew) return;
+    few_key[at] = key;
+    few_col[at] = g;
+    few_mark[at] = __float_as_uint(p.w);
+  };
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) offer(threadIdx.x + k * kThreads, own[k]);
+  for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads) offer(g, part[g]);
+  __syncthreads();
+  int groups = few_n;
+  if (groups <= kFew) {
+    // of these, each one's place among the wanted ones by number
+    for (int i = threadIdx.x; i < groups; i += kThreads) {
+      const uint32_t key = few_key[i];
+      const int g = few_col[i];
+      int rank = 0;
+      for (int k = 0; k < groups; ++k) rank += few_key[k] > key || (few_key[k] == key && few_col[k] < g);
+      few_rank[i] = rank;
     }
-    least = __reduce_min_sync(kAll, least);
-    // with as many groups as are kept, their maxima are as many logits: none below counts
-    if (lane == 0) {
-      grp_least = groups == a.keep ? least : 1u;
-      few_n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups; i += kThreads) {
+      if (few_rank[i] >= a.keep) continue;
+      int at = 0;
+      for (int k = 0; k < groups; ++k) at += few_rank[k] < a.keep && few_col[k] < few_col[i];
+      grp[at] = few_col[i];
+      grp_mark[at] = few_mark[i];
+      if (few_rank[i] == a.keep - 1) last_key = few_key[i];
+    }
+    groups = min(groups, a.keep);
+  } else {
+    auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
+    groups = block_select<kThreads>(group_key, a.groups, a.keep, 1u, list, counts);
+    if (threadIdx.x < 32) {
+      const int mine = lane < groups ? list[lane] : 0x7fffffff;
+      int rank = 0;
+      for (int k = 0; k < groups; ++k) rank += list[k] < mine;
+      uint32_t least = 0xffffffffu;
+      if (lane < groups) {
+        grp[rank] = mine;
+        grp_mark[rank] = __float_as_uint(part[mine].w);
+        least = order_key(part[mine].x);
+      }
+      least = __reduce_min_sync(kAll, least);
+      if (lane == 0) last_key = least;
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0) few_n = 0;
+  // with as many groups as are kept, their maxima are as many logits: none below counts
+  const uint32_t least = groups == a.keep ? last_key : 1u;
+  __syncthreads();
   // their logits from the smallest of these maxima on; columns that were not stored are below it
   const float* x = a.logits + row * a.ldl;
-  const uint32_t least = grp_least;
   for (int k = warp; k < groups; k += kWarps) {
     const int64_t c0 = group_start(a, grp[k]);
     const int n = group_width(a, grp[k]);
-    const uint32_t stored = __float_as_uint(part[grp[k]].w) >> 16;
+    const uint32_t stored = grp_mark[k] >> 16;
     for (int c = lane; c < kLogpWidth; c += 32) {
       const float v = c < n && (stored >> (c >> 5) & 1) ? x[c0 + c] : NAN;
       picked[k * kLogpWidth + c] = v;
@@ -960,9 +1018,10 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     if (lane < found) {
       const float3 n = cand_n[lane][0], o = cand_n[lane][1];
       v = n.x + o.x;
-      // each of fewer than Dm / 32 + 16 roundings loses at most 2^-24 of the terms' magnitudes, whose sum
-      // is at most the product of the lengths
-      bound = (a.Dm / 32 + 16) * 0x1p-24f * 1.01f * sqrtf(n.y + o.y) * sqrtf(n.z + o.z);
+      // each rounding loses at most 2^-24 of the terms' magnitudes, whose sum is at most the product of
+      // the lengths (themselves good to 1 % for any Dm)
+      bound = (8 * ((a.Dm + 4095) / 4096) + 12) * 0x1p-24f * 1.01f * sqrtf(n.y + o.y) *
+              sqrtf(n.z + o.z);
     }
     bool near = false;
     for (int k = 0; k < found; ++k) {

@@ -291,21 +291,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const EmbedA
     place[r] = !in ? 0u : kFirst ? static_cast<uint32_t>(i) : places[i];
   }
   // places before this tile's of each digit: two digits a thread (bins: at most 2 kSortThreads)
-  uint32_t at[2], total[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = 2 * threadIdx.x + k;
-    at[k] = total[k] = 0;
-    if (d >= bins) continue;
+  uint32_t at[2] = {0, 0}, total[2] = {0, 0};
+  if (2 * static_cast<int>(threadIdx.x) < bins) {  // (bins is even)
+    const uint2* hist = reinterpret_cast<const uint2*>(a.hist) + threadIdx.x;
+    const int row = bins / 2, self = blockIdx.x;
     if (scanned) {
-      at[k] = a.hist[static_cast<int64_t>(blockIdx.x) * bins + d];
-      continue;
-    }
-#pragma unroll 8
-    for (int t = 0; t < static_cast<int>(gridDim.x); ++t) {
-      const uint32_t c = a.hist[t * bins + d];
-      if (t < static_cast<int>(blockIdx.x)) at[k] += c;
-      total[k] += c;
+      const uint2 c = hist[static_cast<int64_t>(self) * row];
+      at[0] = c.x;
+      at[1] = c.y;
+    } else {
+#pragma unroll 16
+      for (int t = 0; t < static_cast<int>(gridDim.x); ++t) {
+        const uint2 c = hist[t * row];
+        if (t < self) {
+          at[0] += c.x;
+          at[1] += c.y;
+        }
+        total[0] += c.x;
+        total[1] += c.y;
+      }
     }
   }
   if (!scanned) {

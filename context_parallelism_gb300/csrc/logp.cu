@@ -10,10 +10,12 @@
 // (ln z = ln count + ln(1 + rest / count)).
 //
 // The tensor cores' fp32 sums are truncated, not rounded: 4096 products that add up to 20 come out
-// 8e-5 low. So an accumulator takes 512 products (short calls: 128), and these sums are added up in
-// registers, rounded to nearest, while the next ones run. Entropies of 512 rows, 4096 products a
-// logit, against 64 bits: 1.7e-6 off with one accumulator for all, 1.8e-7 with 512 products, 0.9e-7
-// with 256, which takes 4 % longer where the tensor cores set the time.
+// 8e-5 low. So an accumulator takes 512 products, and these sums are added up in registers, rounded to
+// nearest, while the next ones run. Entropies of 512 rows, 4096 products a logit, against 64 bits:
+// 1.7e-6 off with one accumulator for all, 1.8e-7 with 512 products, 0.9e-7 with 256, which takes 4 %
+// longer where the tensor cores set the time. In short calls, where that costs nothing and a single
+// logp near zero may be all that there is, an accumulator takes 64 products, and eight of them are
+// added up before they are added to the others.
 //
 // Alternatives. The k largest logits lie in the k groups with the largest maxima (equal ones by index:
 // an element outside has k elements before it). So logits are stored, and a row reads k groups of
@@ -73,10 +75,10 @@ __device__ __forceinline__ Sums rebase(const Sums& s, float m) {
 
 // ---- short calls ------------------------------------------------------------------------------
 
-constexpr int kChunk = 2;  // stages of 64 products that one accumulator takes
+constexpr int kChunk = 1;  // stages of 64 products that one accumulator takes
 constexpr int kShortThreads = 192;
 constexpr int N = kLogpShortRows;
-static_assert(N == 16, "an MMA's N, and the columns that add_columns loads");
+static_assert(N == 16, "an MMA's N, and the columns that load_columns loads");
 constexpr int kAccs = 8;
 
 struct ShortLayout {
@@ -91,8 +93,8 @@ struct ShortLayout {
   static_assert(kBytes <= 227 * 1024, "a block's shared memory");
 };
 
-// x[0 .. 15] += 16 columns of this thread's row of an accumulator
-__device__ __forceinline__ void add_columns(uint32_t taddr, float* x) {
+// 16 columns of this thread's row of an accumulator
+__device__ __forceinline__ void load_columns(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -104,7 +106,7 @@ __device__ __forceinline__ void add_columns(uint32_t taddr, float* x) {
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int n = 0; n < 16; ++n) x[n] += __uint_as_float(r[n]);
+  for (int n = 0; n < 16; ++n) v[n] = __uint_as_float(r[n]);
 }
 
 // tm_w: boxes of 128 rows, tm_w16: of 16, tm_h: of N (rows behind the last are zeros).
@@ -262,15 +264,25 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
-      float acc[N];
+      float acc[N], few[N];  // sums of eight pieces at a time, and their sum: fewer roundings of large ones
 #pragma unroll
-      for (int n = 0; n < N; ++n) acc[n] = 0.f;
+      for (int n = 0; n < N; ++n) acc[n] = few[n] = 0.f;
       for (int c = 0; ok && c < chunks; ++c) {
         ok = __all_sync(kAll, wait(acc_full + buf, ph));
         if (!ok) break;
         tc_fence_after();
-        add_columns(tmem + (static_cast<uint32_t>(32 * quarter) << 16) +
-                           static_cast<uint32_t>(buf * N), acc);
+        float v[N];
+        load_columns(tmem + (static_cast<uint32_t>(32 * quarter) << 16) +
+                         static_cast<uint32_t>(buf * N), v);
+#pragma unroll
+        for (int n = 0; n < N; ++n) few[n] += v[n];
+        if (c % 8 == 7 || c == chunks - 1) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            acc[n] += few[n];
+            few[n] = 0.f;
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + buf);
@@ -600,8 +612,12 @@ __global__ void __launch_bounds__(kLongThreads, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          add_columns(mine + static_cast<uint32_t>(buf * 256 + 16 * q), x + 16 * q);
+        for (int q = 0; q < 8; ++q) {
+          float v[16];
+          load_columns(mine + static_cast<uint32_t>(buf * 256 + 16 * q), v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[16 * q + j] += v[j];
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + buf);

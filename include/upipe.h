@@ -268,7 +268,7 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * The gradient of sum g_i logp_i is upipe_ce_bwd's for dloss = -g and this lse.
  * Which of two logits is the larger is decided on sums of the exact products with an error near
  * 2^-45 of their magnitudes, whatever the tile; top + 4 candidates are looked at so, those with the
- * largest tensor-core sums. The values are the tensor cores' fp32 sums of 128 or 512 products each, added up
+ * largest tensor-core sums. The values are the tensor cores' fp32 sums of 64 or 512 products each, added up
  * rounded to nearest. A row with a logit of NaN or +inf, or
  * without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
  * and -1.

@@ -164,9 +164,10 @@ def test_probabilities_near_one(S):
         assert lse[0].item() == pytest.approx(gap + math.log1p(q), rel=2.0 ** -20)
 
 
+@pytest.mark.parametrize("Dm", [64, 1200])
 @pytest.mark.parametrize("S", [9, 90])
-def test_values_that_are_not_finite(S):
-    h, w, t = _inputs(S, 64, 700)
+def test_values_that_are_not_finite(S, Dm):
+    h, w, t = _inputs(S, Dm, 700)
     t = t.clamp(min=0)
     good = up.token_logprobs(h, w, t, top=3)
     h2 = h.clone()

@@ -723,7 +723,7 @@ __device__ int block_select(Key key, int n, int want, uint32_t least, int* list,
 }
 
 // Vectors k0, k0 + 256, .. of two rows of Dm bf16, asked for together: the rows come from anywhere in w.
-constexpr int kAhead = 8;
+constexpr int kAhead = 4;
 struct Vectors {
   uint4 a[kAhead], b[kAhead];
   __device__ __forceinline__ void load(const __nv_bfloat16* h, const __nv_bfloat16* w, int k0, int Dm) {
@@ -740,8 +740,8 @@ struct Vectors {
 };
 
 // <h, w>, <h, h> and <w, w> in fp32, the part that falls to one warp of two (which: 0 or 1; turns of
-// 2048 features). A term of the first is rounded 4 times in its vector, once for each of the lane's
-// vectors (8 a turn) and 6 times across the lanes.
+// 256 kAhead features). A term of the first is rounded 4 times in its vector, once for each of the
+// lane's vectors (kAhead a turn) and 7 times across lanes and warps.
 __device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
                                            int which) {
   uint64_t hw = 0, hh = 0, ww = 0;
@@ -781,11 +781,12 @@ __device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bf
   return r;
 }
 
-// <h, w> by one warp with an error near 2^-45 of the terms: each lane keeps its sums and the sums of what
-// each addition lost.
-__device__ __forceinline__ double dot_exact(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm) {
+// The same part of <h, w> with an error near 2^-45 of the terms: each lane keeps its sums and the sums of
+// what each addition lost.
+__device__ __forceinline__ double dot_exact(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
+                                            int which) {
   float s[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
-  for (int k0 = (threadIdx.x & 31) * 8; k0 < Dm; k0 += 256 * kAhead) {
+  for (int k0 = which * 256 * kAhead + (threadIdx.x & 31) * 8; k0 < Dm; k0 += 2 * 256 * kAhead) {
     Vectors v;
     v.load(h, w, k0, Dm);
 #pragma unroll
@@ -827,7 +828,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   __shared__ uint32_t segment[32];
   __shared__ float cand_x[32];
   __shared__ float3 cand_n[32][2];
-  __shared__ double cand_y[32];
+  __shared__ double cand_y[32], cand_e[32][2];
   __shared__ uint32_t near_mask;
   __shared__ uint32_t few_key[kFew];
   __shared__ uint32_t few_mark[kFew];
@@ -1036,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
       v = n.x + o.x;
       // each rounding loses at most 2^-24 of the terms' magnitudes, whose sum is at most the product of
       // the lengths (themselves good to 1 % for any Dm)
-      bound = (8 * ((a.Dm + 4095) / 4096) + 12) * 0x1p-24f * 1.01f * sqrtf(n.y + o.y) *
+      bound = (kAhead * ((a.Dm + 512 * kAhead - 1) / (512 * kAhead)) + 12) * 0x1p-24f * 1.01f * sqrtf(n.y + o.y) *
               sqrtf(n.z + o.z);
     }
     bool near = false;
@@ -1052,13 +1053,19 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   __syncthreads();
   const uint32_t again = near_mask;
   if (again) {
-    for (int k = warp; k < found; k += kWarps) {
-      if (!(again >> k & 1)) continue;
-      const double y = dot_exact(h, a.w + static_cast<int64_t>(cand[k]) * a.Dm, a.Dm);
-      // where infinities or an overflow leave no sum, the order is that of the logits
-      if (lane == 0) cand_y[k] = fabs(y) <= DBL_MAX ? y : static_cast<double>(cand_x[k]);
+    const int n = __popc(again);
+    for (int k = warp; k < 2 * n; k += kWarps) {
+      const int c = __fns(again, 0, (k >> 1) + 1);
+      const double y = dot_exact(h, a.w + static_cast<int64_t>(cand[c]) * a.Dm, a.Dm, k & 1);
+      if (lane == 0) cand_e[c][k & 1] = y;
     }
     __syncthreads();
+    if (threadIdx.x < 32 && (again >> lane & 1)) {
+      const double y = cand_e[lane][0] + cand_e[lane][1];
+      // where infinities or an overflow leave no sum, the order is that of the logits
+      cand_y[lane] = fabs(y) <= DBL_MAX ? y : static_cast<double>(cand_x[lane]);
+    }
+    __syncwarp();
   }
   if (threadIdx.x >= 32) return;
   if (lane >= found && lane < a.top) {  // fewer columns than asked for

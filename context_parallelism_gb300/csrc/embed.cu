@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kEmbedClass = 17;
 constexpr int kTile = 2048;  // places of a sort block
-constexpr int kFewTiles = 512;
+constexpr int kFewTiles = 96;  // (512 tiles, 2^20 places: 352 us, 400 where each block adds them up)
 constexpr int kSortThreads = 256;
 constexpr int kRounds = kTile / kSortThreads;
 constexpr int kWarps = kSortThreads / 32;
@@ -243,26 +243,36 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const EmbedArg
     a.hist[static_cast<int64_t>(blockIdx.x) * bins + d] = count[d];
 }
 
-// With many tiles: hist[tile][digit] becomes the places before (tile, digit) in the order of digits
-// and tiles. One block, a thread a digit.
-__global__ void __launch_bounds__(kMaxBins) sort_scan_kernel(uint32_t* hist, int64_t tiles, int bins) {
-  __shared__ uint32_t warp_sum[32];
+// With many tiles: hist[tile][digit] becomes the places before the tile of that digit, and hist[tiles] the
+// digits' totals. A block takes 16 digits, 16 threads each with a run of the tiles.
+__global__ void __launch_bounds__(256) sort_scan_kernel(uint32_t* hist, int64_t tiles, int bins) {
+  __shared__ uint32_t sum[16][16];
   launch_dependents();
   grid_dependency_wait();
-  const int d = threadIdx.x;
+  const int d = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+  const int64_t per = (tiles + 15) / 16, lo = part * per, hi = lo + per < tiles ? lo + per : tiles;
   uint32_t total = 0;
   if (d < bins) {
 #pragma unroll 8
-    for (int64_t t = 0; t < tiles; ++t) total += hist[t * bins + d];
+    for (int64_t t = lo; t < hi; ++t) total += hist[t * bins + d];
   }
-  uint32_t at = block_before(total, warp_sum);
+  sum[part][threadIdx.x & 15] = total;
+  __syncthreads();
   if (d >= bins) return;
+  uint32_t at = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t c = sum[k][threadIdx.x & 15];
+    if (k < part) at += c;
+    all += c;
+  }
 #pragma unroll 8
-  for (int64_t t = 0; t < tiles; ++t) {
+  for (int64_t t = lo; t < hi; ++t) {
     const uint32_t c = hist[t * bins + d];
     hist[t * bins + d] = at;
     at += c;
   }
+  if (part == 0) hist[tiles * bins + d] = all;
 }
 
 template <bool kFirst>
@@ -296,9 +306,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const EmbedA
     const uint2* hist = reinterpret_cast<const uint2*>(a.hist) + threadIdx.x;
     const int row = bins / 2, self = blockIdx.x;
     if (scanned) {
-      const uint2 c = hist[static_cast<int64_t>(self) * row];
+      const uint2 c = hist[static_cast<int64_t>(self) * row], all = hist[static_cast<int64_t>(gridDim.x) * row];
       at[0] = c.x;
       at[1] = c.y;
+      total[0] = all.x;
+      total[1] = all.y;
     } else {
 #pragma unroll 16
       for (int t = 0; t < static_cast<int>(gridDim.x); ++t) {
@@ -312,11 +324,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const EmbedA
       }
     }
   }
-  if (!scanned) {
-    const uint32_t start = block_before(total[0] + total[1], warp_sum);
-    at[0] += start;
-    at[1] += start + total[0];
-  }
+  const uint32_t start = block_before(total[0] + total[1], warp_sum);
+  at[0] += start;
+  at[1] += start + total[0];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) digit[r] = (key[r] >> shift) & (bins - 1);
   const int64_t left = a.S - base;
@@ -500,7 +510,7 @@ EmbedPlan plan_embed(int64_t S, int Dm, int64_t V) {
     p.keys[i] = take(static_cast<size_t>(S) * 4);
     p.places[i] = take(static_cast<size_t>(S) * 4);
   }
-  p.hist = take(static_cast<size_t>(p.tiles) * (size_t(1) << p.bits) * 4);
+  p.hist = take(static_cast<size_t>(p.tiles + 1) * (size_t(1) << p.bits) * 4);
   p.present = take(static_cast<size_t>((V + 31) / 32) * 4);
   p.part = take(static_cast<size_t>(p.chunks) * 2 * Dm * 4);
   p.total = off;
@@ -563,7 +573,7 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
         launch(sort_count_kernel<true>, p.tiles, kSortThreads, 0, false, a, k, shift, bins);
       else
         launch(sort_count_kernel<false>, p.tiles, kSortThreads, 0, true, a, k, shift, bins);
-      if (scanned) launch(sort_scan_kernel, 1, kMaxBins, 0, true, a.hist, p.tiles, bins);
+      if (scanned) launch(sort_scan_kernel, (bins + 15) / 16, 256, 0, true, a.hist, p.tiles, bins);
       if (pass == 0)
         launch(sort_scatter_kernel<true>, p.tiles, kSortThreads, 0, true, a, k, pl, keys[in ^ 1],
                places[in ^ 1], shift, p.bits, scanned);

@@ -48,7 +48,7 @@ def test_workspace():
     two partial rows for each chunk of 8 places or more."""
     ws = up.upipe_embed_workspace_bytes
     for S, Dm, V in [(1, 8, 1), (4097, 1000, 32003), (131072, 4096, 128256), (1 << 20, 512, 1 << 20)]:
-        tiles = -(-S // 4096)
+        tiles = -(-S // 2048) + 1
         most = 16 * S + tiles * 512 * 4 + V // 8 + 4 + -(-S // 8) * 2 * Dm * 4 + 7 * 256
         assert 16 * S < ws(S, Dm, V) <= most
     assert ws(131072, 4096, 128256) < 80 << 20

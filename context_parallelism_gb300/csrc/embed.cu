@@ -18,8 +18,9 @@
 // Sort: a stable radix sort of 32-bit tokens with their places, in passes of up to 9 bits (17 bits of
 // vocabulary: 2 passes). A place's rank in its block: warps count 32 places at a time, matching equal
 // digits by ballots. Up to kSmall places one block sorts in shared memory (beside it, where the whole
-// table is small, other blocks write its zeros). More places: two launches a pass, histograms of 2048 places and scatter, each scatter block adding up the histograms before it
-// (with more than kFewTiles blocks a launch between does that).
+// table is small, other blocks write its zeros). More places: two launches a pass, histograms of 2048
+// places and scatter, each scatter block adding up the histograms before it (with more than kFewTiles
+// blocks a launch between does that).
 #include "internal.h"
 #include "rope.cuh"
 
@@ -449,8 +450,12 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const
   }
 }
 
-// One block for each chunk in which a run begins that goes on: its partial sums in order.
-__global__ void __launch_bounds__(128) embed_join_kernel(const EmbedArgs a, const uint32_t* keys) {
+// One block for each chunk in which a run begins that goes on: its partial sums, kJoin runs of chunks one
+// beside the other (a token that fills a tenth of a long sequence has hundreds), then these in order.
+constexpr int kJoin = 4;
+__global__ void __launch_bounds__(128 * kJoin) embed_join_kernel(const EmbedArgs a,
+                                                                 const uint32_t* keys) {
+  __shared__ float4 sums[kJoin - 1][2][128];
   launch_dependents();
   grid_dependency_wait();
   const int64_t chunk = blockIdx.x / a.slices;
@@ -466,17 +471,33 @@ __global__ void __launch_bounds__(128) embed_join_kernel(const EmbedArgs a, cons
     const int64_t i = (last + 1 + threadIdx.x) * a.chunk;
     more = __syncthreads_count(i < a.S && keys[i] == k);
   }
-  const int f = (slice * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-  if (f >= a.Dm) return;
+  const int threads = blockDim.x / kJoin, part = threadIdx.x / threads,
+            col = threadIdx.x - part * threads;
+  const int f = (slice * threads + col) * 8;
+  const bool in = f < a.Dm;
+  const int64_t per = (last - chunk + kJoin) / kJoin;  // partial sums of a part, the chunk's own first
+  const int64_t from = chunk + part * per, to = from + per - 1 < last ? from + per - 1 : last;
   float s[8];
-  const float4* first = reinterpret_cast<const float4*>(part_at(a, chunk, 1, f));
-  const float4 u = first[0], v = first[1];
-  s[0] = u.x; s[1] = u.y; s[2] = u.z; s[3] = u.w;
-  s[4] = v.x; s[5] = v.y; s[6] = v.z; s[7] = v.w;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  if (in) {
 #pragma unroll 8
-  for (int64_t c = chunk + 1; c <= last; ++c) {
-    const float4* p = reinterpret_cast<const float4*>(part_at(a, c, 0, f));
-    const float4 x = p[0], y = p[1];
+    for (int64_t c = from; c <= to; ++c) {
+      const float4* p = reinterpret_cast<const float4*>(part_at(a, c, c == chunk ? 1 : 0, f));
+      const float4 x = p[0], y = p[1];
+      s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+      s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+    }
+    if (part > 0) {
+      sums[part - 1][0][col] = make_float4(s[0], s[1], s[2], s[3]);
+      sums[part - 1][1][col] = make_float4(s[4], s[5], s[6], s[7]);
+    }
+  }
+  __syncthreads();
+  if (part > 0 || !in) return;
+#pragma unroll
+  for (int p = 0; p < kJoin - 1; ++p) {
+    const float4 x = sums[p][0][col], y = sums[p][1][col];
     s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
     s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
   }
@@ -585,7 +606,7 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
   const int64_t zero = a.present ? (a.V + kZeroRows - 1) / kZeroRows : 0;
   const uint32_t *k = keys[in], *pl = places[in];
   launch(embed_sum_kernel, p.chunks * p.slices + zero, p.threads, 0, true, a, k, pl);
-  if (p.chunks > 1) launch(embed_join_kernel, p.chunks * p.slices, p.threads, 0, true, a, k);
+  if (p.chunks > 1) launch(embed_join_kernel, p.chunks * p.slices, p.threads * kJoin, 0, true, a, k);
   return e;
 }
 

@@ -843,8 +843,8 @@ int check_embed(int64_t S, int Dm, int64_t V, double scale) {
   if (S < 0 || Dm < 1 || V < 1)
     return lfail(UPIPE_ERR_INVALID_ARG, "S=%lld Dm=%d V=%lld", (long long)S, Dm, (long long)V);
   if (!std::isfinite(scale)) return lfail(UPIPE_ERR_INVALID_ARG, "scale must be finite");
-  if (Dm % 8 || S > (int64_t(1) << 30) || V >= (int64_t(1) << 31))
-    return lfail(UPIPE_ERR_UNSUPPORTED, "need Dm %% 8 == 0, S <= 2^30, V < 2^31");
+  if (Dm % 8 || Dm > (1 << 24) || S > (int64_t(1) << 30) || V >= (int64_t(1) << 31))
+    return lfail(UPIPE_ERR_UNSUPPORTED, "need Dm %% 8 == 0, Dm <= 2^24, S <= 2^30, V < 2^31");
   // blocks of one launch: the places' chunks and the rows that are zeroed
   const EmbedPlan p = plan_embed(S < 1 ? 1 : S, Dm, V);
   if (p.chunks * p.slices + V / 16 + 1 > 0x7fffffff ||

@@ -17,7 +17,7 @@ def _bwd(token=FAKE, dh=FAKE, dw=FAKE, S=5, Dm=64, V=100, scale=1.0, add=0, ws=F
     return up._lib.upipe_embed_bwd(token, dh, dw, S, Dm, V, scale, add, ws, wb, None)
 
 
-SIZES = [(dict(S=-1), INV), (dict(Dm=0), INV), (dict(V=0), INV), (dict(Dm=60), UNS),
+SIZES = [(dict(S=-1), INV), (dict(Dm=0), INV), (dict(V=0), INV), (dict(Dm=60), UNS), (dict(Dm=(1 << 24) + 8), UNS),
          (dict(S=(1 << 30) + 1), UNS), (dict(V=1 << 31), UNS), (dict(scale=float("nan")), INV),
          (dict(scale=float("inf")), INV), (dict(S=1 << 30, Dm=1 << 20), UNS),
          (dict(token=None), INV), (dict(token=FAKE + 4), INV), (dict(), INV)]  # no device memory

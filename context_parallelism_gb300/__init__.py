@@ -684,7 +684,7 @@ def token_logprobs(h, w, target=None, top=0, seq_tile=4096, workspace=None, stre
     None: logp is None), the entropy, the log of the sum of the exponentials, and the `top` most
     likely tokens with theirs (None, None for top = 0), seq_tile tokens at a time. h may be a pinned
     host tensor (staged tile by tile). The gradient of sum g * logp: ce_loss_backward with
-    dloss = -g and this lse."""
+    dloss = -g and this lse. With top the workspace holds a tile's logits (seq_tile * V * 4 bytes)."""
     torch = _torch or _lazy_torch()
     f32, i64 = torch.float32, torch.int64
     if len(_matrix(h, "h", torch.bfloat16)) != 2 or len(_matrix(w, "w", torch.bfloat16)) != 2 or \
@@ -839,23 +839,16 @@ def _phases(phases):
     return 2 * phases.shape[0]
 
 
-def _q_or_k(q, k):
-    """B, S, D of the tensors that are there."""
+def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
+    torch = _torch or _lazy_torch()
     ref = q if q is not None else k
     if ref is None or ref.dim() != 4:
         raise ValueError("q and k must be [B, S, heads, D] (one may be None)")
-    B, S, _, D = ref.shape
+    B, S, _, D = shape = ref.shape
     if k is not None and k is not ref:
         ks = k.shape
         if len(ks) != 4 or ks[0] != B or ks[1] != S or ks[3] != D:
             raise ValueError("q and k must agree in B, S and D")
-    return ref, B, S, D
-
-
-def _rope(fn, where, q, k, phases, mscale, interleaved, positions, start, inplace, stream):
-    torch = _torch or _lazy_torch()
-    ref, B, S, D = _q_or_k(q, k)
-    shape = ref.shape
     pos = None
     if positions is not None:
         _dense(positions, torch.int64, shape[:2], "positions")
@@ -929,6 +922,19 @@ def _rotation(phases, positions, lead):
     if phases is None:
         return 0, None, pos
     return _phases(phases), phases.data_ptr(), pos
+
+
+def _q_or_k(q, k):
+    """B, S, D of the tensors that are there."""
+    ref = q if q is not None else k
+    if ref is None or ref.dim() != 4:
+        raise ValueError("q and k must be [B, S, heads, D] (one may be None)")
+    B, S, _, D = ref.shape
+    if k is not None and k is not ref:
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != B or ks[1] != S or ks[3] != D:
+            raise ValueError("q and k must agree in B, S and D")
+    return ref, B, S, D
 
 
 def norm_rope_forward(q, k, q_weight, k_weight, phases=None, mscale=1.0, eps=1e-6, offset=0.0,

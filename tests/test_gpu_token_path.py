@@ -162,3 +162,48 @@ def test_prefill_and_decode(packed):
         assert (logp.double() - p[:, i].gather(1, text[:, i:i + 1])[:, 0]).abs().max() <= 2 * off
         assert (top.double() - p[:, i].gather(1, index)).abs().max() <= 2 * off
         assert (top[:, :-1] >= top[:, 1:] - 1e-5).all()
+
+
+def test_two_threads():
+    """Calls from two threads at once, each on a stream of its own."""
+    import threading
+
+    m = _model(2)
+    ph, _ = up.rope_phases(D)
+    want, got, errors = [], [None, None], []
+
+    def work(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        t = torch.randint(-1, V, (3000,), generator=g, device=DEV)
+        x = up.embed_forward(t, m["w"], scale=2.0)
+        q = x.view(1, 3000, Dm // D, D)
+        y, _ = up.norm_rope_forward(q, None, m["qn"], None, ph, start=seed)
+        dx, _, dw, _ = up.norm_rope_backward(y, None, q, None, m["qn"], None, ph, start=seed)
+        table = up.embed_backward(t, dx.view(3000, Dm), V, scale=2.0)
+        out = up.token_logprobs(y.view(3000, Dm), m["w"], t, top=5)
+        few = up.token_logprobs(y.view(3000, Dm)[:3].clone(), m["w"], t[:3].clone(), top=5)
+        return [x, y, dx, dw, table, *out, *few]
+
+    for seed in (0, 1):
+        want.append(work(seed))
+    torch.cuda.synchronize()
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i] = work(i)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in (0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
+    up.upipe_sync_status()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -463,10 +463,10 @@ struct EmbedArgs {
 cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaStream_t stream);
 
 // ---- token log probabilities (logp.cu) --------------------------------------------------------
-// Rows [0, M) of one tile of a call. The logits' columns come in `groups` groups: `per_run` in each run
-// of `run` columns, kLogpWidth columns in a group (fewer at a run's end).
+// Rows [0, M) of one tile of a call. The logits' columns come in `groups` groups: of kLogpWidth up to
+// `full`, of `rest` behind.
 constexpr int kLogpShortRows = 16;    // rows of a tile that the kernel for short calls takes at most
-constexpr int kLogpShortBlocks = 152;
+constexpr int kLogpBlocks = 152;      // of that kernel
 constexpr int kLogpMargin = 4;        // candidates kept behind the last alternative
 constexpr int kLogpMaxTop = 24;
 
@@ -482,22 +482,22 @@ struct LogpArgs {
   int64_t* top_index;
   int M, Dm, top, keep;
   int64_t V;
-  int groups, per_run, run;
+  int64_t full;                // a multiple of kLogpWidth
+  int groups, rest;            // rest: a multiple of 16, at most kLogpWidth
   uint32_t* best;              // longer tiles with logits: [keep][M], see logp.cu
   uint32_t* err;
 };
 constexpr int kLogpWidth = 128;  // columns of a group
 __host__ __device__ inline int64_t group_start(const LogpArgs& a, int g) {
-  const int r = g / a.per_run;
-  return static_cast<int64_t>(r) * a.run + static_cast<int64_t>(g - r * a.per_run) * kLogpWidth;
+  const int whole = static_cast<int>(a.full / kLogpWidth);
+  return g < whole ? static_cast<int64_t>(g) * kLogpWidth
+                   : a.full + static_cast<int64_t>(g - whole) * a.rest;
 }
-// Columns of a group (0 or less: none).
+// Columns of a group: 1 or more.
 __host__ __device__ inline int group_width(const LogpArgs& a, int g) {
-  const int64_t c = group_start(a, g);
-  const int64_t in_run = a.run - static_cast<int64_t>(g % a.per_run) * kLogpWidth;
-  int64_t n = in_run < kLogpWidth ? in_run : kLogpWidth;
-  if (a.V - c < n) n = a.V - c;
-  return static_cast<int>(n);
+  const int64_t c = group_start(a, g), left = a.V - c;
+  const int n = c < a.full ? kLogpWidth : a.rest;
+  return left < n ? static_cast<int>(left) : n;
 }
 // Logits and groups of up to kLogpShortRows rows. Maps of w with boxes of 128 and of 16 rows, of h with
 // one of kLogpShortRows.

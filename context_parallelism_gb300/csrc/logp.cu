@@ -26,8 +26,11 @@
 // and what it lost (every product of two bf16 is exact in fp32). Equal ones go by index.
 //
 // Up to 16 rows are bound by HBM: every row of w is read once. 128 rows of w are the M of an MMA, the
-// few rows of h its N. Blocks own equal runs of rows of w (multiples of 16: with whole tiles of 128 the
-// last of seven rounds over 152 SMs would be six tenths full).
+// few rows of h its N. Each round of the 152 blocks takes the next 152 tiles; the last, which would be
+// six tenths full at 128256 rows, has tiles of an equal, smaller multiple of 16 rows. (One contiguous
+// run of rows for each block, which balances them as well, takes 4 us longer: 187 against 183 for one
+// token, five alternatives. For 17 to 128 tokens, whose last round is 45 tiles of 256 on 152 SMs, a
+// shorter last round takes 10 us longer, 179 against 170: its stages hold less of w for the same h.)
 //
 // More rows are bound by HBM up to about 250 and by the tensor cores beyond: 128 x 256 tiles of h and
 // w, persistent blocks. Eight warps hold a tile's sums, 128 columns of a row each; the work on a
@@ -129,9 +132,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   constexpr uint32_t kCols = kAccs * N;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t v_lo = static_cast<int64_t>(blockIdx.x) * a.run;
-  const int rows = static_cast<int>(a.V - v_lo < a.run ? a.V - v_lo : a.run);
-  const int tiles = (rows + 127) / 128;
+  const int tiles = a.groups;
   const int nk = (a.Dm + 63) / 64;
 
   if (threadIdx.x == 0) {
@@ -180,9 +181,9 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       uint32_t ph = 0;
       int64_t fills = 0;
       bool ok = true;
-      for (int t = 0; ok && t < tiles; ++t) {
-        const int left = rows - 128 * t, y0 = static_cast<int>(v_lo) + 128 * t;
-        // rows behind the run's last keep what the stage held: their results are not used
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const int left = group_width(a, t), y0 = static_cast<int>(group_start(a, t));
+        // rows behind the tile's last keep what the stage held: their results are not used
         const int boxes = left >= 128 ? 0 : (left + 15) / 16;
         const uint32_t bytes = (boxes ? boxes * 2048u : 16384u) + L::kB;
         for (int kb = 0; kb < nk; ++kb) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       int s = 0, buf = 0;
       uint32_t ph = 0, acc_ph = 1;
       bool ok = true;
-      for (int t = 0; ok && t < tiles; ++t) {
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         for (int kb = 0; kb < nk; ++kb) {
           const bool first = kb % kChunk == 0;
           if ((first && !wait(acc_empty + buf, acc_ph)) || !wait(full + s, ph)) {
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     int buf = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       float acc[N], few[N];  // sums of eight pieces at a time, and their sum: fewer roundings of large ones
 #pragma unroll
       for (int n = 0; n < N; ++n) acc[n] = few[n] = 0.f;
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         tile[n * 128 + r] = acc[n];
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      const int left = rows - 128 * t;  // columns of this tile, and more
-      const int64_t col = v_lo + 128 * t + 4 * lane;
+      const int left = group_width(a, t);
+      const int64_t col = group_start(a, t) + 4 * lane;
 #pragma unroll 2
       for (int n = quarter; n < a.M; n += 4) {
         float4 v = reinterpret_cast<const float4*>(tile + n * 128)[lane];
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         if (4 * lane + 1 >= left) v.y = -INFINITY;
         if (4 * lane + 2 >= left) v.z = -INFINITY;
         if (4 * lane + 3 >= left) v.w = -INFINITY;
-        // (a run's columns are a multiple of 16, or end the padded row)
+        // (a tile's columns are a multiple of 16, or end the padded row)
         if (a.logits && 4 * lane < left) *reinterpret_cast<float4*>(a.logits + n * a.ldl + col) = v;
         const float x[4] = {v.x, v.y, v.z, v.w};
         if (a.target) {
@@ -337,14 +338,9 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           sum1 += __shfl_xor_sync(kAll, sum1, o);
         }
         if (lane == 0)
-          a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] =
-              make_float4(m, sum, sum1, mark(count, 15u));
+          a.part[static_cast<int64_t>(n) * a.groups + t] = make_float4(m, sum, sum1, mark(count, 15u));
       }
     }
-    // groups that this run does not reach
-    for (int t = tiles; t < a.per_run; ++t)
-      for (int n = threadIdx.x - 64; n < a.M; n += 128)
-        a.part[static_cast<int64_t>(n) * a.groups + blockIdx.x * a.per_run + t] = no_sums();
   }
 
   tc_fence_before();
@@ -923,10 +919,10 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     return;
   }
 
-  // the groups with the largest maxima (one of a run that ends before it has no column), by number
+  // the groups with the largest maxima, by number
   auto offer = [&](int g, const float4& p) {
     const uint32_t key = order_key(p.x);
-    if (g >= a.groups || key < grp_least || group_width(a, g) <= 0) return;
+    if (g >= a.groups || key < grp_least) return;
     const int at = atomicAdd(&few_n, 1);
     if (at >= kFew) return;
     few_key[at] = key;
@@ -958,7 +954,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     }
     groups = min(groups, a.keep);
   } else {
-    auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
+    auto group_key = [&](int g) { return order_key(part[g].x); };
     groups = block_select<kThreads>(group_key, a.groups, a.keep, 1u, list, counts);
     if (threadIdx.x < 32) {
       const int mine = lane < groups ? list[lane] : 0x7fffffff;
@@ -1092,8 +1088,8 @@ cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, co
                                    ShortLayout::kBytes);
   if (e != cudaSuccess) return e;
   launch_begin(kClass, stream);
-  logp_short_kernel<<<static_cast<unsigned>((a.V + a.run - 1) / a.run), kShortThreads,
-                      ShortLayout::kBytes, stream>>>(tw, tw16, th, a);
+  const int blocks = a.groups < kLogpBlocks ? a.groups : kLogpBlocks;  // a tile is a group
+  logp_short_kernel<<<blocks, kShortThreads, ShortLayout::kBytes, stream>>>(tw, tw16, th, a);
   e = cudaGetLastError();
   launch_end(kClass, stream);
   return e;

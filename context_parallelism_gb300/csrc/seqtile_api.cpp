@@ -936,7 +936,8 @@ struct LogpPlan {
   int64_t T = 0;             // tokens per tile
   int64_t ldl = 0;           // row pitch of the stored logits
   int keep = 0;              // candidates of a row
-  int run = 0, per_run = 0, short_groups = 0;  // of tiles of up to kLogpShortRows rows
+  int64_t full = 0;          // columns, tiles of up to kLogpShortRows rows: see LogpArgs
+  int rest = 0, short_groups = 0;
   int groups = 0;            // of longer ones
   size_t part = 0, tl = 0, logits = 0, best = 0, h[2] = {0, 0}, total = 0;
 };
@@ -959,10 +960,10 @@ LogpPlan plan_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile, bool
   p.T = seq_tile < S ? seq_tile : S;
   p.ldl = (V + 31) / 32 * 32;
   p.keep = top + kLogpMargin;
-  const int64_t run = (V + kLogpShortBlocks - 1) / kLogpShortBlocks;
-  p.run = static_cast<int>((run + 15) / 16 * 16);
-  p.per_run = (p.run + kLogpWidth - 1) / kLogpWidth;
-  p.short_groups = static_cast<int>((V + p.run - 1) / p.run) * p.per_run;
+  const int64_t left = V % (kLogpBlocks * kLogpWidth);
+  p.full = V - left;
+  p.rest = left ? static_cast<int>((left + 16 * kLogpBlocks - 1) / (16 * kLogpBlocks) * 16) : kLogpWidth;
+  p.short_groups = static_cast<int>(p.full / kLogpWidth + (left + p.rest - 1) / p.rest);
   p.groups = static_cast<int>((V + kLogpWidth - 1) / kLogpWidth);
   const int64_t few = p.T < kLogpShortRows ? p.T : kLogpShortRows;
   const size_t parts = static_cast<size_t>(p.T) * p.groups,
@@ -1066,16 +1067,17 @@ int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* l
     a.err = err;
     CUtensorMap th, tw, tw16;
     if (Mc <= kLogpShortRows) {
-      a.run = p.run;
-      a.per_run = p.per_run;
+      a.full = p.full;
+      a.rest = p.rest;
       a.groups = p.short_groups;
       LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, kLogpShortRows));
       LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 128));
       LOSS_CUDA(make_tmap_bf16(&tw16, w, Dm, V, 1, 16));
       LOSS_CUDA(launch_logp_short(tw, tw16, th, a, stream));
     } else {
-      a.groups = a.per_run = p.groups;
-      a.run = p.groups * kLogpWidth;
+      a.full = V / kLogpWidth * kLogpWidth;
+      a.rest = kLogpWidth;
+      a.groups = p.groups;
       LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, 128));
       LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 256));
       if (top) {

@@ -40,8 +40,9 @@ def test_workspace():
                                       (70, 8, 1, 24, 128, 0), (131072, 4096, 128256, 20, 8192, 2),
                                       (64, 72, 2433, 1, 256, 0)]:
         T = min(S, tile)
-        run = -(-(-(-V // 152)) // 16) * 16
-        short = -(-V // run) * -(-run // 128)
+        left = V % (152 * 128)  # up to 16 tokens: rounds of 152 groups of 128 columns, and one of less
+        rest = -(-left // (152 * 16)) * 16
+        short = (V - left) // 128 + (-(-left // rest) if left else 0)
         part = max(T * -(-V // 128), min(T, 16) * short) * 16
         want = al(part) + al(4 * T)
         want += al(4 * T * (-(-V // 32) * 32)) + al(4 * T * (top + 4)) if top else 0

@@ -463,10 +463,10 @@ struct EmbedArgs {
 cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaStream_t stream);
 
 // ---- token log probabilities (logp.cu) --------------------------------------------------------
-// Rows [0, M) of one tile of a call. The logits' columns come in `groups` groups: of kLogpWidth up to
-// `full`, of `rest` behind.
+// Rows [0, M) of one tile of a call. The logits' columns come in tiles of `tile`, a group each, or two if
+// it is above kLogpWidth: that many columns, and the others.
 constexpr int kLogpShortRows = 16;    // rows of a tile that the kernel for short calls takes at most
-constexpr int kLogpBlocks = 152;      // of that kernel
+constexpr int kLogpBlocks = 152;      // at most, one an SM
 constexpr int kLogpMargin = 4;        // candidates kept behind the last alternative
 constexpr int kLogpMaxTop = 24;
 
@@ -475,35 +475,36 @@ struct LogpArgs {
   const int64_t* target;       // [M], or NULL
   float* tlogit;               // [M] logit at the target
   float4* part;                // [M][groups]: see logp.cu (the last word: logp_mark)
-  float* logits;               // [M][ldl], or NULL (no alternatives)
-  int64_t ldl;
+  float* logits;               // [M][groups][kLogpWidth], or NULL (no alternatives)
   float *logp, *entropy, *lse; // [M]; each may be NULL
   float* top_logp;             // [M][top]
   int64_t* top_index;
   int M, Dm, top, keep;
   int64_t V;
-  int64_t full;                // a multiple of kLogpWidth
-  int groups, rest;            // rest: a multiple of 16, at most kLogpWidth
+  int groups, tile;            // tile: at most 2 kLogpWidth
   uint32_t* best;              // longer tiles with logits: [keep][M], see logp.cu
   uint32_t* err;
 };
 constexpr int kLogpWidth = 128;  // columns of a group
-__host__ __device__ inline int64_t group_start(const LogpArgs& a, int g) {
-  const int whole = static_cast<int>(a.full / kLogpWidth);
-  return g < whole ? static_cast<int64_t>(g) * kLogpWidth
-                   : a.full + static_cast<int64_t>(g - whole) * a.rest;
+__host__ __device__ inline int logp_tiles(const LogpArgs& a) {
+  return static_cast<int>((a.V + a.tile - 1) / a.tile);
 }
-// Columns of a group: 1 or more.
+__host__ __device__ inline int64_t group_start(const LogpArgs& a, int g) {
+  if (a.tile <= kLogpWidth) return static_cast<int64_t>(g) * a.tile;
+  return static_cast<int64_t>(g >> 1) * a.tile + (g & 1) * kLogpWidth;
+}
+// Columns of a group (0 or less: none).
 __host__ __device__ inline int group_width(const LogpArgs& a, int g) {
-  const int64_t c = group_start(a, g), left = a.V - c;
-  const int n = c < a.full ? kLogpWidth : a.rest;
+  int n = a.tile;
+  if (n > kLogpWidth) n = g & 1 ? n - kLogpWidth : kLogpWidth;
+  const int64_t left = a.V - group_start(a, g);
   return left < n ? static_cast<int>(left) : n;
 }
-// Logits and groups of up to kLogpShortRows rows. Maps of w with boxes of 128 and of 16 rows, of h with
-// one of kLogpShortRows.
-cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
-                              const LogpArgs& a, cudaStream_t stream);
-// The same of more rows, one run of all columns. Maps of h with boxes of 128 rows, of w with 256.
+// Logits and groups of up to kLogpShortRows rows, tiles of up to 128 columns. Maps of w with boxes of
+// a.tile rows, of h with one of kLogpShortRows.
+cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& th, const LogpArgs& a,
+                              cudaStream_t stream);
+// The same of more rows. Maps of h with boxes of 128 rows, of w with a.tile.
 cudaError_t launch_logp_long(const CUtensorMap& th, const CUtensorMap& tw, const LogpArgs& a, int sms,
                              cudaStream_t stream);
 cudaError_t launch_logp_pick(const LogpArgs& a, cudaStream_t stream);

@@ -26,15 +26,14 @@
 // and what it lost (every product of two bf16 is exact in fp32). Equal ones go by index.
 //
 // Up to 16 rows are bound by HBM: every row of w is read once. 128 rows of w are the M of an MMA, the
-// few rows of h its N. Each round of the 152 blocks takes the next 152 tiles; the last, which would be
-// six tenths full at 128256 rows, has tiles of an equal, smaller multiple of 16 rows. (One contiguous
-// run of rows for each block, which balances them as well, takes 4 us longer: 187 against 183 for one
-// token, five alternatives. For 17 to 128 tokens, whose last round is 45 tiles of 256 on 152 SMs, a
-// shorter last round takes 10 us longer, 179 against 170: its stages hold less of w for the same h.)
+// few rows of h its N. More rows are bound by HBM up to about 250 and by the tensor cores beyond:
+// 128 x 256 tiles of h and w, persistent blocks. Eight warps hold a tile's sums, 128 columns of a row
+// each; the work on a finished tile runs beside the next one's first 512 products.
 //
-// More rows are bound by HBM up to about 250 and by the tensor cores beyond: 128 x 256 tiles of h and
-// w, persistent blocks. Eight warps hold a tile's sums, 128 columns of a row each; the work on a
-// finished tile runs beside the next one's first 512 products.
+// Tiles have fewer columns than that where it fills the last round of blocks (LogpArgs::tile). It takes
+// every SM's copies in flight to reach 7 TB/s: with whole tiles of 256, 48 tokens of 128256 columns are
+// 3.3 rounds, of which the last 0.3 took as long as 0.7 of the others (174 us against 167 now, without
+// alternatives); with one run of rows of w for each block, up to 16 tokens took 178 us, now 161.
 #include <cfloat>
 
 #include "internal.h"
@@ -112,10 +111,9 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, float (&v)[16]) {
   for (int n = 0; n < 16; ++n) v[n] = __uint_as_float(r[n]);
 }
 
-// tm_w: boxes of 128 rows, tm_w16: of 16, tm_h: of N (rows behind the last are zeros).
+// tm_w: boxes of a.tile rows, tm_h: of N (rows behind the last are zeros). A tile is a group.
 __global__ void __launch_bounds__(kShortThreads, 1)
     logp_short_kernel(const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_w16,
                       const __grid_constant__ CUtensorMap tm_h, const LogpArgs a) {
   using L = ShortLayout;
   extern __shared__ uint8_t smem_raw[];
@@ -182,10 +180,8 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       int64_t fills = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int left = group_width(a, t), y0 = static_cast<int>(group_start(a, t));
-        // rows behind the tile's last keep what the stage held: their results are not used
-        const int boxes = left >= 128 ? 0 : (left + 15) / 16;
-        const uint32_t bytes = (boxes ? boxes * 2048u : 16384u) + L::kB;
+        // (of 128 rows of A those behind the tile's last keep what was there: results not used)
+        const uint32_t bytes = a.tile * 128u + L::kB;
         for (int kb = 0; kb < nk; ++kb) {
           if (!wait(empty + s, ph ^ 1)) {
             ok = false;
@@ -194,12 +190,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           uint8_t* sa = smem + s * L::kStage;
           mbar_arrive_expect_tx(full + s, bytes);
           tma_load_3d(sa + L::kA, &tm_h, kb * 64, 0, 0, full + s);
-          if (!boxes) {
-            tma_load_3d(sa, &tm_w, kb * 64, y0, 0, full + s);
-          } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_3d(sa + i * 2048, &tm_w16, kb * 64, y0 + 16 * i, 0, full + s);
-          }
+          tma_load_3d(sa, &tm_w, kb * 64, t * a.tile, 0, full + s);
           ++fills;
           if (++s == L::kStages) {
             s = 0;
@@ -310,8 +301,9 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         if (4 * lane + 1 >= left) v.y = -INFINITY;
         if (4 * lane + 2 >= left) v.z = -INFINITY;
         if (4 * lane + 3 >= left) v.w = -INFINITY;
-        // (a tile's columns are a multiple of 16, or end the padded row)
-        if (a.logits && 4 * lane < left) *reinterpret_cast<float4*>(a.logits + n * a.ldl + col) = v;
+        const int64_t at = static_cast<int64_t>(n) * a.groups + t;
+        if (a.logits && 4 * lane < left)
+          *reinterpret_cast<float4*>(a.logits + at * kLogpWidth + 4 * lane) = v;
         const float x[4] = {v.x, v.y, v.z, v.w};
         if (a.target) {
           const int64_t k = a.target[n] - col;
@@ -338,7 +330,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           sum1 += __shfl_xor_sync(kAll, sum1, o);
         }
         if (lane == 0)
-          a.part[static_cast<int64_t>(n) * a.groups + t] = make_float4(m, sum, sum1, mark(count, 15u));
+          a.part[at] = make_float4(m, sum, sum1, mark(count, 15u));
       }
     }
   }
@@ -375,18 +367,19 @@ __device__ __forceinline__ void long_tile(int64_t t, int m_tiles, int n_tiles, i
   *mt = grp * kLongGroup + static_cast<int>(rem - static_cast<int64_t>(*nt) * wide);
 }
 
-// Sums, target and wanted logits of 128 columns from col0 on of one row, x.
+// Sums, target and wanted logits of group g of one row: x, up to 128 columns from col0 to end.
 // Logits are wanted for the row's `keep` largest alone. Slot g % keep of `best` holds the largest
 // logit of every keep-th group so far, so the smallest of the slots is a bound below which no logit
 // can be among them: a slice of 32 columns below it is not stored (of 4096 x 128256 logits 6 % are, with
 // nine to keep; with all of them stored the call took 0.5 ms more). The bound only grows; an older
 // one stores more, never less.
-__device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int64_t col0,
+__device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int g, int col0, int end,
                                            uint32_t bound, float (&x)[128]) {
-  if (col0 + 128 > a.V) {
+  if (col0 + 128 > end) {
+    const int n = end - col0;
 #pragma unroll
     for (int j = 0; j < 128; ++j)
-      if (col0 + j >= a.V) x[j] = -INFINITY;
+      if (j >= n) x[j] = -INFINITY;
   }
   float top[4];
 #pragma unroll
@@ -396,15 +389,14 @@ __device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int64
     for (int j = 2; j < 32; j += 2) top[s] = fmax3(top[s], x[32 * s + j], x[32 * s + j + 1]);
   }
   const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  const int g = static_cast<int>(col0 / kLogpWidth);
   uint32_t stored = 0;
   if (a.logits) {
     atomicMax(a.best + static_cast<int64_t>(g % a.keep) * a.M + row, order_key(mx));
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      if (col0 + 32 * s >= a.V || order_key(top[s]) < bound) continue;
+      if (col0 + 32 * s >= end || order_key(top[s]) < bound) continue;
       stored |= 1u << s;
-      float4* dst = reinterpret_cast<float4*>(a.logits + row * a.ldl + col0 + 32 * s);
+      float4* dst = reinterpret_cast<float4*>(a.logits + (row * a.groups + g) * kLogpWidth + 32 * s);
 #pragma unroll
       for (int v = 0; v < 8; ++v)
         dst[v] = make_float4(x[32 * s + 4 * v], x[32 * s + 4 * v + 1], x[32 * s + 4 * v + 2],
@@ -425,7 +417,7 @@ __device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int64
   a.part[row * a.groups + g] = make_float4(mx, rest, sum1, mark(count, stored));
   if (a.target) {
     const int64_t k = a.target[row] - col0;
-    if (k >= 0 && k < 128 && col0 + k < a.V) {
+    if (k >= 0 && k < 128 && col0 + k < end) {
       float v = 0.f;
 #pragma unroll
       for (int j = 0; j < 128; ++j)  // (written as x[k], or as ?:, it would put x into local memory)
@@ -456,7 +448,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlot + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m_tiles = (a.M + 127) / 128, n_tiles = static_cast<int>((a.V + 255) / 256);
+  const int m_tiles = (a.M + 127) / 128, n_tiles = logp_tiles(a);
   const int64_t tiles = static_cast<int64_t>(m_tiles) * n_tiles;
   const int nk = (a.Dm + 63) / 64;
 
@@ -516,9 +508,9 @@ __global__ void __launch_bounds__(kLongThreads, 1)
             break;
           }
           uint8_t* sa = smem + s * L::kStage;
-          mbar_arrive_expect_tx(full + s, L::kStage);
+          mbar_arrive_expect_tx(full + s, L::kA + a.tile * 128u);
           tma_load_3d(sa, &tm_h, kb * 64, mt * 128, 0, full + s);
-          tma_load_3d(sa + L::kA, &tm_w, kb * 64, nt * 256, 0, full + s);
+          tma_load_3d(sa + L::kA, &tm_w, kb * 64, nt * a.tile, 0, full + s);
           ++fills;
           if (++s == L::kStages) {
             s = 0;
@@ -536,7 +528,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer: the whole warp, converged; one lane's products go out ----------------
-    const uint32_t idesc = idesc_bf16(128, 256, false, false);
+    const uint32_t idesc = idesc_bf16(128, (a.tile + 15) / 16 * 16, false, false);
     const uint32_t s0 = smem_u32(smem);
     const uint64_t dA0 = kdesc0(s0), dB0 = kdesc0(s0 + L::kA);
     int s = 0, buf = 0;
@@ -583,7 +575,6 @@ __global__ void __launch_bounds__(kLongThreads, 1)
       int mt, nt;
       long_tile(t, m_tiles, n_tiles, &mt, &nt);
       const int64_t row = static_cast<int64_t>(mt) * 128 + 32 * quarter + lane;
-      const int64_t col0 = static_cast<int64_t>(nt) * 256 + 128 * half;
       uint32_t bound = 0xffffffffu;
       if (a.logits && row < a.M) {
         // eight loads at a time: one after the other they would take longer than a piece of the tile
@@ -620,7 +611,14 @@ __global__ void __launch_bounds__(kLongThreads, 1)
         buf ^= 1;
         ph ^= buf == 0;
       }
-      if (ok && row < a.M && col0 < a.V) finish_row(a, row, col0, bound, x);
+      if (!ok || row >= a.M || 128 * half >= a.tile) continue;
+      const int per = a.tile > kLogpWidth ? 2 : 1, g = nt * per + half;
+      const int col0 = nt * a.tile + 128 * half;
+      const int end = min((nt + 1) * a.tile, static_cast<int>(a.V));
+      if (col0 < end)
+        finish_row(a, row, g, col0, end, bound, x);
+      else
+        a.part[row * a.groups + g] = no_sums();
     }
   }
 
@@ -919,10 +917,10 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     return;
   }
 
-  // the groups with the largest maxima, by number
+  // the groups with the largest maxima (one behind the last column has none), by number
   auto offer = [&](int g, const float4& p) {
     const uint32_t key = order_key(p.x);
-    if (g >= a.groups || key < grp_least) return;
+    if (g >= a.groups || key < grp_least || group_width(a, g) <= 0) return;
     const int at = atomicAdd(&few_n, 1);
     if (at >= kFew) return;
     few_key[at] = key;
@@ -954,7 +952,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     }
     groups = min(groups, a.keep);
   } else {
-    auto group_key = [&](int g) { return order_key(part[g].x); };
+    auto group_key = [&](int g) { return group_width(a, g) > 0 ? order_key(part[g].x) : 0u; };
     groups = block_select<kThreads>(group_key, a.groups, a.keep, 1u, list, counts);
     if (threadIdx.x < 32) {
       const int mine = lane < groups ? list[lane] : 0x7fffffff;
@@ -976,9 +974,9 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   const uint32_t least = groups == a.keep ? last_key : 1u;
   __syncthreads();
   // their logits from the smallest of these maxima on; columns that were not stored are below it
-  const float* x = a.logits + row * a.ldl;
+  const float* x = a.logits + row * a.groups * kLogpWidth;
   for (int k = warp; k < groups; k += kWarps) {
-    const int64_t c0 = group_start(a, grp[k]);
+    const int64_t c0 = static_cast<int64_t>(grp[k]) * kLogpWidth;
     const int n = group_width(a, grp[k]);
     const uint32_t stored = grp_mark[k] >> 16;
     for (int c = lane; c < kLogpWidth; c += 32) {
@@ -1082,14 +1080,14 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
 
 }  // namespace
 
-cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& tw16, const CUtensorMap& th,
-                              const LogpArgs& a, cudaStream_t stream) {
+cudaError_t launch_logp_short(const CUtensorMap& tw, const CUtensorMap& th, const LogpArgs& a,
+                              cudaStream_t stream) {
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_short_kernel),
                                    ShortLayout::kBytes);
   if (e != cudaSuccess) return e;
   launch_begin(kClass, stream);
-  const int blocks = a.groups < kLogpBlocks ? a.groups : kLogpBlocks;  // a tile is a group
-  logp_short_kernel<<<blocks, kShortThreads, ShortLayout::kBytes, stream>>>(tw, tw16, th, a);
+  const int blocks = a.groups < kLogpBlocks ? a.groups : kLogpBlocks;
+  logp_short_kernel<<<blocks, kShortThreads, ShortLayout::kBytes, stream>>>(tw, th, a);
   e = cudaGetLastError();
   launch_end(kClass, stream);
   return e;
@@ -1100,7 +1098,7 @@ cudaError_t launch_logp_long(const CUtensorMap& th, const CUtensorMap& tw, const
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&logp_long_kernel),
                                    LongLayout::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((a.M + 127) / 128) * ((a.V + 255) / 256);
+  const int64_t tiles = static_cast<int64_t>((a.M + 127) / 128) * logp_tiles(a);
   launch_begin(kClass, stream);
   logp_long_kernel<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kLongThreads,
                      LongLayout::kBytes, stream>>>(th, tw, a);

@@ -934,11 +934,7 @@ namespace {
 
 struct LogpPlan {
   int64_t T = 0;             // tokens per tile
-  int64_t ldl = 0;           // row pitch of the stored logits
   int keep = 0;              // candidates of a row
-  int64_t full = 0;          // columns, tiles of up to kLogpShortRows rows: see LogpArgs
-  int rest = 0, short_groups = 0;
-  int groups = 0;            // of longer ones
   size_t part = 0, tl = 0, logits = 0, best = 0, h[2] = {0, 0}, total = 0;
 };
 
@@ -955,29 +951,42 @@ int check_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile) {
   return UPIPE_OK;
 }
 
+// Columns of a tile for M rows. As many rounds of tiles over the SMs as the widest tiles make, cut evenly
+// where that is worth more than the odd width costs (48 tokens, 128256 columns: 4 rounds of 211, not 3.3
+// of 256; 4096 tokens: 105.5 of 256). At least 64 with many rows, which each tile reads again.
+int logp_tile(int64_t M, int64_t V) {
+  const bool few = M <= kLogpShortRows;
+  const int64_t most = few ? kLogpWidth : 2 * kLogpWidth, least = few ? 16 : 64;
+  const int64_t m = few ? 1 : (M + 127) / 128;
+  const int64_t rounds = (m * ((V + most - 1) / most) + kLogpBlocks - 1) / kLogpBlocks;
+  const int64_t n = rounds * kLogpBlocks / m;  // tiles of columns
+  const int64_t width = (V + n - 1) / n;
+  return static_cast<int>(width < least ? least : width > most * 31 / 32 ? most : width);
+}
+
+int logp_groups(int64_t M, int64_t V) {
+  const int tile = logp_tile(M, V);
+  return static_cast<int>((V + tile - 1) / tile) * (tile > kLogpWidth ? 2 : 1);
+}
+
 LogpPlan plan_logp(int64_t S, int Dm, int64_t V, int top, int64_t seq_tile, bool host_act) {
   LogpPlan p;
   p.T = seq_tile < S ? seq_tile : S;
-  p.ldl = (V + 31) / 32 * 32;
   p.keep = top + kLogpMargin;
-  const int64_t left = V % (kLogpBlocks * kLogpWidth);
-  p.full = V - left;
-  p.rest = left ? static_cast<int>((left + 16 * kLogpBlocks - 1) / (16 * kLogpBlocks) * 16) : kLogpWidth;
-  p.short_groups = static_cast<int>(p.full / kLogpWidth + (left + p.rest - 1) / p.rest);
-  p.groups = static_cast<int>((V + kLogpWidth - 1) / kLogpWidth);
-  const int64_t few = p.T < kLogpShortRows ? p.T : kLogpShortRows;
-  const size_t parts = static_cast<size_t>(p.T) * p.groups,
-               few_parts = static_cast<size_t>(few) * p.short_groups;
+  const int64_t last = S % p.T;  // rows of a shorter tile
+  const size_t parts = static_cast<size_t>(p.T) * logp_groups(p.T, V),
+               last_parts = static_cast<size_t>(last) * (last ? logp_groups(last, V) : 0);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += al(bytes);
     return at;
   };
-  p.part = take((parts > few_parts ? parts : few_parts) * 16);
+  const size_t groups = parts > last_parts ? parts : last_parts;
+  p.part = take(groups * 16);
   p.tl = take(static_cast<size_t>(p.T) * 4);
   if (top) {
-    p.logits = take(static_cast<size_t>(p.T) * p.ldl * 4);
+    p.logits = take(groups * kLogpWidth * 4);
     p.best = take(static_cast<size_t>(p.T) * p.keep * 4);
   }
   if (host_act) plan_slots(&off, p.T, int64_t(Dm) * 2, p.h);
@@ -1053,7 +1062,6 @@ int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* l
     a.tlogit = reinterpret_cast<float*>(ws + p.tl);
     a.part = reinterpret_cast<float4*>(ws + p.part);
     a.logits = top ? reinterpret_cast<float*>(ws + p.logits) : nullptr;
-    a.ldl = p.ldl;
     a.logp = logp ? logp + r0 : nullptr;
     a.entropy = entropy ? entropy + r0 : nullptr;
     a.lse = lse ? lse + r0 : nullptr;
@@ -1065,21 +1073,15 @@ int upipe_logp_fwd(const void* h, const void* w, const int64_t* target, float* l
     a.keep = p.keep;
     a.V = V;
     a.err = err;
-    CUtensorMap th, tw, tw16;
-    if (Mc <= kLogpShortRows) {
-      a.full = p.full;
-      a.rest = p.rest;
-      a.groups = p.short_groups;
-      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, kLogpShortRows));
-      LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 128));
-      LOSS_CUDA(make_tmap_bf16(&tw16, w, Dm, V, 1, 16));
-      LOSS_CUDA(launch_logp_short(tw, tw16, th, a, stream));
+    a.tile = logp_tile(Mc, V);
+    a.groups = logp_groups(Mc, V);
+    const bool few = Mc <= kLogpShortRows;
+    CUtensorMap th, tw;
+    LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, few ? kLogpShortRows : 128));
+    LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, a.tile));
+    if (few) {
+      LOSS_CUDA(launch_logp_short(tw, th, a, stream));
     } else {
-      a.full = V / kLogpWidth * kLogpWidth;
-      a.rest = kLogpWidth;
-      a.groups = p.groups;
-      LOSS_CUDA(make_tmap_bf16(&th, a.h, Dm, Mc, 1, 128));
-      LOSS_CUDA(make_tmap_bf16(&tw, w, Dm, V, 1, 256));
       if (top) {
         a.best = reinterpret_cast<uint32_t*>(ws + p.best);
         LOSS_CUDA(cudaMemsetAsync(a.best, 0, static_cast<size_t>(Mc) * p.keep * 4, stream));

@@ -279,8 +279,8 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * the loss (host_mask = UPIPE_HOST_ACT).
  * Supported: Dm a multiple of 8, any V up to 2^30, top up to 24, seq_tile a multiple of 128. S = 0
  * does nothing. Workspace: upipe_logp_workspace_bytes: for T = min(seq_tile, S) tokens 16 bytes for
- * each token and 128 columns (up to 16 tokens: up to 152 smaller groups behind the last ones), 4 T, and with
- * top > 0 the tile's logits, 4 T V (V rounded up to 32; few of them are written), and 4 T (top + 4);
+ * each token and group of up to 128 columns (which are cut to fill 152 SMs evenly), 4 T, and with top > 0
+ * the tile's logits, 512 bytes for each token and group (few of them are written), and 4 T (top + 4);
  * each rounded up to 256, plus two slots with UPIPE_HOST_ACT.
  * Results repeat bitwise for the same sizes.
  */

@@ -72,8 +72,10 @@ SHAPES = [  # S, Dm, V, top
     (48, 328, 20011, 20), (5, 2048, 5003, 24), (16, 4096, 3000, 5), (17, 4096, 3000, 5),
     (65, 8, 1, 2), (66, 64, 31, 24), (128, 72, 256, 5), (129, 256, 257, 0), (200, 264, 1000, 1),
     (300, 1000, 2433, 20), (257, 1024, 5003, 24), (70, 2048, 20011, 5), (511, 16, 300, 8),
-    # up to 16 tokens: whole rounds of 152 groups of 128 columns, and a last one of fewer or none
+    # tiles of other numbers of columns, whole and broken last ones, one and several rounds of them
     (3, 72, 38912, 24), (16, 136, 45613, 9), (2, 200, 97281, 0), (9, 72, 128256, 5), (1, 264, 38913, 3),
+    (100, 136, 45613, 9), (17, 72, 128256, 24), (128, 200, 97281, 0), (19, 2048, 38913, 24),
+    (255, 64, 60001, 5), (40, 64, 9729, 3), (40, 64, 19457, 3), (385, 72, 9999, 2),
 ]
 
 

@@ -33,19 +33,25 @@ def test_calls_without_tokens_do_nothing():
     assert _call(S=0, h=None, target=None, ws=None) == OK
 
 
+def _groups(M, V):
+    """Columns go in tiles of up to 128 (16 rows), else 256, as many rounds of 152 as those make, evenly."""
+    most, m = (128, 1) if M <= 16 else (256, -(-M // 128))
+    n = -(-m * -(-V // most) // 152) * 152 // m
+    tile = max(16 if M <= 16 else 64, -(-V // n))
+    tile = most if tile > most * 31 // 32 else tile
+    return -(-V // tile) * (2 if tile > 128 else 1)
+
+
 def test_workspace():
-    """As documented: partial sums of the longer of the two tilings, target logits, logits, slots."""
+    """As documented: partial sums of the groups of columns, target logits, logits, slots."""
     al = lambda x: -(-x // 256) * 256  # noqa: E731
     for S, Dm, V, top, tile, host in [(1, 4096, 128256, 5, 4096, 0), (300, 64, 1000, 0, 128, 2),
                                       (70, 8, 1, 24, 128, 0), (131072, 4096, 128256, 20, 8192, 2),
                                       (64, 72, 2433, 1, 256, 0)]:
         T = min(S, tile)
-        left = V % (152 * 128)  # up to 16 tokens: rounds of 152 groups of 128 columns, and one of less
-        rest = -(-left // (152 * 16)) * 16
-        short = (V - left) // 128 + (-(-left // rest) if left else 0)
-        part = max(T * -(-V // 128), min(T, 16) * short) * 16
-        want = al(part) + al(4 * T)
-        want += al(4 * T * (-(-V // 32) * 32)) + al(4 * T * (top + 4)) if top else 0
+        groups = max(m * _groups(m, V) for m in (T, S % T) if m)
+        want = al(16 * groups) + al(4 * T)
+        want += al(512 * groups) + al(4 * T * (top + 4)) if top else 0
         want += 2 * al(2 * T * Dm) if host else 0
         assert up.upipe_logp_workspace_bytes(S, Dm, V, top, tile, host) == want
     for bad in ((0, 64, 100, 1, 128), (5, 60, 100, 1, 128), (5, 64, 0, 1, 128), (5, 64, 100, 25, 128),

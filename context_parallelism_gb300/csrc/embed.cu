@@ -13,14 +13,17 @@
 // have thousands of places, most have one or none): a chunk adds up its rows run by run. A run that
 // lies inside the chunk goes straight to dw; what belongs to a run that goes on beside the chunk is
 // left as a partial sum, at most two a chunk, and a last kernel joins them in order. Rows of tokens
-// that do not occur are zeroed by blocks of the same launch, from a bitmap that the sort leaves.
+// that do not occur are zeroed by blocks of the same launch, from a bitmap that the sort leaves. (Some
+// of them zeroed beside the sort instead: no gain at 4097 places, 10 us lost at 8192, whose tokens then
+// wait behind the stores.)
 //
-// Sort: a stable radix sort of 32-bit tokens with their places, in passes of up to 9 bits (17 bits of
-// vocabulary: 2 passes). A place's rank in its block: warps count 32 places at a time, matching equal
-// digits by ballots. Up to kSmall places one block sorts in shared memory (beside it, where the whole
-// table is small, other blocks write its zeros). More places: two launches a pass, histograms of 2048
-// places and scatter, each scatter block adding up the histograms before it (with more than kFewTiles
-// blocks a launch between does that).
+// Sort, up to kSmall places: one launch that counts, for each place, the keys before it. That is S^2
+// comparisons, yet 6 us for 4097 places and 13 for 8192 over all SMs, where a radix sort in the shared
+// memory of one block took 18 and 22, and its launches on all SMs 22 (at 10240 places: 16, against 20).
+// More: a stable radix sort of 32-bit tokens with their places, in passes of up to 9 bits (17 bits of
+// vocabulary: 2 passes), two launches a pass, histograms of 2048 places and scatter, each scatter block
+// adding up the histograms before it (with more than kFewTiles blocks a launch between does that). A
+// place's rank in its block: warps count 32 places at a time, matching equal digits by ballots.
 #include "internal.h"
 #include "rope.cuh"
 
@@ -137,81 +140,62 @@ __device__ __forceinline__ uint32_t block_before(uint32_t x, uint32_t* warp_sum)
   return before;
 }
 
-// Block 0 sorts up to kSmall places; the others, if any, write zeros to dw.
+// Up to kSmall places are sorted by counting, for each, the keys before it: a warp takes two places, and
+// every block has all keys in shared memory. With them it also makes its part of the bitmap.
 constexpr int kSmall = 8192;
-constexpr int kSmallThreads = 1024;
-constexpr int kSmallRounds = kSmall / kSmallThreads;
-constexpr int kSmallSmem = kSmall * 4 * 4 + 32 * kMaxBins * 4;
+constexpr int kRankThreads = 512;
+constexpr int kRankBlocks = 152;
+constexpr int kRankWords = 2048;  // of the bitmap at a time
 
-__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const EmbedArgs a, int passes,
-                                                                   int bits, uint32_t* keys_out,
-                                                                   uint32_t* places_out) {
-  extern __shared__ uint32_t sm[];
-  __shared__ uint32_t warp_sum[32];
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const EmbedArgs a, uint32_t* keys_out,
+                                                            uint32_t* places_out) {
+  extern __shared__ uint4 quad[];
+  __shared__ uint32_t word[kRankWords];
+  uint32_t* key = reinterpret_cast<uint32_t*>(quad);
   launch_dependents();
-  if (blockIdx.x > 0) {
-    const int64_t n = a.V * (a.Dm / 4), step = static_cast<int64_t>(gridDim.x - 1) * kSmallThreads;
-    float4* dst = reinterpret_cast<float4*>(a.dw);
-    for (int64_t k = static_cast<int64_t>(blockIdx.x - 1) * kSmallThreads + threadIdx.x; k < n; k += step)
-      dst[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    return;
-  }
-  uint32_t* keys[2] = {sm, sm + kSmall};
-  uint32_t* places[2] = {sm + 2 * kSmall, sm + 3 * kSmall};
-  uint32_t(*count)[kMaxBins] = reinterpret_cast<uint32_t(*)[kMaxBins]>(sm + 4 * kSmall);
-  const int n = static_cast<int>(a.S);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (n + 1023) / 1024;  // rounds: a warp's places are 32 * per in a row
-  const int warps = (n + 32 * per - 1) / (32 * per);
-  for (int i = threadIdx.x; i < n; i += kSmallThreads) {
-    const uint32_t key = first_key(a, i);
-    keys[0][i] = key;
-    places[0][i] = i;
-    mark_present(a, key);
-  }
-  const int bins = 1 << bits;
-  int in = 0;
-  for (int pass = 0; pass < passes; ++pass, in ^= 1) {
-    for (int d = threadIdx.x; d < warps * bins; d += kSmallThreads) count[d >> bits][d & (bins - 1)] = 0;
-    __syncthreads();
-    const int base = warp * 32 * per, left = n - base;
-    uint32_t key[kSmallRounds], place[kSmallRounds], digit[kSmallRounds], rank[kSmallRounds];
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      const int i = base + r * 32 + lane;
-      const bool is = r < per && i < n;
-      key[r] = is ? keys[in][i] : 0;
-      place[r] = is ? places[in][i] : 0;
-      digit[r] = (key[r] >> (pass * bits)) & (bins - 1);
-    }
-    const int mine = left < 32 * per ? left : 32 * per;  // of this warp; none: 0 or less
-    warp_ranks<kSmallRounds>(digit, mine > 0 ? mine : 0, bits, count[warp], rank);
-    __syncthreads();
-    uint32_t total = 0;
-    const int d = threadIdx.x;
-    if (d < bins) {
+  const int n = static_cast<int>(a.S), quads = (n + 3) / 4;
 #pragma unroll 8
-      for (int k = 0; k < warps; ++k) total += count[k][d];
+  for (int i = threadIdx.x; i < 4 * quads; i += kRankThreads)
+    key[i] = i < n ? first_key(a, i) : 0xffffffffu;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (n + kRankBlocks - 1) / kRankBlocks;
+  const int lo = blockIdx.x * per, hi = min(lo + per, n);
+  for (int i = lo + 2 * warp; i < hi; i += kRankThreads / 16) {
+    const int j = min(i + 1, hi - 1);
+    const uint32_t ki = key[i], kj = key[j];
+    const int qi = i >> 2, qj = j >> 2;
+    uint32_t ci = 0, cj = 0;
+#pragma unroll 4
+    for (int q = lane; q < quads; q += 32) {
+      const uint4 x = quad[q];
+      const uint32_t ti = ki + (q < qi), tj = kj + (q < qj);  // equal keys count where they come before
+      ci += (x.x < ti) + (x.y < ti) + (x.z < ti) + (x.w < ti);
+      cj += (x.x < tj) + (x.y < tj) + (x.z < tj) + (x.w < tj);
     }
-    uint32_t at = block_before(total, warp_sum);
-    if (d < bins) {
-      for (int k = 0; k < warps; ++k) {
-        const uint32_t c = count[k][d];
-        count[k][d] = at;
-        at += c;
-      }
+    if (lane < (i & 3)) ci += key[4 * qi + lane] == ki;
+    if (lane < (j & 3)) cj += key[4 * qj + lane] == kj;
+    ci = __reduce_add_sync(0xffffffffu, ci);
+    cj = __reduce_add_sync(0xffffffffu, cj);
+    if (lane < 2) {  // (the same place twice at the end)
+      const uint32_t to = lane ? cj : ci;
+      keys_out[to] = lane ? kj : ki;
+      places_out[to] = lane ? j : i;
+    }
+  }
+  if (!a.present) return;
+  const int64_t words = (a.V + 31) / 32, some = (words + kRankBlocks - 1) / kRankBlocks;
+  const int64_t first = blockIdx.x * some, end = first + some < words ? first + some : words;
+  for (int64_t w0 = first; w0 < end; w0 += kRankWords) {
+    const uint32_t len = static_cast<uint32_t>(end - w0 < kRankWords ? end - w0 : kRankWords);
+    for (uint32_t k = threadIdx.x; k < len; k += kRankThreads) word[k] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kRankThreads) {
+      const uint32_t at = (key[i] >> 5) - static_cast<uint32_t>(w0);  // (those before: large)
+      if (at < len) atomicOr(&word[at], 1u << (key[i] & 31));
     }
     __syncthreads();
-    const bool last = pass == passes - 1;
-    uint32_t* ko = last ? keys_out : keys[in ^ 1];
-    uint32_t* po = last ? places_out : places[in ^ 1];
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      if (r * 32 + lane >= mine) break;
-      const uint32_t to = count[warp][digit[r]] + rank[r];
-      ko[to] = key[r];
-      po[to] = place[r];
-    }
+    for (uint32_t k = threadIdx.x; k < len; k += kRankThreads) a.present[w0 + k] = word[k];
     __syncthreads();
   }
 }
@@ -384,8 +368,8 @@ constexpr int kAhead = 8;  // rows of dh in flight a thread
 __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const uint32_t* keys,
                                                         const uint32_t* places) {
   __shared__ uint32_t key[kMaxChunk + 2], place[kMaxChunk];
-  launch_dependents();
   grid_dependency_wait();
+  launch_dependents();  // here, so that the next kernel has the sorted keys from its start
   const int64_t units = a.chunks * a.slices;
   if (static_cast<int64_t>(blockIdx.x) >= units) {
     const int64_t v0 = (static_cast<int64_t>(blockIdx.x) - units) * kZeroRows;
@@ -452,25 +436,26 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const
 
 // One block for each chunk in which a run begins that goes on: its partial sums, kJoin runs of chunks one
 // beside the other (a token that fills a tenth of a long sequence has hundreds), then these in order.
+// Which runs these are it finds while the last sums are made (1 us less).
 constexpr int kJoin = 4;
 __global__ void __launch_bounds__(128 * kJoin) embed_join_kernel(const EmbedArgs a,
                                                                  const uint32_t* keys) {
   __shared__ float4 sums[kJoin - 1][2][128];
-  launch_dependents();
-  grid_dependency_wait();
   const int64_t chunk = blockIdx.x / a.slices;
   const int slice = static_cast<int>(blockIdx.x - chunk * a.slices);
   const int64_t lo = chunk * a.chunk, hi = lo + a.chunk;
   if (hi >= a.S) return;  // the last chunk
-  const uint32_t k = keys[hi - 1], next = keys[hi], before = lo > 0 ? keys[lo - 1] : 0xffffffffu;
+  const uint32_t k = __ldcg(keys + hi - 1), next = __ldcg(keys + hi),
+                 before = lo > 0 ? __ldcg(keys + lo - 1) : 0xffffffffu;
   if (k >= static_cast<uint32_t>(a.V) || next != k) return;
   if (before == k) return;  // it began before
   // the last chunk that it reaches: the keys are sorted, so those that begin with it come first
   int64_t last = chunk;
   for (int more = blockDim.x; more == static_cast<int>(blockDim.x); last += more) {
     const int64_t i = (last + 1 + threadIdx.x) * a.chunk;
-    more = __syncthreads_count(i < a.S && keys[i] == k);
+    more = __syncthreads_count(i < a.S && __ldcg(keys + i) == k);
   }
+  grid_dependency_wait();
   const int threads = blockDim.x / kJoin, part = threadIdx.x / threads,
             col = threadIdx.x - part * threads;
   const int f = (slice * threads + col) * 8;
@@ -571,21 +556,12 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
                      args...);
     launch_end(kEmbedClass, stream);
   };
-  // A small table is zeroed whole while the places are sorted (4097 places, 32003 rows of 1000: 37 us, 50
-  // with zeros beside the sums), the rows of tokens that occur are then written twice; a large one
-  // beside the sums, absent rows alone (8192 places, 128256 rows of 4096: 338 us, 358 the other way).
-  const int64_t table = a.V * a.Dm * 4;
-  const bool first = !a.add && p.tiles == 0 && table <= (int64_t(192) << 20);
-  if (first) a.present = nullptr;
-  if (a.present) e = cudaMemsetAsync(a.present, 0, static_cast<size_t>((a.V + 31) / 32) * 4, stream);
-  if (e == cudaSuccess && p.tiles == 0)
-    e = ensure_smem_attr(reinterpret_cast<const void*>(&sort_small_kernel), kSmallSmem);
   int in = 0;
   if (p.tiles == 0) {
-    const int64_t zero = first ? (table + 65535) / 65536 : 0;  // a block for every 64 KB
-    launch(sort_small_kernel, 1 + (zero < 151 ? zero : 151), kSmallThreads, kSmallSmem, false, a,
-           p.passes, p.bits, keys[0], places[0]);
+    launch(rank_kernel, kRankBlocks, kRankThreads, static_cast<size_t>(a.S + 3) / 4 * 16, false, a,
+           keys[0], places[0]);
   } else {
+    if (a.present) e = cudaMemsetAsync(a.present, 0, static_cast<size_t>((a.V + 31) / 32) * 4, stream);
     const int scanned = p.tiles > kFewTiles;
     for (int pass = 0; pass < p.passes; ++pass, in ^= 1) {
       const int shift = pass * p.bits;

@@ -437,7 +437,7 @@ cudaError_t launch_embed(const int64_t* tokens, const void* w, void* h, int64_t 
 // Sizes and workspace (byte offsets) of the gradient; S >= 1, V < 2^31, host arithmetic.
 struct EmbedPlan {
   int passes, bits;         // of the sort
-  int64_t tiles;            // its blocks (0: one block in shared memory)
+  int64_t tiles;            // its blocks (0: few places, sorted by counting)
   int threads, slices;      // of the sums: threads a block, blocks a chunk
   int chunk;                // places a chunk
   int64_t chunks;

@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ float picked[];
   __shared__ float red[kWarps][3];
-  __shared__ float row_max, row_ln;
+  __shared__ float row_ln;
   __shared__ uint32_t counts[256];
   __shared__ int list[32], grp[32], cand[32];
   __shared__ uint32_t grp_least, last_key, grp_mark[32];
@@ -884,38 +884,32 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
     red[warp][2] = count;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    rest = sum1 = count = 0.f;
-    for (int k = 0; k < kWarps; ++k) {
-      rest += red[k][0];
-      sum1 += red[k][1];
-      count += red[k][2];
+  if (warp == kWarps - 1) {  // (the others go on: ln is wanted at the end)
+    rest = lane < kWarps ? red[lane][0] : 0.f;
+    sum1 = lane < kWarps ? red[lane][1] : 0.f;
+    count = lane < kWarps ? red[lane][2] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      rest += __shfl_xor_sync(kAll, rest, o);
+      sum1 += __shfl_xor_sync(kAll, sum1, o);
+      count += __shfl_xor_sync(kAll, count, o);
     }
     // a row with a logit of NaN or +inf, or without a finite one, has no probabilities
     float ln = logf(count) + log1pf(rest / count);
     if (!(fabsf(m) <= FLT_MAX)) ln = __int_as_float(0x7fc00000);
-    if (a.lse) a.lse[row] = m + ln;
-    if (a.entropy) a.entropy[row] = ln - sum1 / (count + rest);
-    if (a.logp) {
-      const int64_t t = a.target[row];
-      a.logp[row] = t < 0 ? 0.f : t < a.V ? (a.tlogit[row] - m) - ln : __int_as_float(0x7fc00000);
+    if (lane == 0) {
+      if (a.lse) a.lse[row] = m + ln;
+      if (a.entropy) a.entropy[row] = ln - sum1 / (count + rest);
+      if (a.logp) {
+        const int64_t t = a.target[row];
+        a.logp[row] = t < 0 ? 0.f : t < a.V ? (a.tlogit[row] - m) - ln : __int_as_float(0x7fc00000);
+      }
+      row_ln = ln;
     }
-    row_max = m;
-    row_ln = ln;
   }
   if (!a.top) return;
-  __syncthreads();
-  m = row_max;
-  const float ln = row_ln;
   float* out_v = a.top_logp + row * a.top;
   int64_t* out_i = a.top_index + row * a.top;
-  if (!(fabsf(ln) <= FLT_MAX)) {
-    for (int k = threadIdx.x; k < a.top; k += kThreads) {
-      out_v[k] = __int_as_float(0x7fc00000);
-      out_i[k] = -1;
-    }
-    return;
-  }
 
   // the groups with the largest maxima (one behind the last column has none), by number
   auto offer = [&](int g, const float4& p) {
@@ -931,6 +925,14 @@ __global__ void __launch_bounds__(kThreads) logp_pick_kernel(const LogpArgs a) {
   for (int k = 0; k < kOwn; ++k) offer(threadIdx.x + k * kThreads, own[k]);
   for (int g = threadIdx.x + kOwn * kThreads; g < a.groups; g += kThreads) offer(g, part[g]);
   __syncthreads();
+  const float ln = row_ln;
+  if (!(fabsf(ln) <= FLT_MAX)) {
+    for (int k = threadIdx.x; k < a.top; k += kThreads) {
+      out_v[k] = __int_as_float(0x7fc00000);
+      out_i[k] = -1;
+    }
+    return;
+  }
   int groups = few_n;
   if (groups <= kFew) {
     // of these, each one's place among the wanted ones by number

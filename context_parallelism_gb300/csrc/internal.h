@@ -459,6 +459,7 @@ struct EmbedArgs {
   float* part;              // [chunks][2][Dm]
   int64_t chunks;
   int chunk, slices;
+  int zero_rows;            // rows of dw that a block writes zeros to, at most (a power of 2, at most 32)
 };
 cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaStream_t stream);
 

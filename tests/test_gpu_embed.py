@@ -142,6 +142,27 @@ def test_long_sequence(n, V):
     assert ((dw.double() - ref).abs() <= (count + 3) * 2.0 ** -24 * size).all()
 
 
+@pytest.mark.parametrize("n,Dm,V", [(300, 8, 152 * 2048 * 32 + 33), (20001, 1032, 5000), (8191, 2056, 400),
+                                    (8192, 64, 31), (40000, 4104, 100)])
+def test_large_tables_and_odd_chunks(n, Dm, V):
+    """A bitmap that a block makes in pieces; chunks of lengths that divide nothing; against index_add."""
+    t, dh = torch.randint(-1, V, (n,), device=DEV), _bf(n, Dm, seed=4)
+    t[n // 3], t[n // 2:n // 2 + n // 5] = V - 1, V // 2
+    dw = up.embed_backward(t, dh, V)
+    live = t >= 0
+    rows, at, count = t[live].unique(return_inverse=True, return_counts=True)
+    ref = torch.zeros((len(rows), Dm), dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(ref)
+    for lo in range(0, int(live.sum()), 4096):
+        x = dh[live][lo:lo + 4096].double()
+        ref.index_add_(0, at[lo:lo + 4096], x)
+        size.index_add_(0, at[lo:lo + 4096], x.abs())
+    assert ((dw[rows].double() - ref).abs() <= (count[:, None] + 3) * 2.0 ** -24 * size).all()
+    absent = torch.ones(V, dtype=torch.bool, device=DEV)
+    absent[rows] = False
+    assert not dw[absent].any()
+
+
 def test_streams_graphs_and_two_workspaces():
     n, Dm, V = 5000, 128, 3000
     t, dh, w = _tokens(n, V, 1, "text").to(DEV), _bf(n, Dm, seed=1), _bf(V, Dm, seed=2)

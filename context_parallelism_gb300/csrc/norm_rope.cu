@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(kBwdThreads, 4) norm_rope_bwd_kernel(const Nor
       if (then == kPer) next = enter((n + 1) * walkers + walker);
       start(then < kPer ? then < w.heads : then - kPer < next.heads, slot);
       const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
-      const float r = inverse_rms(a, ss, x, y);
+      float r = inverse_rms(a, ss, x, y);
+      if (!here) r = 0.f;  // without eps the zeros of no head would make dw NaN
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (turns) {

@@ -445,11 +445,19 @@ __global__ void __launch_bounds__(128 * kJoin) embed_join_kernel(const EmbedArgs
   const int64_t chunk = blockIdx.x / a.slices;
   const int slice = static_cast<int>(blockIdx.x - chunk * a.slices);
   const int64_t lo = chunk * a.chunk, hi = lo + a.chunk;
-  if (hi >= a.S) return;  // the last chunk
-  const uint32_t k = __ldcg(keys + hi - 1), next = __ldcg(keys + hi),
-                 before = lo > 0 ? __ldcg(keys + lo - 1) : 0xffffffffu;
-  if (k >= static_cast<uint32_t>(a.V) || next != k) return;
-  if (before == k) return;  // it began before
+  uint32_t k = 0xffffffffu, next = 0, before = k;
+  if (hi < a.S) {  // not the last chunk
+    k = __ldcg(keys + hi - 1);
+    next = __ldcg(keys + hi);
+    if (lo > 0) before = __ldcg(keys + lo - 1);
+  }
+  if (k >= static_cast<uint32_t>(a.V) || next != k || before == k) {  // (before: it began there)
+    // What comes behind this launch in a stream or a graph waits for it alone, so it must not end before
+    // the sums do, also where no block has anything to join: the first block always waits for them, and
+    // with it the launch. (All blocks: 8192 places of 4096 features added to dw 51.7 us, so 50.3.)
+    if (blockIdx.x == 0) grid_dependency_wait();
+    return;
+  }
   // the last chunk that it reaches: the keys are sorted, so those that begin with it come first
   int64_t last = chunk;
   for (int more = blockDim.x; more == static_cast<int>(blockDim.x); last += more) {

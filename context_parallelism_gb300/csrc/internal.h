@@ -346,6 +346,7 @@ struct NormArgs {
   const void* w[2];         // [D] weights of q's and k's heads, bf16 or (wide) float32; NULL: ones
   int wide;
   float offset, eps;        // the weights are offset + w
+  float eps_up, eps_down;   // eps 2^192 and eps 2^-192 (heads scaled by 2^96 and 2^-96)
   const __nv_bfloat16* x[2];
   int64_t x_b[2], x_s[2], x_h[2];
   int64_t tokens;           // backward

@@ -205,20 +205,38 @@ __device__ __forceinline__ float head_sum(float s, int lanes) {
   return s;
 }
 
-// (ss / D + eps)^(-1/2) of a head whose squares sum to ss; heads whose squares leave fp32's range
-// (elements of 2^59 and more) are summed again, scaled down by 2^96. All lanes of a warp call.
-__device__ __forceinline__ float inverse_rms(const NormArgs& a, float ss, const F8& x, const F8& y) {
-  float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-  const bool out = !(ss <= 0x1p127f);
-  if (__any_sync(0xffffffffu, out)) {
+// (ss / D + eps)^(-1/2) of a head whose squares sum to ss. Heads whose squares leave the range in which
+// fp32 keeps its digits are scaled by a power of two and summed again: down beside a mean above 2^117, up
+// (kTiny) below 2^-96. The factor of the latter may be beyond fp32 itself: x and y become kLow times what
+// they were and the result, that of these, is negative like kLow, which marks it. An eps of 2^-96 or more
+// leaves no such head; the backward has kernels without them, as this path costs it registers (32768
+// tokens 194 us with it, 175 without; half of each head interleaved, 8194 tokens: 98 and 84). All lanes
+// of a warp call.
+constexpr float kLow = -0x1p96f, kLeast = 0x1p-96f;
+template <bool kTiny>
+__device__ __forceinline__ float inverse_rms(const NormArgs& a, float ss, F8& x, F8& y) {
+  const float t = fmaf(ss, a.inv_d, a.eps);
+  float r = rsqrtf(t);
+  const bool high = !(t <= 0x1p117f), low = kTiny && t < kLeast;
+  if (__any_sync(0xffffffffu, high || low)) {
+    const uint64_t c = both(kTiny && low ? kLow : 0x1p-96f);  // (not used for the others' heads)
     F8 u, v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      u.p[i] = fmul2(x.p[i], both(0x1p-96f));
-      v.p[i] = fmul2(y.p[i], both(0x1p-96f));
+      u.p[i] = fmul2(x.p[i], c);
+      v.p[i] = fmul2(y.p[i], c);
     }
     const float s = head_sum(dot_pairs(u, u, v, v), a.lanes);
-    if (out) r = 0x1p-96f * rsqrtf(s * a.inv_d);
+    if (high) r = 0x1p-96f * rsqrtf(fmaf(s, a.inv_d, a.eps_down));
+    if (kTiny) {
+      const uint64_t k = both(low ? kLow : 1.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x.p[i] = fmul2(x.p[i], k);
+        y.p[i] = fmul2(y.p[i], k);
+      }
+      if (low) r = -rsqrtf(fmaf(s, a.inv_d, a.eps_up));
+    }
   }
   return r;
 }
@@ -304,7 +322,7 @@ __global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_kernel(const NormArg
     F8 x, y;
     unpack_chunk<kInter>(va, vb, x, y);
     const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
-    const float r = inverse_rms(a, normed ? ss : 0.f, x, y);
+    const float r = inverse_rms<true>(a, normed ? ss : 1.f, x, y);
     if (here) {
       if (normed) {
 #pragma unroll
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_kernel(const NormArg
 
 // A set of `lanes` lanes keeps one head group and walks the tokens, so that its 16 sums of dw and its
 // weights stay in registers; a block adds its sets' sums in order and leaves 2 D partial sums.
-template <bool kInter, int kPer>
+template <bool kInter, int kPer, bool kTiny>
 __global__ void __launch_bounds__(kBwdThreads, 4) norm_rope_bwd_kernel(const NormArgs a) {
   static_assert(kPer % kBwdAhead == 0, "a head's slot is a constant");
   const RopeArgs& ra = a.r;
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4) norm_rope_bwd_kernel(const Nor
       if (then == kPer) next = enter((n + 1) * walkers + walker);
       start(then < kPer ? then < w.heads : then - kPer < next.heads, slot);
       const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
-      float r = inverse_rms(a, ss, x, y);
+      float r = inverse_rms<kTiny>(a, ss, x, y);
       if (!here) r = 0.f;  // without eps the zeros of no head would make dw NaN
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -442,6 +460,10 @@ __global__ void __launch_bounds__(kBwdThreads, 4) norm_rope_bwd_kernel(const Nor
         for (int i = 0; i < 4; ++i) {
           u.p[i] = fmul2(both(r), ffma2(x.p[i], both(tx), u.p[i]));
           v.p[i] = fmul2(both(r), ffma2(y.p[i], both(tx), v.p[i]));
+          if (kTiny && r < 0.f) {
+            u.p[i] = fmul2(u.p[i], both(kLow));
+            v.p[i] = fmul2(v.p[i], both(kLow));
+          }
         }
         pack_chunk<kInter>(u, v, ga, gb);
         __nv_bfloat16* dx = w.dx + j * step * ra.dst_h[t];
@@ -531,6 +553,14 @@ int bwd_heads(int64_t tokens, int heads, int D) {
   return tokens * heads * ((D + 15) / 16) < 152 * 1024 ? kBwdShort : kBwdLong;
 }
 
+template <bool kTiny>
+auto* bwd_kernel(int per, bool interleaved) {
+  return per == kBwdLong ? interleaved ? norm_rope_bwd_kernel<true, kBwdLong, kTiny>
+                                       : norm_rope_bwd_kernel<false, kBwdLong, kTiny>
+                         : interleaved ? norm_rope_bwd_kernel<true, kBwdShort, kTiny>
+                                       : norm_rope_bwd_kernel<false, kBwdShort, kTiny>;
+}
+
 template <bool kInter, bool kAppend>
 void launch_fwd(const NormArgs& a, unsigned grid, cudaStream_t stream) {
   if (a.per == kFwdLong)
@@ -589,9 +619,7 @@ cudaError_t launch_norm_rope_bwd(NormArgs a, bool interleaved, float* dq_w, floa
                                  cudaStream_t stream) {
   plan_groups(&a, bwd_heads(a.tokens, a.r.heads[0] + a.r.heads[1], a.r.D));
   const int blocks = norm_bwd_blocks(a.tokens, a.r.D, a.r.heads[0], a.r.heads[1]);
-  auto* kernel = a.per == kBwdLong
-                     ? interleaved ? norm_rope_bwd_kernel<true, kBwdLong> : norm_rope_bwd_kernel<false, kBwdLong>
-                     : interleaved ? norm_rope_bwd_kernel<true, kBwdShort> : norm_rope_bwd_kernel<false, kBwdShort>;
+  auto* kernel = a.eps < kLeast ? bwd_kernel<true>(a.per, interleaved) : bwd_kernel<false>(a.per, interleaved);
   launch_begin(16, stream);
   kernel<<<blocks, kBwdThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();

@@ -228,6 +228,8 @@ int check_norm(const upipe_norm* n, bool has_q, bool has_k, int D, NormArgs* a, 
   a->wide = n->wide;
   a->offset = static_cast<float>(n->offset);
   a->eps = static_cast<float>(n->eps);
+  a->eps_up = static_cast<float>(std::fmin(n->eps * 0x1p192, 0x1p96));  // (used below 2^-96)
+  a->eps_down = static_cast<float>(n->eps * 0x1p-192);
   int st = UPIPE_OK;
   if (a->w[0]) st = p->add(a->w[0], "q_weight", 16);
   if (st == UPIPE_OK && a->w[1]) st = p->add(a->w[1], "k_weight", 16);

@@ -412,7 +412,8 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
 
 /* Weights of the two norms: device [D], bf16 or (wide = 1) float32, 16-byte aligned, shared by
  * the heads of their tensor. NULL: all ones (offset is not added). offset: 0, or 1 for weights that
- * are kept as their distance from one. eps >= 0. */
+ * are kept as their distance from one. eps >= 0, of any size: heads whose squares fp32 does not hold are
+ * scaled before they are summed. Without eps a head of zeros gives NaN. */
 typedef struct {
   const void* q_weight;
   const void* k_weight;

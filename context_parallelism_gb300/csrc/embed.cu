@@ -517,6 +517,9 @@ EmbedPlan plan_embed(int64_t S, int Dm, int64_t V) {
   p.chunk = static_cast<int>((all + round * rounds - 1) / (round * rounds));
   if (p.chunk < 8) p.chunk = 8;
   p.chunks = (S + p.chunk - 1) / p.chunk;
+  p.zero_rows = 32;
+  while (p.zero_rows > 1 && int64_t(p.zero_rows) * Dm * 4 > kZeroBytes) p.zero_rows /= 2;
+  p.blocks = p.chunks * p.slices + (V + p.zero_rows - 1) / p.zero_rows;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -590,11 +593,9 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
                places[in ^ 1], shift, p.bits, scanned);
     }
   }
-  a.zero_rows = 32;
-  while (a.zero_rows > 1 && a.zero_rows * a.Dm * 4 > kZeroBytes) a.zero_rows /= 2;
-  const int64_t zero = a.present ? (a.V + a.zero_rows - 1) / a.zero_rows : 0;
+  a.zero_rows = p.zero_rows;
   const uint32_t *k = keys[in], *pl = places[in];
-  launch(embed_sum_kernel, p.chunks * p.slices + zero, p.threads, 0, true, a, k, pl);
+  launch(embed_sum_kernel, a.present ? p.blocks : p.chunks * p.slices, p.threads, 0, true, a, k, pl);
   if (p.chunks > 1) launch(embed_join_kernel, p.chunks * p.slices, p.threads * kJoin, 0, true, a, k);
   return e;
 }

@@ -442,6 +442,8 @@ struct EmbedPlan {
   int threads, slices;      // of the sums: threads a block, blocks a chunk
   int chunk;                // places a chunk
   int64_t chunks;
+  int zero_rows;            // rows of dw that a block writes zeros to, at most (a power of 2, at most 32)
+  int64_t blocks;           // of the sums with all rows' zeros
   size_t keys[2], places[2], hist, present, part, total;
 };
 EmbedPlan plan_embed(int64_t S, int Dm, int64_t V);
@@ -460,7 +462,7 @@ struct EmbedArgs {
   float* part;              // [chunks][2][Dm]
   int64_t chunks;
   int chunk, slices;
-  int zero_rows;            // rows of dw that a block writes zeros to, at most (a power of 2, at most 32)
+  int zero_rows;
 };
 cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaStream_t stream);
 

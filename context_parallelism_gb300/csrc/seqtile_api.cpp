@@ -845,11 +845,19 @@ int check_embed(int64_t S, int Dm, int64_t V, double scale) {
   if (!std::isfinite(scale)) return lfail(UPIPE_ERR_INVALID_ARG, "scale must be finite");
   if (Dm % 8 || Dm > (1 << 24) || S > (int64_t(1) << 30) || V >= (int64_t(1) << 31))
     return lfail(UPIPE_ERR_UNSUPPORTED, "need Dm %% 8 == 0, Dm <= 2^24, S <= 2^30, V < 2^31");
-  // blocks of one launch: the places' chunks and the rows that are zeroed
-  const EmbedPlan p = plan_embed(S < 1 ? 1 : S, Dm, V);
-  if (p.chunks * p.slices + V / 16 + 1 > 0x7fffffff ||
-      (S + 7) / 8 * ((Dm + 1023) / 1024) > 0x7fffffff)
+  // blocks of one launch: the forward's (as the places' chunks of the backward)
+  if ((S + 7) / 8 * ((Dm + 1023) / 1024) > 0x7fffffff)
     return lfail(UPIPE_ERR_UNSUPPORTED, "S=%lld Dm=%d: too many blocks", (long long)S, Dm);
+  return UPIPE_OK;
+}
+
+// The same of the gradient, whose blocks are the places' chunks and the rows that are zeroed.
+int check_embed_bwd(int64_t S, int Dm, int64_t V, double scale) {
+  const int st = check_embed(S, Dm, V, scale);
+  if (st != UPIPE_OK) return st;
+  if (plan_embed(S < 1 ? 1 : S, Dm, V).blocks > 0x7fffffff)
+    return lfail(UPIPE_ERR_UNSUPPORTED, "S=%lld Dm=%d V=%lld: too many blocks", (long long)S, Dm,
+                 (long long)V);
   return UPIPE_OK;
 }
 
@@ -880,7 +888,7 @@ int upipe_embed_fwd(const int64_t* token, const void* w, void* h, int64_t S, int
 }
 
 size_t upipe_embed_workspace_bytes(int64_t S, int Dm, int64_t V) {
-  if (check_embed(S, Dm, V, 1.0) != UPIPE_OK || S == 0) return 0;
+  if (check_embed_bwd(S, Dm, V, 1.0) != UPIPE_OK || S == 0) return 0;
   return plan_embed(S, Dm, V).total;
 }
 
@@ -889,7 +897,7 @@ int upipe_embed_bwd(const int64_t* token, const void* dh, float* dw, int64_t S, 
                     void* stream_) {
   const NvtxRange range("upipe_embed_bwd");
   set_last_error("");
-  int st = check_embed(S, Dm, V, scale);
+  int st = check_embed_bwd(S, Dm, V, scale);
   if (st != UPIPE_OK) return st;
   if (add != 0 && add != 1) return lfail(UPIPE_ERR_INVALID_ARG, "add must be 0 or 1");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);

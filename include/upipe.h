@@ -333,8 +333,8 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
  * table gives a row of NaN and has none either. w [V][Dm], h, dh [S][Dm] bf16, dw [V][Dm] float32,
  * dense. One rounding of h; dw is summed in fp32, in an order that the tokens alone decide: results
  * repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
- * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31. S = 0 reads nothing (add = 0: dw becomes
- * zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
+ * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31, and launches of fewer than 2^31 blocks
+ * (8 x 1024 elements of h, 16 KB of dw). S = 0 reads nothing (add = 0: dw becomes zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
  * may run at the same time need workspaces of their own.
  */
 int upipe_embed_fwd(const int64_t* token, const void* w, void* h, int64_t S, int Dm, int64_t V,

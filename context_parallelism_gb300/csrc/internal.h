@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstddef>
+#include <cfloat>
 #include <cstdint>
 
 #include <cstdio>
@@ -86,6 +87,9 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
+
+// Whether a factor that kernels take as a float is finite there (false for NaN).
+inline bool finite32(double v) { return v >= -FLT_MAX && v <= FLT_MAX; }
 
 // Restores the caller's current device when the scope ends (the entry points select the
 // device their tensors live on, and must not leave it changed).

@@ -147,7 +147,7 @@ int check_rope_sizes(const upipe_heads* q, const upipe_heads* k, const upipe_hea
   if (st != UPIPE_OK) return st;
   if (interleaved != 0 && interleaved != 1)
     return pfail(UPIPE_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  if (!std::isfinite(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite");
+  if (!finite32(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite in 32 bits");
   const bool has_q = present(q), has_k = present(k);
   if (!has_q && !has_k) return pfail(UPIPE_ERR_INVALID_ARG, "neither q nor k");
   if ((has_q && !present(q_out)) || (has_k && !present(k_out)))
@@ -220,8 +220,8 @@ int rope(const char* where, const upipe_heads* q, const upipe_heads* k, const up
 int check_norm(const upipe_norm* n, bool has_q, bool has_k, int D, NormArgs* a, Placed* p) {
   if (!n) return pfail(UPIPE_ERR_INVALID_ARG, "norm is NULL");
   if (D > 512) return pfail(UPIPE_ERR_UNSUPPORTED, "D=%d (a norm takes up to 512)", D);
-  if (!(n->eps >= 0.0) || !std::isfinite(n->eps) || !std::isfinite(n->offset))
-    return pfail(UPIPE_ERR_INVALID_ARG, "norm: eps must be finite and not negative, offset finite");
+  if (!(n->eps >= 0.0) || !finite32(n->eps) || !finite32(n->offset))
+    return pfail(UPIPE_ERR_INVALID_ARG, "norm: eps and offset must be finite in 32 bits, eps not negative");
   if (n->wide != 0 && n->wide != 1) return pfail(UPIPE_ERR_INVALID_ARG, "norm: wide must be 0 or 1");
   a->w[0] = has_q ? n->q_weight : nullptr;
   a->w[1] = has_k ? n->k_weight : nullptr;
@@ -336,7 +336,7 @@ int append(const char* where, bool with_norm, const upipe_norm* norm, const upip
   if (phase) {
     st = check_rot(D, rot_dim);
     if (st != UPIPE_OK) return st;
-    if (!std::isfinite(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite");
+    if (!finite32(mscale)) return pfail(UPIPE_ERR_INVALID_ARG, "mscale must be finite in 32 bits");
   } else if ((st = check_features(D)) != UPIPE_OK) {
     return st;
   }

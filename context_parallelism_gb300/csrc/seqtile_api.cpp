@@ -21,7 +21,6 @@
 // while tile i computes, and each tile's outputs are copied out on an outbound copy stream
 // while the next tile computes (the block-input offload the talk lists before sequence
 // tiling: activations live on the host and are brought in when needed).
-#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -842,7 +841,7 @@ namespace {
 int check_embed(int64_t S, int Dm, int64_t V, double scale) {
   if (S < 0 || Dm < 1 || V < 1)
     return lfail(UPIPE_ERR_INVALID_ARG, "S=%lld Dm=%d V=%lld", (long long)S, Dm, (long long)V);
-  if (!std::isfinite(scale)) return lfail(UPIPE_ERR_INVALID_ARG, "scale must be finite");
+  if (!finite32(scale)) return lfail(UPIPE_ERR_INVALID_ARG, "scale must be finite in 32 bits");
   if (Dm % 8 || Dm > (1 << 24) || S > (int64_t(1) << 30) || V >= (int64_t(1) << 31))
     return lfail(UPIPE_ERR_UNSUPPORTED, "need Dm %% 8 == 0, Dm <= 2^24, S <= 2^30, V < 2^31");
   // blocks of one launch: the forward's (as the places' chunks of the backward)

@@ -331,7 +331,7 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
  *   where no token is v; add = 1: added to what is there, rows without a token are not touched).
  * token [S] int64; a negative one (padding) gives a row of zeros and has no gradient; one beyond the
  * table gives a row of NaN and has none either. w [V][Dm], h, dh [S][Dm] bf16, dw [V][Dm] float32,
- * dense. One rounding of h; dw is summed in fp32, in an order that the tokens alone decide: results
+ * dense. scale is taken in 32 bits. One rounding of h; dw is summed in fp32, in an order that the tokens alone decide: results
  * repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
  * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31, and launches of fewer than 2^31 blocks
  * (8 x 1024 elements of h, 16 KB of dw). S = 0 reads nothing (add = 0: dw becomes zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
@@ -413,7 +413,7 @@ int upipe_rope_bwd(const upipe_heads* dq_out, const upipe_heads* dk_out, const u
 /* Weights of the two norms: device [D], bf16 or (wide = 1) float32, 16-byte aligned, shared by
  * the heads of their tensor. NULL: all ones (offset is not added). offset: 0, or 1 for weights that
  * are kept as their distance from one. eps >= 0, of any size: heads whose squares fp32 does not hold are
- * scaled before they are summed. Without eps a head of zeros gives NaN. */
+ * scaled before they are summed. Without eps a head of zeros gives NaN. Both are finite in 32 bits. */
 typedef struct {
   const void* q_weight;
   const void* k_weight;

@@ -757,8 +757,8 @@ def embed_backward(tokens, dh, V, scale=1.0, dw=None, workspace=None, stream=Non
     if workspace is None:
         workspace = _empty(stream, dh, (upipe_embed_workspace_bytes(S, Dm, V),), torch.uint8)
     st = _lib.upipe_embed_bwd(tokens.data_ptr(), dh.data_ptr(), dw.data_ptr(), S, Dm, V, scale,
-                              1 if add else 0, workspace.data_ptr(), workspace.numel(),
-                              _stream(stream, dh))
+                              1 if add else 0, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream, dh))
     if st:
         raise UpipeError(st, "upipe_embed_bwd")
     return dw

@@ -1051,8 +1051,8 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_len, q=None, q_out=None, p
     in its sequence. phases None: nothing is rotated. q_out: where q goes (q itself: in place).
     eps: each head of q and k is normed before, with q_weight, k_weight and offset, as by
     norm_rope_forward."""
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("a norm's weights without its eps")
+    if eps is None and (q_weight is not None or k_weight is not None or offset):
+        raise ValueError("a norm's weights or offset without its eps")
     B, S, dims, lens, cu = _batch(k, cu_seqlens, seq_len)
     shape = k.shape
     lead, D = shape[:-2], k_pages.shape[-1]

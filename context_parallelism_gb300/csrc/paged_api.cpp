@@ -166,7 +166,8 @@ int check_rope_tensors(const upipe_heads* q, const upipe_heads* k, const upipe_h
   bool in_place = true;
   const upipe_heads* in[2] = {q, k};
   const upipe_heads* out[2] = {q_out, k_out};
-  const char* names[4] = {"q", "k", "q_out", "k_out"};
+  static const char* const kNames[2][4] = {{"q", "k", "q_out", "k_out"}, {"dq_out", "dk_out", "dq", "dk"}};
+  const char* const* names = kNames[back];
   int st = UPIPE_OK;
   for (int i = 0; i < 2; ++i) {
     if (!present(in[i])) continue;
@@ -179,7 +180,7 @@ int check_rope_tensors(const upipe_heads* q, const upipe_heads* k, const upipe_h
     in_place = in_place && same_place(in[i], out[i]);
   }
   if (has_q && has_k && q_out->data == k_out->data)
-    return pfail(UPIPE_ERR_INVALID_ARG, "q_out and k_out are one tensor");
+    return pfail(UPIPE_ERR_INVALID_ARG, "%s and %s are one tensor", names[2], names[3]);
   if (with_rot) st = p->add(phase, "phase", 16);
   if (st == UPIPE_OK && pos) st = p->add(pos, "pos", 8);
   a->B = B;

@@ -209,9 +209,9 @@ __device__ __forceinline__ float head_sum(float s, int lanes) {
 // fp32 keeps its digits are scaled by a power of two and summed again: down beside a mean above 2^117, up
 // (kTiny) below 2^-96. The factor of the latter may be beyond fp32 itself: x and y become kLow times what
 // they were and the result, that of these, is negative like kLow, which marks it. An eps of 2^-96 or more
-// leaves no such head; the backward has kernels without them, as this path costs it registers (32768
-// tokens 194 us with it, 175 without; half of each head interleaved, 8194 tokens: 98 and 84). All lanes
-// of a warp call.
+// leaves no such head, so there are kernels without them: the path costs the backward registers (32768
+// tokens 194 us with it, 175 without; half of each head interleaved, 8194 tokens: 98 and 84) and the
+// forward 1 % (8194 tokens 57.7 and 57.1). All lanes of a warp call.
 constexpr float kLow = -0x1p96f, kLeast = 0x1p-96f;
 template <bool kTiny>
 __device__ __forceinline__ float inverse_rms(const NormArgs& a, float ss, F8& x, F8& y) {
@@ -253,7 +253,7 @@ __device__ __forceinline__ void unrolled(F& f) {
 // Thread -> (token, head group, lane of a head), lane fastest; groups number q's, k's, v's heads. A
 // group's kPer heads share the angles and the weights, folded into one map of the chunk; all their
 // loads are started before anything else.
-template <bool kInter, bool kAppend, int kPer>
+template <bool kInter, bool kAppend, int kPer, bool kTiny>
 __global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_kernel(const NormArgs a) {
   __shared__ uint4 stage[2 * kPer][kFwdThreads];
   const RopeArgs& ra = a.r;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_kernel(const NormArg
     F8 x, y;
     unpack_chunk<kInter>(va, vb, x, y);
     const float ss = head_sum(dot_pairs(x, x, y, y), a.lanes);
-    const float r = inverse_rms<true>(a, normed ? ss : 1.f, x, y);
+    const float r = inverse_rms<kTiny>(a, normed ? ss : 1.f, x, y);
     if (here) {
       if (normed) {
 #pragma unroll
@@ -553,20 +553,20 @@ int bwd_heads(int64_t tokens, int heads, int D) {
   return tokens * heads * ((D + 15) / 16) < 152 * 1024 ? kBwdShort : kBwdLong;
 }
 
+template <bool kTiny, bool kAppend>
+auto* fwd_kernel(int per, bool interleaved) {
+  return per == kFwdLong ? interleaved ? norm_rope_kernel<true, kAppend, kFwdLong, kTiny>
+                                       : norm_rope_kernel<false, kAppend, kFwdLong, kTiny>
+                         : interleaved ? norm_rope_kernel<true, kAppend, kFwdShort, kTiny>
+                                       : norm_rope_kernel<false, kAppend, kFwdShort, kTiny>;
+}
+
 template <bool kTiny>
 auto* bwd_kernel(int per, bool interleaved) {
   return per == kBwdLong ? interleaved ? norm_rope_bwd_kernel<true, kBwdLong, kTiny>
                                        : norm_rope_bwd_kernel<false, kBwdLong, kTiny>
                          : interleaved ? norm_rope_bwd_kernel<true, kBwdShort, kTiny>
                                        : norm_rope_bwd_kernel<false, kBwdShort, kTiny>;
-}
-
-template <bool kInter, bool kAppend>
-void launch_fwd(const NormArgs& a, unsigned grid, cudaStream_t stream) {
-  if (a.per == kFwdLong)
-    norm_rope_kernel<kInter, kAppend, kFwdLong><<<grid, kFwdThreads, 0, stream>>>(a);
-  else
-    norm_rope_kernel<kInter, kAppend, kFwdShort><<<grid, kFwdThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -578,6 +578,10 @@ cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t 
   // eight), eight beyond (1024 tokens: 6.4, 7.4 with two)
   plan_groups(&a, tokens * H * ((a.r.D + 15) / 16) < 152 * 1536 ? kFwdShort : kFwdLong);
   const int64_t per_tok = static_cast<int64_t>(a.lanes) * a.r.n_groups;
+  const bool tiny = a.eps < kLeast;
+  auto* kernel = append ? tiny ? fwd_kernel<true, true>(a.per, interleaved) : fwd_kernel<false, true>(a.per, interleaved)
+                 : tiny ? fwd_kernel<true, false>(a.per, interleaved)
+                        : fwd_kernel<false, false>(a.per, interleaved);
   // thread indices fit 32 bits; a longer call goes in several launches
   const int64_t most = ((int64_t(1) << 31) - 1) / per_tok;
   for (int64_t t0 = 0; t0 < tokens; t0 += most) {
@@ -586,13 +590,7 @@ cudaError_t launch_norm_rope(NormArgs a, bool interleaved, bool append, int64_t 
     a.r.units = static_cast<uint32_t>(n * per_tok);
     const unsigned grid = static_cast<unsigned>((n * per_tok + kFwdThreads - 1) / kFwdThreads);
     launch_begin(16, stream);
-    if (append) {
-      if (interleaved) launch_fwd<true, true>(a, grid, stream);
-      else launch_fwd<false, true>(a, grid, stream);
-    } else {
-      if (interleaved) launch_fwd<true, false>(a, grid, stream);
-      else launch_fwd<false, false>(a, grid, stream);
-    }
+    kernel<<<grid, kFwdThreads, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     launch_end(16, stream);
     if (e != cudaSuccess) return e;

@@ -28,6 +28,68 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kHeads = 4;  // heads of one token per thread
 
+// Two vectors x, y of one head that hold eight pairs: (x_i, y_i) in the half layout,
+// consecutive elements of x and then of y in the interleaved one.
+template <bool kInter>
+__device__ __forceinline__ void rotate_pairs(float (&x)[8], float (&y)[8], const float (&c)[8],
+                                             const float (&s)[8]) {
+  float u[8], v[8];
+  if (kInter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
+      u[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
+      v[2 * i] = y[2 * i] * c[4 + i] - y[2 * i + 1] * s[4 + i];
+      v[2 * i + 1] = y[2 * i + 1] * c[4 + i] + y[2 * i] * s[4 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = x[i] * c[i] - y[i] * s[i];
+      v[i] = y[i] * c[i] + x[i] * s[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = u[i];
+    y[i] = v[i];
+  }
+}
+
+// Factors of chunk c's eight pairs at position pos (see above on the angles).
+__device__ __forceinline__ void chunk_angles(const uint64_t* phase, int c, int64_t pos,
+                                             float mscale, float sin_scale, float (&cs)[8],
+                                             float (&sn)[8]) {
+  const ulonglong2* ph = reinterpret_cast<const ulonglong2*>(phase) + 4 * c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const ulonglong2 p = ph[q];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint64_t t = static_cast<uint64_t>(pos) * (e ? p.y : p.x);
+      const float half_turns = __ll2float_rn(static_cast<int64_t>(t)) * 0x1p-63f;
+      float s_, c_;
+      sincospif(half_turns, &s_, &c_);
+      cs[2 * q + e] = c_ * mscale;
+      sn[2 * q + e] = s_ * sin_scale;
+    }
+  }
+}
+
+// The two vectors of a head that chunk c holds: a turning chunk's pairs, or (behind the rotated
+// part) sixteen features in a row.
+__device__ __forceinline__ bool chunk_features(int c, int rot, bool inter, int* o0, int* o1) {
+  const int nr = rot >> 4;
+  if (c < nr) {
+    *o0 = inter ? 16 * c : 8 * c;
+    *o1 = inter ? 16 * c + 8 : rot / 2 + 8 * c;
+    return true;
+  }
+  *o0 = rot + 16 * (c - nr);
+  *o1 = *o0 + 8;
+  return false;
+}
+
 template <bool kInter>
 __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float (&c)[8],
                                        const float (&s)[8]) {

@@ -1,5 +1,5 @@
-// Device code that the rotary kernels share: the bf16 vectors, the rotation of eight pairs, the
-// angles of a position, and where a token of a batch lies and goes.
+// Device code that several kernels share: bf16 vectors as floats (the rotary, norm, embedding and log
+// probability kernels), and where a token of a batch lies and goes (the first two).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,54 +21,6 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
   return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
                     pack_bf16(f[6], f[7]));
-}
-
-// Two vectors x, y of one head that hold eight pairs: (x_i, y_i) in the half layout,
-// consecutive elements of x and then of y in the interleaved one.
-template <bool kInter>
-__device__ __forceinline__ void rotate_pairs(float (&x)[8], float (&y)[8], const float (&c)[8],
-                                             const float (&s)[8]) {
-  float u[8], v[8];
-  if (kInter) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-      u[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-      v[2 * i] = y[2 * i] * c[4 + i] - y[2 * i + 1] * s[4 + i];
-      v[2 * i + 1] = y[2 * i + 1] * c[4 + i] + y[2 * i] * s[4 + i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[i] = x[i] * c[i] - y[i] * s[i];
-      v[i] = y[i] * c[i] + x[i] * s[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = u[i];
-    y[i] = v[i];
-  }
-}
-
-// Factors of chunk c's eight pairs at position pos (see rope.cu on the angles).
-__device__ __forceinline__ void chunk_angles(const uint64_t* phase, int c, int64_t pos,
-                                             float mscale, float sin_scale, float (&cs)[8],
-                                             float (&sn)[8]) {
-  const ulonglong2* ph = reinterpret_cast<const ulonglong2*>(phase) + 4 * c;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const ulonglong2 p = ph[q];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint64_t t = static_cast<uint64_t>(pos) * (e ? p.y : p.x);
-      const float half_turns = __ll2float_rn(static_cast<int64_t>(t)) * 0x1p-63f;
-      float s_, c_;
-      sincospif(half_turns, &s_, &c_);
-      cs[2 * q + e] = c_ * mscale;
-      sn[2 * q + e] = s_ * sin_scale;
-    }
-  }
 }
 
 // Batch row and place of a token (packed rows of an append: row 0, the token itself), its position
@@ -125,20 +77,6 @@ __device__ __forceinline__ bool place_token(const RopeArgs& a, int64_t tok, bool
   p->b = b;
   p->i = i;
   return true;
-}
-
-// The two vectors of a head that chunk c holds: a turning chunk's pairs, or (behind the rotated
-// part) sixteen features in a row.
-__device__ __forceinline__ bool chunk_features(int c, int rot, bool inter, int* o0, int* o1) {
-  const int nr = rot >> 4;
-  if (c < nr) {
-    *o0 = inter ? 16 * c : 8 * c;
-    *o1 = inter ? 16 * c + 8 : rot / 2 + 8 * c;
-    return true;
-  }
-  *o0 = rot + 16 * (c - nr);
-  *o1 = *o0 + 8;
-  return false;
 }
 
 }  // namespace upipe

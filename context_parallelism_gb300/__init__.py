@@ -684,7 +684,10 @@ def token_logprobs(h, w, target=None, top=0, seq_tile=4096, workspace=None, stre
     None: logp is None), the entropy, the log of the sum of the exponentials, and the `top` most
     likely tokens with theirs (None, None for top = 0), seq_tile tokens at a time. h may be a pinned
     host tensor (staged tile by tile). The gradient of sum g * logp: ce_loss_backward with
-    dloss = -g and this lse. With top the workspace holds a tile's logits (seq_tile * V * 4 bytes)."""
+    dloss = -g and this lse. top_index goes by the exact logits; top_logp is what logp gives these tokens,
+    so that nearly equal neighbours may be a rounding out of order. With top the workspace has room for a
+    tile's logits, 512 bytes for each token and group of up to 128 columns: seq_tile * V * 4 bytes where the
+    groups are full, more where they are not."""
     torch = _torch or _lazy_torch()
     f32, i64 = torch.float32, torch.int64
     if len(_matrix(h, "h", torch.bfloat16)) != 2 or len(_matrix(w, "w", torch.bfloat16)) != 2 or \

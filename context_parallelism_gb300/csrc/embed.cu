@@ -361,7 +361,7 @@ __device__ __forceinline__ float* part_at(const EmbedArgs& a, int64_t chunk, int
 
 // Blocks [0, chunks * slices): one slice of features of one chunk of the sorted places. The others:
 // rows of dw whose token does not occur, zero_rows each.
-// (131072 places of 4096 features: 499 us with a row a block, 517 with 16; 16384 of 256: 52, 65 with 4 rows)
+// (131072 places of 4096 features: 499 to 506 us with a row a block, 517 with 16; 16384 of 256: 52, 65 with 4 rows)
 constexpr int kZeroBytes = 16384;
 constexpr int kMaxChunk = 128;
 constexpr int kAhead = 8;  // rows of dh in flight a thread
@@ -510,9 +510,12 @@ EmbedPlan plan_embed(int64_t S, int Dm, int64_t V) {
   const int vecs = Dm / 8;
   p.threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
   p.slices = (vecs + p.threads - 1) / p.threads;
-  // chunks: as long as an equal share of whole rounds of the blocks that are resident (8 on each of 152
-  // SMs), so that the last round is full and partial sums (two a chunk) stay few: 32768 places of 4096
-  // features 208 us, 218 with powers of two and at least twice as many chunks
+  // chunks: as long as an equal share of whole rounds of 1216 blocks, those of 128 threads that are resident
+  // (8 on each of 152 SMs), so that the last round is full and partial sums (two a chunk) stay few: 32768
+  // places of 4096 features 208 us, 218 with powers of two and at least twice as many chunks. More of the
+  // narrower blocks of fewer features are resident, yet rounds of as many, with shorter chunks, are worse
+  // for most sizes (256 features, 32 threads a block, rounds of 1216 and of 4864: 32768 places 46.6 and
+  // 65.2 us, 16384 45.7 and 50.5, 131072 88.5 and 84.4).
   const int64_t all = S * p.slices, round = 1216, rounds = (all + round * kMaxChunk - 1) / (round * kMaxChunk);
   p.chunk = static_cast<int>((all + round * rounds - 1) / (round * rounds));
   if (p.chunk < 8) p.chunk = 8;

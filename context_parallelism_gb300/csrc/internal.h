@@ -474,7 +474,7 @@ cudaError_t launch_embed_bwd(EmbedArgs a, const EmbedPlan& p, uint8_t* ws, cudaS
 // Rows [0, M) of one tile of a call. The logits' columns come in tiles of `tile`, a group each, or two if
 // it is above kLogpWidth: that many columns, and the others.
 constexpr int kLogpShortRows = 16;    // rows of a tile that the kernel for short calls takes at most
-constexpr int kLogpBlocks = 152;      // at most, one an SM
+constexpr int kLogpBlocks = 152;      // the SMs that tiles are cut for, and most blocks of the kernel for short calls
 constexpr int kLogpMargin = 4;        // candidates kept behind the last alternative
 constexpr int kLogpMaxTop = 24;
 
@@ -482,7 +482,7 @@ struct LogpArgs {
   const __nv_bfloat16 *h, *w;  // [M][Dm], [V][Dm]
   const int64_t* target;       // [M], or NULL
   float* tlogit;               // [M] logit at the target
-  float4* part;                // [M][groups]: see logp.cu (the last word: logp_mark)
+  float4* part;                // [M][groups]: see logp.cu (the last word: mark)
   float* logits;               // [M][groups][kLogpWidth], or NULL (no alternatives)
   float *logp, *entropy, *lse; // [M]; each may be NULL
   float* top_logp;             // [M][top]

@@ -370,8 +370,8 @@ __device__ __forceinline__ void long_tile(int64_t t, int m_tiles, int n_tiles, i
 // Sums, target and wanted logits of group g of one row: x, up to 128 columns from col0 to end.
 // Logits are wanted for the row's `keep` largest alone. Slot g % keep of `best` holds the largest
 // logit of every keep-th group so far, so the smallest of the slots is a bound below which no logit
-// can be among them: a slice of 32 columns below it is not stored (of 4096 x 128256 logits 6 % are, with
-// nine to keep; with all of them stored the call took 0.5 ms more). The bound only grows; an older
+// can be among them: a slice of 32 columns below it is not stored (of 4096 x 128256 logits 2 % are, with
+// nine to keep, 6 % with 28; with all of them stored the call took 0.5 ms more). The bound only grows; an older
 // one stores more, never less.
 __device__ __forceinline__ void finish_row(const LogpArgs& a, int64_t row, int g, int col0, int end,
                                            uint32_t bound, float (&x)[128]) {
@@ -776,7 +776,7 @@ __device__ __forceinline__ float3 dot_near(const __nv_bfloat16* h, const __nv_bf
 }
 
 // The same part of <h, w> with an error near 2^-45 of the terms: each lane keeps its sums and the sums of
-// what each addition lost.
+// what each addition lost (Knuth's error-free transformation of a sum).
 __device__ __forceinline__ double dot_exact(const __nv_bfloat16* h, const __nv_bfloat16* w, int Dm,
                                             int which) {
   float s[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};

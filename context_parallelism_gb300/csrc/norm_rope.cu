@@ -17,10 +17,10 @@
 //
 // Bound: HBM, once enough bytes are in flight: the loads go to the thread's own places in shared
 // memory as asynchronous copies, which hold no registers (131072 tokens of 32 + 8 heads of 128: 568 us
-// with loads to registers, 385 so, 105 % of a copy's rate), and the angles are shared by eight heads.
+// with loads to registers, 385 so, 104 % of a copy's rate), and the angles are shared by eight heads.
 // Copies past L1 want whole sectors to a request: with the 32 bytes of four interleaved pairs in one
-// lane, two requests of half sectors, the backward of 8194 tokens took 123 us, now 85. The backward
-// of 32768 tokens takes 170 us, 89 % of a copy's rate; its 330 instructions a lane and head are next.
+// lane, two requests of half sectors, the backward of 8194 tokens took 123 us, now 83. The backward
+// of 32768 tokens takes 173 us, 87 % of a copy's rate; its 325 instructions a lane and head are next.
 #include "internal.h"
 #include "rope.cuh"
 

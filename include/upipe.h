@@ -268,8 +268,11 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * The gradient of sum g_i logp_i is upipe_ce_bwd's for dloss = -g and this lse.
  * Which of two logits is the larger is decided on sums of the exact products with an error near
  * 2^-45 of their magnitudes, whatever the tile; top + 4 candidates are looked at so, those with the
- * largest tensor-core sums. The values are the tensor cores' fp32 sums of 64 or 512 products each, added up
- * rounded to nearest. A row with a logit of NaN or +inf, or
+ * largest tensor-core sums: where more columns than that lie within the tensor cores' error of the last
+ * place, the last ones may be others of these. The values are the tensor cores' fp32 sums of 64 or 512
+ * products each, added up rounded to nearest, for a target and for an alternative alike: top_logp of a token
+ * is, bit for bit, the logp that the call gives it as a target, and neighbours of nearly equal logits may
+ * have values a rounding out of order (sort them where they must descend). A row with a logit of NaN or +inf, or
  * without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
  * and -1.
  * Layouts (dense): h [S][Dm], w [V][Dm] bf16; target, top_index [S], [S][top] int64; logp, entropy,
@@ -331,8 +334,8 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
  *   where no token is v; add = 1: added to what is there, rows without a token are not touched).
  * token [S] int64; a negative one (padding) gives a row of zeros and has no gradient; one beyond the
  * table gives a row of NaN and has none either. w [V][Dm], h, dh [S][Dm] bf16, dw [V][Dm] float32,
- * dense. scale is taken in 32 bits. One rounding of h; dw is summed in fp32, in an order that the tokens alone decide: results
- * repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
+ * dense. scale is taken in 32 bits. One rounding of h; dw is summed in fp32, in an order that the tokens and the
+ * sizes S, Dm and V decide: results repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
  * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31, and launches of fewer than 2^31 blocks
  * (8 x 1024 elements of h, 16 KB of dw). S = 0 reads nothing (add = 0: dw becomes zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
  * may run at the same time need workspaces of their own.
@@ -553,7 +556,7 @@ enum {
   UPIPE_K_ATTN_PREFIX = 15, /* the shared prefix on 128-row tensor-core tiles */
   UPIPE_K_NORM_ROPE = 16, /* head norms with the rotation, into the paged cache too */
   UPIPE_K_EMBED = 17,     /* token embedding, its gradient and the sort of the tokens */
-  UPIPE_K_LOGP = 18,      /* token log probabilities: short calls' logits, selection */
+  UPIPE_K_LOGP = 18,      /* token log probabilities: logits of short and long calls, selection */
   UPIPE_K_COUNT = 19
 };
 

@@ -361,7 +361,8 @@ __device__ __forceinline__ float* part_at(const EmbedArgs& a, int64_t chunk, int
 
 // Blocks [0, chunks * slices): one slice of features of one chunk of the sorted places. The others:
 // rows of dw whose token does not occur, zero_rows each.
-// (131072 places of 4096 features: 499 to 506 us with a row a block, 517 with 16; 16384 of 256: 52, 65 with 4 rows)
+// (131072 places of 4096 features: 499 to 506 us with a row a block, 517 with 16; 16384 of 256: 52, 65 with
+// 4 rows)
 constexpr int kZeroBytes = 16384;
 constexpr int kMaxChunk = 128;
 constexpr int kAhead = 8;  // rows of dh in flight a thread

@@ -272,8 +272,8 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * place, the last ones may be others of these. The values are the tensor cores' fp32 sums of 64 or 512
  * products each, added up rounded to nearest, for a target and for an alternative alike: top_logp of a token
  * is, bit for bit, the logp that the call gives it as a target, and neighbours of nearly equal logits may
- * have values a rounding out of order (sort them where they must descend). A row with a logit of NaN or +inf, or
- * without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
+ * have values a rounding out of order (sort them where they must descend).
+ * A row with a logit of NaN or +inf, or without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
  * and -1.
  * Layouts (dense): h [S][Dm], w [V][Dm] bf16; target, top_index [S], [S][top] int64; logp, entropy,
  * lse [S], top_logp [S][top] float32. target and logp may both be NULL, entropy and lse each;
@@ -334,10 +334,12 @@ int upipe_mlp_bwd(const void* x, const void* w_gu, const void* w_d, const void* 
  *   where no token is v; add = 1: added to what is there, rows without a token are not touched).
  * token [S] int64; a negative one (padding) gives a row of zeros and has no gradient; one beyond the
  * table gives a row of NaN and has none either. w [V][Dm], h, dh [S][Dm] bf16, dw [V][Dm] float32,
- * dense. scale is taken in 32 bits. One rounding of h; dw is summed in fp32, in an order that the tokens and the
- * sizes S, Dm and V decide: results repeat bitwise. Every pointer: device memory of one device, 16-byte aligned (token 8, workspace 256).
- * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31, and launches of fewer than 2^31 blocks
- * (8 x 1024 elements of h, 16 KB of dw). S = 0 reads nothing (add = 0: dw becomes zeros). Neither call allocates anything or uses the status word: both may be captured. Calls that
+ * dense. scale is taken in 32 bits. One rounding of h; dw is summed in fp32, in an order that the tokens
+ * and the sizes S, Dm and V decide: results repeat bitwise. Every pointer: device memory of one device,
+ * 16-byte aligned (token 8, workspace 256).
+ * Supported: Dm a multiple of 8 up to 2^24, S up to 2^30, V below 2^31, and launches of fewer than 2^31
+ * blocks (8 x 1024 elements of h, 16 KB of dw). S = 0 reads nothing (add = 0: dw becomes zeros). Neither
+ * call allocates anything or uses the status word: both may be captured. Calls that
  * may run at the same time need workspaces of their own.
  */
 int upipe_embed_fwd(const int64_t* token, const void* w, void* h, int64_t S, int Dm, int64_t V,

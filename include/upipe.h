@@ -273,8 +273,8 @@ int upipe_ce_fwd_bwd(const void* h, const void* w, const int64_t* target, const 
  * products each, added up rounded to nearest, for a target and for an alternative alike: top_logp of a token
  * is, bit for bit, the logp that the call gives it as a target, and neighbours of nearly equal logits may
  * have values a rounding out of order (sort them where they must descend).
- * A row with a logit of NaN or +inf, or without a finite one, gives NaN and indices of -1; a row of fewer than `top` columns ends in -inf
- * and -1.
+ * A row with a logit of NaN or +inf, or without a finite one, gives NaN and indices of -1; a row of fewer
+ * than `top` columns ends in -inf and -1.
  * Layouts (dense): h [S][Dm], w [V][Dm] bf16; target, top_index [S], [S][top] int64; logp, entropy,
  * lse [S], top_logp [S][top] float32. target and logp may both be NULL, entropy and lse each;
  * top_logp and top_index are NULL when top = 0. h and w 16-byte, workspace 256-byte aligned, the
